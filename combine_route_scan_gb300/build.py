@@ -58,7 +58,7 @@ def sources():
 
 def _inputs_mtime() -> float:
     files = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    files.append(os.path.join(os.path.dirname(HERE), "include", "moe.h"))
+    files += glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h"))
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 

@@ -65,6 +65,23 @@ cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* p
   return cudaSuccess;
 }
 
+int num_sms_of_current_device() {
+  static std::atomic<int> cache[64] = {};  // callers may be on several host threads
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) {
+    const int c = cache[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace crs
 
 using namespace crs;
@@ -177,23 +194,6 @@ WsLayout make_layout(const moe_config_t* c, const Shape& sh) {
   }
   L.total = off;
   return L;
-}
-
-int num_sms_of_current_device() {
-  static std::atomic<int> cache[64] = {};  // callers may be on several host threads
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) {
-    const int c = cache[dev].load(std::memory_order_relaxed);
-    if (c > 0) return c;
-  }
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

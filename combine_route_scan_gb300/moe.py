@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in include/moe.h (libcrs_moe.so).
+"""Python binding of the C ABI in include/moe.h and include/moe_experts.h
+(libcrs_moe.so).
 
 Argument marshalling only: every function takes torch tensors (device memory
 owned by the caller), passes their data pointers and the current CUDA stream
@@ -39,7 +40,16 @@ BULK_MIN_BYTES = 2 * 1024 * 1024
 # Every symbol include/moe.h declares.
 EXPORTS = ("moe_get_workspace_size", "moe_workspace_init", "moe_dispatch", "moe_combine",
            "moe_dispatch_ffn_combine", "moe_combine_noalloc", "moe_get_device_status", "moe_status_string")
+# ... and include/moe_experts.h.
+EXPERTS_EXPORTS = ("moe_route", "moe_route_backward", "moe_mx_scale_bytes", "moe_mx_quantize", "moe_expert_product")
 NOALLOC_MAX_PICKS = 262144
+
+MOE_F32, MOE_MXFP4 = 3, 4
+FLOAT_CODE = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2_SUM = 0, 1
+SF_ROWS, SF_TILED = 0, 1
+EPI_NONE, EPI_SWIGLU = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -79,6 +89,25 @@ def config(ep_world_size: int, bs: int, h: int, topk: int, moe_expert_num: int, 
                      ffn_intermediate, yd, None, None, 0, scales_kind, None)
 
 
+class RouterConfig(ctypes.Structure):
+    """moe_router_config_t."""
+    _fields_ = [
+        ("tokens", ctypes.c_int32), ("expert_num", ctypes.c_int32), ("topk", ctypes.c_int32),
+        ("group_num", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("group_score", ctypes.c_int32),
+        ("score_func", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+        ("scaling", ctypes.c_float), ("logits_stride", ctypes.c_int64),
+    ]
+
+
+def router_config(tokens: int, expert_num: int, topk: int, logits_dtype, group_num: int = 1, topk_group: int = 1,
+                  group_score: int = GROUP_MAX, score_func: int = SCORE_SOFTMAX, renormalize: bool = True,
+                  scaling: float = 1.0, logits_stride: Optional[int] = None) -> RouterConfig:
+    """moe_router_config_t; logits_stride defaults to expert_num (rows one after the other)."""
+    dt = FLOAT_CODE[logits_dtype] if isinstance(logits_dtype, torch.dtype) else int(logits_dtype)
+    return RouterConfig(tokens, expert_num, topk, group_num, topk_group, group_score, score_func, int(renormalize), dt,
+                        scaling, expert_num if logits_stride is None else logits_stride)
+
+
 _lib = None
 
 
@@ -101,8 +130,16 @@ def lib() -> ctypes.CDLL:
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_launch_count.argtypes = []
         L.moe_launch_count.restype = ctypes.c_uint64
+        R, I32, I64 = ctypes.POINTER(RouterConfig), ctypes.c_int32, ctypes.c_int64
+        L.moe_route.argtypes = [R, P, P, P, P, P]
+        L.moe_route_backward.argtypes = [R, P, P, P, P, I64, P]
+        L.moe_mx_scale_bytes.argtypes = [I32, I64, I32, I32]
+        L.moe_mx_scale_bytes.restype = ctypes.c_uint64
+        L.moe_mx_quantize.argtypes = [P, I32, I32, I64, I32, I64, I64, I32, P, P, P]
+        L.moe_expert_product.argtypes = [C, P, P, P, P, P, I32, I32, I32, I32, P, P, P, ctypes.c_size_t, P]
         for f in ("moe_get_workspace_size", "moe_workspace_init", "moe_dispatch", "moe_combine",
-                  "moe_dispatch_ffn_combine", "moe_combine_noalloc", "moe_get_device_status"):
+                  "moe_dispatch_ffn_combine", "moe_combine_noalloc", "moe_get_device_status", "moe_route",
+                  "moe_route_backward", "moe_mx_quantize", "moe_expert_product"):
             getattr(L, f).restype = ctypes.c_int32
         _lib = L
     return _lib
@@ -220,6 +257,98 @@ def combine_noalloc(cfg: MoeConfig, expert_out, assist_info, ep_recv_count, expe
                                      _ptr(x_out), _ptr(status), _stream(stream)), "moe_combine_noalloc")
 
 
+def _rows_ptr(t: torch.Tensor, rows: int, cols: int, stride: int, what: str):
+    """Address of a tensor of `rows` contiguous rows of `cols` elements, `stride` apart."""
+    if t.is_contiguous():
+        ok = rows < 2 or stride == cols
+    else:
+        ok = t.dim() == 2 and t.stride(1) == 1 and (t.stride(0) == stride or rows < 2)
+    if not ok or t.dim() < 1 or t.shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError(f"{what}: expected {rows} contiguous rows of {cols} elements, {stride} apart")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _typed_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, n: int, what: str):
+    if t is not None and (t.dtype != dtype or t.numel() != n):
+        raise ValueError(f"{what}: expected {n} elements of {dtype}")
+    return _ptr(t)
+
+
+def route(rc: RouterConfig, logits, bias, expert_ids, expert_scales, stream=None):
+    """moe_route: logits [tokens, E] of the configuration's type, bias None or
+    fp32 [E] -> expert_ids int32 and expert_scales fp32 [tokens, K], as dispatch
+    and combine take them (with any leading axes, such as [W, bs, K])."""
+    T, E, K = rc.tokens, rc.expert_num, rc.topk
+    if FLOAT_CODE.get(logits.dtype) != rc.logits_dtype:
+        raise ValueError("logits: not of the configuration's type")
+    _check(lib().moe_route(ctypes.byref(rc), _rows_ptr(logits, T, E, rc.logits_stride, "logits"),
+                           _typed_ptr(bias, torch.float32, E, "bias"),
+                           _typed_ptr(expert_ids, torch.int32, T * K, "expert_ids"),
+                           _typed_ptr(expert_scales, torch.float32, T * K, "expert_scales"), _stream(stream)),
+           "moe_route")
+
+
+def route_backward(rc: RouterConfig, logits, expert_ids, grad_scales, grad_logits, stream=None):
+    """moe_route_backward: the gradient of route's weights, written to
+    grad_logits (of the logits' shape and type; its rows may be strided)."""
+    T, E, K = rc.tokens, rc.expert_num, rc.topk
+    if FLOAT_CODE.get(logits.dtype) != rc.logits_dtype or grad_logits.dtype != logits.dtype:
+        raise ValueError("logits, grad_logits: not of the configuration's type")
+    gs = grad_logits.stride(-2) if grad_logits.dim() == 2 and grad_logits.shape[0] > 1 else E
+    _check(lib().moe_route_backward(ctypes.byref(rc), _rows_ptr(logits, T, E, rc.logits_stride, "logits"),
+                                    _typed_ptr(expert_ids, torch.int32, T * K, "expert_ids"),
+                                    _typed_ptr(grad_scales, torch.float32, T * K, "grad_scales"),
+                                    _rows_ptr(grad_logits, T, E, gs, "grad_logits"), gs, _stream(stream)),
+           "moe_route_backward")
+
+
+def mx_scale_bytes(experts: int, rows: int, cols: int, layout: int = SF_ROWS) -> int:
+    return int(lib().moe_mx_scale_bytes(experts, rows, cols, layout))
+
+
+def mx_quantize(x, codes, scales, layout: int = SF_ROWS, stream=None):
+    """moe_mx_quantize: x [rows, cols] or [experts, rows, cols] (contiguous
+    rows, any strides between them) -> codes uint8 [..., cols / 2] and scales
+    uint8 (alloc_mx sizes both)."""
+    if x.dim() not in (2, 3) or x.dtype not in FLOAT_CODE or not x.is_cuda:
+        raise ValueError("x: expected a 2D or 3D CUDA tensor of float32, float16 or bfloat16")
+    E, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
+    if cols > 1 and x.stride(-1) != 1:
+        raise ValueError("x: expected contiguous rows")
+    rs = x.stride(-2) if rows > 1 else cols
+    _check(lib().moe_mx_quantize(x.data_ptr(), FLOAT_CODE[x.dtype], E, rows, cols, rs, x.stride(0) if x.dim() == 3 else 0,
+                                 layout, _typed_ptr(codes, torch.uint8, E * rows * (cols // 2), "codes"),
+                                 _typed_ptr(scales, torch.uint8, mx_scale_bytes(E, rows, cols, layout), "scales"),
+                                 _stream(stream)), "moe_mx_quantize")
+
+
+def expert_product(cfg: MoeConfig, x, x_scales, ep_recv_count, w, w_scales, y, y_scales=None,
+                   epilogue: int = EPI_NONE, ws=None, stream=None):
+    """moe_expert_product: dispatched MX FP4 rows x [W, A, k/2] with x_scales [W, A, k/32]
+    times w [E, n, k/2] with tiled w_scales -> y [W, A, c] float16 / bfloat16, or
+    uint8 codes [W, A, c/2] with y_scales [W, A, ceil(c/32)]; c = n, or n/2
+    with EPI_SWIGLU. ws is the dispatch's workspace."""
+    W, E = cfg.ep_world_size, cfg.moe_expert_num
+    rows = W * cfg.bs * W * min(E // W, cfg.topk)  # W * A
+    n, k = w.shape[-2], 2 * w.shape[-1]
+    c = n // 2 if epilogue == EPI_SWIGLU else n
+    u8 = torch.uint8
+    if y.dtype == u8:
+        yp, ydt = _typed_ptr(y, u8, rows * (c // 2), "y"), MOE_MXFP4
+    else:
+        yp, ydt = _typed_ptr(y, y.dtype, rows * c, "y"), DTYPE_CODE.get(y.dtype, -1)
+    _check(lib().moe_expert_product(ctypes.byref(cfg), _typed_ptr(x, u8, rows * (k // 2), "x"),
+                                    _typed_ptr(x_scales, u8, rows * (k // 32), "x_scales"),
+                                    _typed_ptr(ep_recv_count, torch.int32, E * W, "ep_recv_count"),
+                                    _typed_ptr(w, u8, E * n * (k // 2), "w"),
+                                    _typed_ptr(w_scales, u8, E * (-(-n // 128)) * (-(-k // 128)) * 512, "w_scales"),
+                                    n, k, epilogue, ydt, yp,
+                                    _typed_ptr(y_scales, u8, rows * (-(-c // 32)), "y_scales"), _ptr(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream)), "moe_expert_product")
+
+
 def get_device_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream; returns and clears the first device-side error."""
     v = ctypes.c_int32(0)
@@ -278,3 +407,13 @@ def alloc_dispatch_outputs(cfg: MoeConfig, x_dtype: torch.dtype, device="cuda", 
         "expand_scales": torch.empty((W, A), dtype=sdt, device=device) if expand_scales else None,
         "seg_plane": torch.empty((W, L * W), dtype=torch.uint8, device=device) if seg_plane else None,
     }
+
+
+def alloc_mx(x: torch.Tensor, layout: int = SF_ROWS) -> tuple:
+    """(codes, scales) that mx_quantize fills for x; scales [..., rows, ceil(cols/32)]
+    (SF_ROWS) or [experts, row tiles, block tiles, 512] (SF_TILED)."""
+    *lead, rows, cols = x.shape
+    blocks = -(-cols // 32)
+    codes = torch.empty((*x.shape[:-1], cols // 2), dtype=torch.uint8, device=x.device)
+    shape = (*lead, rows, blocks) if layout == SF_ROWS else (*(lead or [1]), -(-rows // 128), -(-blocks // 4), 512)
+    return codes, torch.empty(shape, dtype=torch.uint8, device=x.device)
