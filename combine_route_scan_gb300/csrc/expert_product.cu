@@ -4,22 +4,24 @@
 //
 // On the tensor cores' block-scaled path (tcgen05.mma kind::mxf4: E2M1 codes, one
 // E8M0 scale for 32 elements of K, fp32 accumulators in TMEM):
-//   * a unit is 128 rows of one expert (the MMA's A operand) against up to 256
+//   * a unit is 128 rows of one expert (the MMA's A operand) against up to 192
 //     of its weight rows (B). The rows are A although an expert may have only a
 //     few: streaming weights from HBM takes 23 bytes a clock and SM, the MMA eats
 //     64 of them a clock, so the unused rows cost nothing that is short, and
 //     each epilogue thread has one row with neighbouring features in registers;
-//   * codes come by TMA in 128-byte-swizzled boxes, 256 elements of K a stage;
-//     only as many 32-row boxes of A as the unit has rows;
+//   * codes come by TMA in 128-byte-swizzled boxes, 256 elements of K a stage; a
+//     unit of few rows takes a box of 32 rows of A, the rest 128;
 //   * the weights' scales, laid out in the tensor cores' order (MOE_SF_TILED), come
-//     by one bulk copy for 128 rows and 256 elements; the rows' scales lie a row
-//     after the other as dispatch wrote them: a warp brings them into the same
-//     order with 4-byte cp.async. tcgen05.cp then takes both to TMEM, in the
-//     MMA's own issue order;
-//   * warps: 0 TMA, 1 MMA, 2 row scales, 4..11 epilogue (two for each quarter of
-//     the accumulator's lanes). An epilogue thread takes its whole share of the
-//     accumulator into registers (128 of them) and hands it back at once, so one
-//     accumulator is enough: the next unit's MMAs run while this one is stored;
+//     by one more box, 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the
+//     copy engine busy for longer than the codes did); the rows' scales lie a row
+//     after the other as dispatch wrote them: a lane brings 16 bytes of its rows
+//     (r, r + 32, ..) at a time by cp.async and stores them in that order; the same
+//     warp's tcgen05.cp takes both to TMEM and tells the MMA warp, which is left
+//     with four MMAs and one commit a stage (what it has to issue bounds a stage);
+//   * warps: 0 TMA, 1 MMA, 2 and 3 scales, 4..11 epilogue (two for each quarter of
+//     the accumulator's lanes). Two accumulators of 192 columns and the scales fill
+//     TMEM, so that the next unit's MMAs run while this one is read (256 columns
+//     would leave room for one: the hand-over then stood still for each unit);
 //   * one persistent CTA an SM; units are dealt out round-robin over all experts
 //     (their running tile counts are scanned in shared memory), n-tiles of one
 //     row tile adjacent, so that rows and weights are read from L2 but once from HBM.
@@ -39,34 +41,45 @@ namespace crs {
 struct ProductParams {
   const uint8_t* xs;       // [W*A][K/32]
   const int32_t* ep;       // [W][L*W]
-  const uint8_t* wsf;      // [E][nt128][kt128][512]
   void* y;                 // [W*A][C]
   uint8_t* ys;             // [W*A][ceil(C/32)], MX FP4 output
   int W, L, E, N, K, C;    // C output columns
+  int xs_align;            // bytes that a copy of row scales may take: 16, 8, 4 or 1
   long long A;
   int* status;
   uint64_t timeout_ns;
+};
+
+// Boxes of 32 and 128 rows of x, of 64, 128 and 192 rows of w, and of the scales of
+// 2 x 128 rows of w: one copy a stage each.
+struct ProductMaps {
+  CUtensorMap x32, x128, w64, w128, w192, wsf;
 };
 
 constexpr int kProductThreads = 384;
 constexpr int kProductStages = 4;
 constexpr int kEpilogueWarp = 4;             // first of the eight
 constexpr int kRowsTile = 128;               // MMA M
-constexpr int kMaxBoxes = 4;                 // of 64 weight rows: MMA N <= 256
+constexpr int kMaxBoxes = 3;                 // of 64 weight rows: MMA N <= 192
 constexpr int kKStage = 256;                 // elements of K a stage: 128 bytes a row
 constexpr uint32_t kABytes = kRowsTile * 128;
-constexpr uint32_t kBBox = 64 * 128;
-constexpr uint32_t kBBytes = kMaxBoxes * kBBox;
-constexpr uint32_t kSfaBytes = 2 * 512;      // 128 rows x 8 scales
+constexpr uint32_t kBBytes = kMaxBoxes * 64 * 128;
 constexpr uint32_t kSfbBytes = 2 * 1024;     // 2 x 128 rows x 8 scales
-constexpr uint32_t kProductStage = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+constexpr uint32_t kProductStage = kABytes + kBBytes + kSfbBytes;
 static_assert(kProductStage % 1024 == 0, "stages stay 1024-byte aligned");
 constexpr uint32_t kSfCols = 24;             // TMEM columns of a stage's scales: 2 x 4 of the rows, 2 x 8 of the weights
-constexpr uint32_t kAccCols = 256;
+constexpr uint32_t kAccCols = kMaxBoxes * 64;
+static_assert(2 * kAccCols + kProductStages * kSfCols <= 512, "TMEM holds two accumulators and the stages' scales");
+// Row scales go by pairs of stages (16 bytes a row): two warps take turns, each
+// with loads of kScaleSlots - 1 pairs under way, and two pairs in the tensor cores'
+// order from which tcgen05.cp takes them.
+constexpr int kScaleWarps = 2, kScaleSlots = 3, kScaleRing = 2;
+constexpr uint32_t kScalePair = 128 * 16;
 
-// Shared memory behind the stages: running row tiles [E+1], first row [E], row count [E].
+// Shared memory behind the stages: the ring of row scales, row scales under way,
+// running row tiles [E+1], first row [E], row count [E].
 __host__ __device__ inline size_t product_smem(int E) {
-  return 1024 + (size_t)kProductStages * kProductStage + ((size_t)3 * E + 1) * 4;
+  return 1024 + (size_t)kProductStages * kProductStage + kScaleWarps * (kScaleRing + kScaleSlots) * kScalePair + ((size_t)3 * E + 1) * 4;
 }
 
 struct ProductUnit {
@@ -74,22 +87,23 @@ struct ProductUnit {
   long long row0;
 };
 
+// Unit u, found by a whole warp: the expert whose tiles [pre[e], pre[e+1]) hold
+// row tile mt, first among every (E/32)th expert, then among those between.
 __device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, const int* pre, int u, int n_tiles, int width) {
-  const int mt = u / n_tiles;
-  int lo = 0, hi = p.E;  // the expert whose tiles [pre[e], pre[e+1]) hold mt
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= mt) lo = mid;
-    else hi = mid;
-  }
+  const int lane = threadIdx.x & 31;
+  const int mt = u / n_tiles, step = (p.E + 31) >> 5;
+  const int far = lane * step;
+  const int block = (31 - __clz(__ballot_sync(0xffffffffu, far < p.E && pre[far] <= mt))) * step;
+  const int near = block + lane;
+  const int e = block + 31 - __clz(__ballot_sync(0xffffffffu, lane < step && near < p.E && pre[near] <= mt));
   const int* first = pre + p.E + 1;
   const int* count = first + p.E;
-  const int at = (mt - pre[lo]) * kRowsTile;
+  const int at = (mt - pre[e]) * kRowsTile;
   ProductUnit x;
-  x.e = lo;
+  x.e = e;
   x.n0 = (u - mt * n_tiles) * width;
-  x.rows = min(kRowsTile, count[lo] - at);
-  x.row0 = (long long)(lo / p.L) * p.A + first[lo] + at;
+  x.rows = min(kRowsTile, count[e] - at);
+  x.row0 = (long long)(e / p.L) * p.A + first[e] + at;
   return x;
 }
 
@@ -99,9 +113,14 @@ struct ProductAbort {
   uint64_t limit;
 };
 
+// A wait of the pipeline, bounded by `limit` once it has lasted a while: reading
+// the global timer at every wait that has to wait at all cost more than the wait.
 __device__ __forceinline__ bool product_wait(uint64_t* bar, uint32_t parity, const ProductAbort& a) {
-  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int it = 0; it < 64; ++it)
+    if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 63u) {
@@ -115,28 +134,67 @@ __device__ __forceinline__ bool product_wait(uint64_t* bar, uint32_t parity, con
   }
 }
 
-// Scales of rows [row0, row0 + rows) for one stage, in the tensor cores' order:
-// the 4 bytes of row r and k-group j at j * 512 + (r % 32) * 16 + (r / 32) * 4.
-// Whole 4-byte groups (K % 128 == 0) go by cp.async; other row lengths leave
-// unaligned rows, whose bytes are gathered by plain loads.
-__device__ __forceinline__ void load_row_scales(const ProductParams& p, const ProductUnit& un, int kb, uint8_t* dst) {
-  const int lane = threadIdx.x & 31, blocks = p.K / 32, left = blocks - kb * 8;
-  const uint8_t* src = p.xs + (size_t)un.row0 * blocks + kb * 8;
-  if ((blocks & 3) == 0) {
-    const int groups = left >= 8 ? 2 : 1;
-    for (int r = lane; r < un.rows; r += 32)
-      for (int j = 0; j < groups; ++j)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + j * 512 + lane * 16 + (r >> 5) * 4)),
-                     "l"(src + (size_t)r * blocks + j * 4)
-                     : "memory");
+// The same for a whole warp: one lane asks, so that waiting warps leave the
+// shared-memory pipe to those at work.
+__device__ __forceinline__ bool product_wait_warp(uint64_t* bar, uint32_t parity, const ProductAbort& a) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = product_wait(bar, parity, a);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The 16 scale bytes of rows lane, lane + 32, .. of a unit for stages kb and
+// kb + 1 into this lane's part of a slot, by the widest asynchronous copies that
+// the row length (K / 32 bytes) and x_scales' address align; what lies beyond the
+// row's end is left as it is, or zero where a stage's last MMA reads it.
+__device__ __forceinline__ void load_row_scales(const ProductParams& p, const ProductUnit& un, int kb, uint32_t slot) {
+  const int lane = threadIdx.x & 31, blocks = p.K / 32, left = min(16, blocks - kb * 8);
+  const uint8_t* src = p.xs + (size_t)(un.row0 + lane) * blocks + kb * 8;
+  const size_t step = (size_t)32 * blocks;
+  const uint32_t dst = slot + lane * 16;
+  if (p.xs_align == 16) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < un.rows)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + c * 512), "l"(src + c * step) : "memory");
+  } else if (p.xs_align > 1) {
+    for (int c = 0; lane + 32 * c < un.rows; ++c)
+      for (int b = 0; b < left; b += p.xs_align) {
+        if (p.xs_align == 8)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + c * 512 + b), "l"(src + c * step + b) : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + c * 512 + b), "l"(src + c * step + b) : "memory");
+      }
   } else {
-    for (int r = lane; r < un.rows; r += 32)
-      for (int j = 0; j < 2; ++j) {
+    for (int c = 0; lane + 32 * c < un.rows; ++c)
+      for (int i = 0; i < 4; ++i) {
         uint32_t v = 0;
         for (int b = 0; b < 4; ++b)
-          if (j * 4 + b < left) v |= (uint32_t)__ldg(src + (size_t)r * blocks + j * 4 + b) << (8 * b);
-        *reinterpret_cast<uint32_t*>(dst + j * 512 + lane * 16 + (r >> 5) * 4) = v;
+          if (4 * i + b < left) v |= (uint32_t)__ldg(src + c * step + 4 * i + b) << (8 * b);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + c * 512 + 4 * i), "r"(v) : "memory");
       }
+  }
+}
+
+// One stage's scales to TMEM: 128 rows of x and CHUNKS x 128 weight rows, GROUPS of 128 elements of K.
+template <int CHUNKS, int GROUPS>
+__device__ __forceinline__ void product_scales(uint32_t ta, uint64_t adesc, uint64_t bdesc) {
+#pragma unroll
+  for (int j = 0; j < GROUPS; ++j) {
+    tc_cp_scales(ta + 4 * j, adesc + j * 32);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) tc_cp_scales(ta + 8 + 8 * j + 4 * c, bdesc + c * 64 + j * 32);
+  }
+}
+
+// One stage's STEPS MMAs of 64 elements of K; ta and tb are the scales' columns.
+template <int STEPS>
+__device__ __forceinline__ void product_mmas(uint32_t acc, uint64_t adesc, uint64_t bdesc, uint32_t ta, uint32_t tb,
+                                             uint32_t idesc, bool accumulate) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) {
+    constexpr uint32_t kPair = (2u << 4) | (2u << 29);  // the upper two of a column's four scales
+    tc_mma_mxf4(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc | (kk & 1 ? kPair : 0), ta + 4 * (kk >> 1),
+                tb + 8 * (kk >> 1), kk > 0 || accumulate);
   }
 }
 
@@ -202,25 +260,31 @@ __device__ __forceinline__ void store_results(const ProductParams& p, long long 
 
 template <int YT, bool SWIGLU>
 __global__ void __launch_bounds__(kProductThreads, 1)
-    expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                          ProductParams p) {
+    expert_product_kernel(const __grid_constant__ ProductMaps maps, ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
-  __shared__ __align__(8) uint64_t full[kProductStages], empty[kProductStages], acc_full, acc_empty, drained;
+  __shared__ __align__(8) uint64_t full[kProductStages], empty[kProductStages], acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(8) uint64_t scaled[kProductStages], taken[kScaleWarps][kScaleRing];
   __shared__ uint32_t tmem_slot;
   __shared__ long long scan_scratch[32];
   __shared__ volatile int s_abort;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
-  int* pre = reinterpret_cast<int*>(sm + (size_t)kProductStages * kProductStage);
+  uint8_t* ring = sm + (size_t)kProductStages * kProductStage;
+  uint8_t* slots = ring + kScaleWarps * kScaleRing * kScalePair;
+  int* pre = reinterpret_cast<int*>(slots + kScaleWarps * kScaleSlots * kScalePair);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kProductStages; ++i) {
-      mbar_init(&full[i], 2);  // the TMA thread's expect_tx and the row-scale warp
+      mbar_init(&full[i], 1);
+      mbar_init(&scaled[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&acc_full, 1);
-    mbar_init(&acc_empty, kProductThreads / 32 - kEpilogueWarp);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kProductThreads / 32 - kEpilogueWarp);
+    }
+    for (int i = 0; i < kScaleWarps * kScaleRing; ++i) mbar_init(&taken[0][i], 1);
     mbar_init(&drained, 1);
     mbar_fence_init();
     s_abort = 0;
@@ -268,10 +332,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const uint32_t tmem_sf = tmem + kAccCols;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  const uint32_t tmem_sf = tmem + 2 * kAccCols;
 
-  const int m_tiles = pre[p.E], KB = (p.K + kKStage - 1) / kKStage;
+  const int m_tiles = __shfl_sync(0xffffffffu, pre[p.E], 0), KB = (p.K + kKStage - 1) / kKStage;
   // weight rows a unit: the width whose rounds of units cost least, a unit's
   // cost being its weight rows and half a box for its rows and its ends
   int boxes = 1;
@@ -288,137 +352,225 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
   const int width = boxes * 64, n_tiles = (p.N + width - 1) / width;
   const int units = m_tiles * n_tiles;
+  const bool whole = p.K % kKStage == 0;
   const ProductAbort ab{&s_abort, p.status, p.timeout_ns};
 
+  // Every role walks the same units and stages. The copying and the multiplying warp
+  // run theirs with all lanes on values that the compiler can see are uniform, one
+  // elected lane issuing: their instructions bound a stage, and under a divergent
+  // branch every descriptor took the slow way into uniform registers.
   if (warp == 0) {
-    if (lane == 0) {
-      const int nt128 = (p.N + 127) / 128, kt128 = (p.K + 127) / 128;
-      uint32_t it = 0;
-      for (int u = blockIdx.x; u < units && !s_abort; u += gridDim.x) {
-        const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
-        const int a_boxes = (un.rows + 31) >> 5;
-        const int c0 = un.n0 >> 7, chunks = min(nt128, (un.n0 + width + 127) >> 7) - c0;
-        const uint8_t* sf = p.wsf + ((size_t)un.e * nt128 + c0) * kt128 * 512;
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const uint32_t stage = it % kProductStages, round = it / kProductStages;
-          if (round > 0 && !product_wait(&empty[stage], (round - 1) & 1u, ab)) break;
-          uint8_t* st = sm + stage * kProductStage;
-          const uint32_t sf_bytes = 512u * (uint32_t)min(2, kt128 - 2 * kb);
-          mbar_arrive_expect_tx(&full[stage], (uint32_t)a_boxes * 4096u + (uint32_t)boxes * kBBox + (uint32_t)chunks * sf_bytes);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_3d(st + kABytes + b * kBBox, &map_w, kb * 128, un.n0 + b * 64, un.e, &full[stage]);
-          for (int b = 0; b < a_boxes; ++b)
-            tma_load_2d(st + b * 4096, &map_x, kb * 128, (int)(un.row0 + b * 32), &full[stage]);
-          for (int c = 0; c < chunks; ++c)
-            bulk_g2s(st + kABytes + kBBytes + kSfaBytes + c * 1024, sf + ((size_t)c * kt128 + 2 * kb) * 512, sf_bytes,
-                     &full[stage]);
+    const int nt128 = (p.N + 127) / 128;
+    const CUtensorMap* mw = boxes == 3 ? &maps.w192 : boxes == 2 ? &maps.w128 : &maps.w64;
+    const uint32_t sm0 = smem_u32(sm), bar0 = smem_u32(full);
+    const bool leader = elect_one();
+    uint32_t stage = 0, phase = 1;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
+      const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
+                row = __shfl_sync(0xffffffffu, (int)un.row0, 0);
+      const bool few = rows <= 32;
+      const CUtensorMap* mx = few ? &maps.x32 : &maps.x128;
+      const uint32_t bytes = (uint32_t)width * 128u + (few ? 32u * 128u : kABytes) + kSfbBytes;
+      const int sf_row = e * nt128 + (un.n0 >> 7);
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = __all_sync(0xffffffffu, product_wait(&empty[stage], phase, ab));
+        if (!ok) break;
+        const uint32_t st = sm0 + stage * kProductStage, bar = bar0 + stage * 8;
+        if (leader) {
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          tma_load_3d(st + kABytes, mw, kb * 128, un.n0, e, bar);
+          tma_load_2d(st, mx, kb * 128, row, bar);
+          tma_load_2d(st + kABytes + kBBytes, &maps.wsf, kb * 256, sf_row, bar);
+        }
+        if (++stage == kProductStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_mxf4(width);
-      uint32_t it = 0, done = 0;
-      for (int u = blockIdx.x; u < units && !s_abort; u += gridDim.x, ++done) {
-        const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
-        const int c0 = un.n0 >> 7, chunks = ((un.n0 + width + 127) >> 7) - c0;
-        const uint32_t shift = (un.n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
-        if (done > 0 && !product_wait(&acc_empty, (done - 1) & 1u, ab)) break;
+    const uint64_t adesc0 = sw128_desc(sm), bdesc0 = sw128_desc(sm + kABytes);
+    const bool leader = elect_one();
+    const int n_step = (int)gridDim.x % n_tiles;
+    int n_index = (int)blockIdx.x % n_tiles;
+    uint32_t stage = 0, phase = 0, done = 0;
+    bool ok = true, ready = false;  // the next stage was seen to be there before this one's MMAs went out
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
+      const int n0 = n_index * width, cols = min(width, (p.N - n0 + 63) & ~63);
+      n_index += n_step;
+      if (n_index >= n_tiles) n_index -= n_tiles;
+      const uint32_t shift = (n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
+      const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * kAccCols;
+      ok = product_wait(&acc_empty[buf], ((done >> 1) & 1) ^ 1, ab);
+      for (int kb = 0; kb < KB && ok; ++kb) {
+        if (!ready) ok = product_wait(&full[stage], phase, ab) && product_wait(&scaled[stage], phase, ab);
+        if (!ok) break;
         tc_fence_after();
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const uint32_t stage = it % kProductStages, round = it / kProductStages;
-          if (!product_wait(&full[stage], round & 1u, ab)) break;
-          tc_fence_after();
-          const uint8_t* st = sm + stage * kProductStage;
-          const uint8_t* sfa = st + kABytes + kBBytes;
-          const uint32_t ta = tmem_sf + stage * kSfCols, tb = ta + 8;
-          const int steps = min(4, (p.K - kb * kKStage + 63) / 64);
-          for (int j = 0; j < (steps + 1) / 2; ++j) {
-            tc_cp_scales(ta + 4 * j, sf_desc(sfa + j * 512));
-            for (int c = 0; c < chunks; ++c) tc_cp_scales(tb + 8 * j + 4 * c, sf_desc(sfa + kSfaBytes + c * 1024 + j * 512));
-          }
-          const uint64_t adesc = sw128_desc(st), bdesc = sw128_desc(st + kABytes);
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint32_t id = (kk & 1) * 2;  // which two of a column's four scales
-            tc_mma_mxf4(tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc | (id << 4) | (id << 29), ta + 4 * (kk >> 1),
-                        tb + 8 * (kk >> 1) + shift, (kb | kk) != 0);
-          }
-          tc_commit(&empty[stage]);
+        const uint32_t step = stage * (kProductStage >> 4), here = stage;
+        const uint32_t ta = tmem_sf + stage * kSfCols, tb = ta + 8 + shift;
+        if (++stage == kProductStages) {
+          stage = 0;
+          phase ^= 1;
         }
-        tc_commit(&acc_full);
+        const bool there = mbar_test_wait(&full[stage], phase), taken_up = mbar_test_wait(&scaled[stage], phase);
+        if (leader) {
+          const int steps = whole || kb + 1 < KB ? 4 : (p.K - kb * kKStage + 63) / 64;
+          if (steps == 4) product_mmas<4>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
+          else if (steps == 3) product_mmas<3>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
+          else if (steps == 2) product_mmas<2>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
+          else product_mmas<1>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
+          tc_commit(&empty[here]);
+          if (kb + 1 == KB) tc_commit(&acc_full[buf]);
+        }
+        ready = there && taken_up;
       }
-      tc_commit(&drained);
     }
-  } else if (warp == 2) {
-    // row scales: cp.async of stage it, arrival for the stage two before
-    uint32_t it = 0;
-    const auto arrive = [&](uint32_t stage) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[stage]);
+    if (leader) tc_commit(&drained);
+  } else if (warp < 2 + kScaleWarps) {
+    // scales: this warp's pairs of stages are every kScaleWarps-th one
+    const int pairs = (KB + 1) / 2;
+    const uint32_t slot0 = smem_u32(slots) + (warp - 2) * kScaleSlots * kScalePair;
+    const uint8_t* my_ring = ring + (warp - 2) * kScaleRing * kScalePair;
+    const uint32_t ring0 = smem_u32(my_ring) + lane * 16;
+    const uint64_t asf0 = sf_desc(my_ring), bsf0 = sf_desc(sm + kABytes + kBBytes);
+    const bool leader = elect_one();
+    int load_u = blockIdx.x, load_pair = warp - 2;
+    uint32_t load_slot = 0;
+    bool fresh = true;
+    ProductUnit ahead{};
+    const auto load_next = [&] {
+      while (load_pair >= pairs) {
+        load_pair -= pairs;
+        load_u += gridDim.x;
+        fresh = true;
+      }
+      if (load_u < units) {
+        if (fresh) ahead = product_unit(p, pre, load_u, n_tiles, width);
+        fresh = false;
+        load_row_scales(p, ahead, load_pair * 2, slot0 + load_slot * kScalePair);
+        load_slot = load_slot + 1 == kScaleSlots ? 0 : load_slot + 1;
+        load_pair += kScaleWarps;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    for (int i = 0; i < kScaleSlots - 1; ++i) load_next();
+    uint32_t stage = 0, phase = 0, slot = 0, at = 0, at_phase = 1;
+    int turn = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const uint32_t stage = it % kProductStages, round = it / kProductStages;
-        if (round > 0) {
-          ok = product_wait(&empty[stage], (round - 1) & 1u, ab);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+      const int n0 = (u % n_tiles) * width;
+      const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
+      for (int kb = 0; kb < KB && ok; kb += 2) {
+        const int here = min(2, KB - kb);  // stages of this pair
+        if (turn != warp - 2) {
+          stage += here;
+          if (stage >= kProductStages) {
+            stage -= kProductStages;
+            phase ^= 1;
+          }
+          turn = turn + 1 == kScaleWarps ? 0 : turn + 1;
+          continue;
         }
-        load_row_scales(p, un, kb, sm + stage * kProductStage + kABytes + kBBytes);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (it >= 2) {
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          arrive((it - 2) % kProductStages);
+        turn = turn + 1 == kScaleWarps ? 0 : turn + 1;
+        load_next();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
+        // the lane's own rows: word i of row c is 128-element group i of the two stages
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
+                       : "r"(slot0 + slot * kScalePair + c * 512 + lane * 16));
+        slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+        ok = __all_sync(0xffffffffu, product_wait(&taken[warp - 2][at], at_phase, ab));
+        if (!ok) break;
+        // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
+        const uint32_t dst = ring0 + at * kScalePair;
+        const auto put = [&](int i, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * 512), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+        };
+        put(0, v[0].x, v[1].x, v[2].x, v[3].x);
+        put(1, v[0].y, v[1].y, v[2].y, v[3].y);
+        put(2, v[0].z, v[1].z, v[2].z, v[3].z);
+        put(3, v[0].w, v[1].w, v[2].w, v[3].w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (int h = 0; h < here; ++h) {
+          // the weights' scales are in the stage; its TMEM columns are free since the stage was
+          ok = __all_sync(0xffffffffu, product_wait(&full[stage], phase, ab));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t ta = tmem_sf + stage * kSfCols;
+            const uint64_t asf = asf0 + at * (kScalePair >> 4) + h * 64, bsf = bsf0 + stage * (kProductStage >> 4);
+            if (p.K - (kb + h) * kKStage <= 128) {  // a last stage of one group
+              if (two) product_scales<2, 1>(ta, asf, bsf);
+              else product_scales<1, 1>(ta, asf, bsf);
+            } else {
+              if (two) product_scales<2, 2>(ta, asf, bsf);
+              else product_scales<1, 2>(ta, asf, bsf);
+            }
+            tc_commit(&scaled[stage]);
+            if (h + 1 == here) tc_commit(&taken[warp - 2][at]);
+          }
+          __syncwarp();
+          if (++stage == kProductStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (++at == kScaleRing) {
+          at = 0;
+          at_phase ^= 1;
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok)
-      for (uint32_t i = it >= 2 ? it - 2 : 0; i < it; ++i) arrive(i % kProductStages);
   } else if (warp >= kEpilogueWarp) {
     const int q = warp & 3, half = (warp - kEpilogueWarp) >> 2;
     uint32_t done = 0;
     for (int u = blockIdx.x; u < units && !s_abort; u += gridDim.x, ++done) {
       const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
-      if (!product_wait(&acc_full, done & 1u, ab)) break;
+      const uint32_t buf = done & 1;
+      if (!product_wait_warp(&acc_full[buf], (done >> 1) & 1, ab)) break;
       tc_fence_after();
       const int r = 32 * q + lane;
-      const bool mine = 32 * q < un.rows && half < boxes;
-      uint32_t v[2][64];
-      if (mine) {
-        const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + half * 64;
-        tc_ld64(t, v[0]);
-        if (half + 2 < boxes) tc_ld64(t + 128, v[1]);
-        tc_wait_ld();
+      if (32 * q < un.rows) {
+        const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kAccCols;
+        // 64 columns at a time, the third part by the halves in turn
+#pragma unroll 1
+        for (int g = 0; g < boxes; ++g) {
+          const int n = un.n0 + g * 64;
+          if ((g == 2 ? (int)(done & 1) : g) != half || n >= p.N) continue;
+          uint32_t v[64];
+          tc_ld64(acc + g * 64, v);
+          tc_wait_ld();
+          if (r < un.rows) {
+            if (SWIGLU) {
+              float h[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
+                // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
+                // bits that follows
+                h[j] = __fdividef(a, 1.0f + __expf(-a)) * b;
+              }
+              store_results<YT>(p, un.row0 + r, n / 2, h);
+            } else {
+              float h[64];
+#pragma unroll
+              for (int j = 0; j < 64; ++j) h[j] = __uint_as_float(v[j]);
+              store_results<YT>(p, un.row0 + r, n, h);
+            }
+          }
+          __syncwarp();
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty);
-      if (mine && r < un.rows) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int n = un.n0 + (half + 2 * i) * 64;
-          if (half + 2 * i >= boxes || n >= p.N) break;
-          if (SWIGLU) {
-            float h[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float g = __uint_as_float(v[i][2 * j]), up = __uint_as_float(v[i][2 * j + 1]);
-              // __fdividef is within 2 ulps, far below the rounding to 16 or 4 bits that follows
-              h[j] = __fdividef(g, 1.0f + expf(-g)) * up;
-            }
-            store_results<YT>(p, un.row0 + r, n / 2, h);
-          } else {
-            float h[64];
-#pragma unroll
-            for (int j = 0; j < 64; ++j) h[j] = __uint_as_float(v[i][j]);
-            store_results<YT>(p, un.row0 + r, n, h);
-          }
-        }
-      }
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
     }
   }
 
@@ -468,7 +620,20 @@ static bool product_map(CUtensorMap* m, const void* base, unsigned long long byt
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-typedef void (*ProductKernel)(CUtensorMap, CUtensorMap, ProductParams);
+// Rows of scale tiles (512 bytes for every 128 elements of K), boxes of 1 KB x 2 rows.
+static bool scale_map(CUtensorMap* m, const void* base, unsigned long long bytes, unsigned long long rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = product_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {bytes / 4, rows};
+  cuuint64_t strides[1] = {bytes};
+  cuuint32_t box[2] = {256, 2};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+typedef void (*ProductKernel)(ProductMaps, ProductParams);
 template <int YT>
 ProductKernel product_kernel(bool swiglu) {
   return swiglu ? expert_product_kernel<YT, true> : expert_product_kernel<YT, false>;
@@ -506,14 +671,18 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   const int nsm = num_sms_of_current_device();
   if (nsm <= 0) return MOE_ERR_CUDA;
 
-  CUtensorMap mx, mw;
-  if (!product_map(&mx, x, (unsigned long long)k / 2, (unsigned long long)W * A, 0, 32) ||
-      !product_map(&mw, w, (unsigned long long)k / 2, (unsigned long long)n, (unsigned long long)E, 64))
+  ProductMaps maps;
+  const unsigned long long row_bytes = (unsigned long long)k / 2, rows = (unsigned long long)W * A;
+  const auto map_w = [&](CUtensorMap* m, unsigned box) {
+    return product_map(m, w, row_bytes, (unsigned long long)n, (unsigned long long)E, box);
+  };
+  if (!product_map(&maps.x32, x, row_bytes, rows, 0, 32) || !product_map(&maps.x128, x, row_bytes, rows, 0, 128) ||
+      !scale_map(&maps.wsf, w_scales, (unsigned long long)(k + 127) / 128 * 512, (unsigned long long)E * ((n + 127) / 128)) ||
+      !map_w(&maps.w64, 64) || !map_w(&maps.w128, 128) || !map_w(&maps.w192, 192))
     return MOE_ERR_CUDA;
   ProductParams p{};
   p.xs = x_scales;
   p.ep = ep_recv_count;
-  p.wsf = w_scales;
   p.y = y;
   p.ys = y_scales;
   p.W = W;
@@ -522,6 +691,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   p.N = n;
   p.K = k;
   p.C = C;
+  p.xs_align = k % 512 == 0 && aligned(x_scales, 16) ? 16 : k % 256 == 0 && aligned(x_scales, 8) ? 8 : k % 128 == 0 ? 4 : 1;
   p.A = A;
   p.status = &static_cast<WsHeader*>(ws)->status;
   p.timeout_ns = (uint64_t)cfg->wait_timeout_us * 1000ull;
@@ -536,7 +706,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   // a unit is at least 64 weight rows of an expert's tile: no more CTAs than that
   const long long most = ((long long)W * A / kRowsTile + E) * ((n + 63) / 64);
   PdlLaunch L(dim3((unsigned)(most < nsm ? most : nsm)), dim3(kProductThreads), smem, static_cast<cudaStream_t>(stream));
-  if (cudaLaunchKernelEx(&L.cfg, kernel, mx, mw, p) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaLaunchKernelEx(&L.cfg, kernel, maps, p) != cudaSuccess) return MOE_ERR_CUDA;
   note_launches(1);
   return MOE_OK;
 }
