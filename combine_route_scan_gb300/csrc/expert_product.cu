@@ -10,7 +10,8 @@
 //     64 of them a clock, so the unused rows cost nothing that is short, and
 //     each epilogue thread has one row with neighbouring features in registers;
 //   * codes come by TMA in 128-byte-swizzled boxes, 256 elements of K a stage; a
-//     unit of few rows takes a box of 32 rows of A, the rest 128;
+//     unit of few rows takes a box of 32 rows of A, the rest 128, and where every
+//     expert has few rows the stages are that much smaller and more;
 //   * the weights' scales, laid out in the tensor cores' order (MOE_SF_TILED), come
 //     by one more box, 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the
 //     copy engine busy for longer than the codes did); the rows' scales lie a row
@@ -57,29 +58,61 @@ struct ProductMaps {
 };
 
 constexpr int kProductThreads = 384;
-constexpr int kProductStages = 4;
+constexpr int kMaxStages = 8;
 constexpr int kEpilogueWarp = 4;             // first of the eight
 constexpr int kRowsTile = 128;               // MMA M
+constexpr int kFewRows = 32;
 constexpr int kMaxBoxes = 3;                 // of 64 weight rows: MMA N <= 192
 constexpr int kKStage = 256;                 // elements of K a stage: 128 bytes a row
-constexpr uint32_t kABytes = kRowsTile * 128;
-constexpr uint32_t kBBytes = kMaxBoxes * 64 * 128;
 constexpr uint32_t kSfbBytes = 2 * 1024;     // 2 x 128 rows x 8 scales
-constexpr uint32_t kProductStage = kABytes + kBBytes + kSfbBytes;
-static_assert(kProductStage % 1024 == 0, "stages stay 1024-byte aligned");
-constexpr uint32_t kSfCols = 24;             // TMEM columns of a stage's scales: 2 x 4 of the rows, 2 x 8 of the weights
-constexpr uint32_t kAccCols = kMaxBoxes * 64;
-static_assert(2 * kAccCols + kProductStages * kSfCols <= 512, "TMEM holds two accumulators and the stages' scales");
-// Row scales go by pairs of stages (16 bytes a row): two warps take turns, each
-// with loads of kScaleSlots - 1 pairs under way, and two pairs in the tensor cores'
-// order from which tcgen05.cp takes them.
-constexpr int kScaleWarps = 2, kScaleSlots = 3, kScaleRing = 2;
-constexpr uint32_t kScalePair = 128 * 16;
+// Row scales are read for pairs of stages (16 bytes a row). Two warps bring them to
+// the tensor cores, one the even and one the odd stages of the ring: the number of
+// stages is even, so that a stage's barriers have one and the same waiter, which
+// cannot be a round ahead. Each has kScaleSlots pairs under way or landed, and the
+// scales of one stage in the tensor cores' order, from which tcgen05.cp takes them.
+constexpr int kScaleWarps = 2, kScaleSlots = 3;
+constexpr uint32_t kScalePair = 128 * 16, kScaleStage = 128 * 8;
+constexpr size_t kProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
 
-// Shared memory behind the stages: the ring of row scales, row scales under way,
-// running row tiles [E+1], first row [E], row count [E].
-__host__ __device__ inline size_t product_smem(int E) {
-  return 1024 + (size_t)kProductStages * kProductStage + kScaleWarps * (kScaleRing + kScaleSlots) * kScalePair + ((size_t)3 * E + 1) * 4;
+// Shared memory behind the stages: row scales in order and under way, running
+// row tiles [E+1], first row [E], row count [E].
+__host__ __device__ inline uint32_t product_fixed_smem(int E) {
+  return (uint32_t)kScaleWarps * (kScaleStage + kScaleSlots * kScalePair) + ((3u * E + 1) * 4 + 15) / 16 * 16;
+}
+
+// How a launch cuts its work: weight rows a unit, rows of A kept for a stage, and
+// as many stages as shared memory holds (the way of a stage from its release
+// through the copies, tcgen05.cp and their barriers back to the MMA takes some
+// 2600 clocks, which the others have to cover).
+struct ProductShape {
+  int width, n_tiles, stages;
+  uint32_t a_bytes, stage_bytes, sf_cols;
+};
+
+__device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles, bool few) {
+  int boxes = 1;
+  long long best = 1ll << 62;
+  // the width whose rounds of units cost least: with few rows a unit streams its
+  // weights (its cost is their bytes), with many it also moves its rows
+  for (int b = kMaxBoxes; b >= 1; --b) {
+    const long long units = (long long)m_tiles * ((N + 64 * b - 1) / (64 * b));
+    const long long cost = (units + gridDim.x - 1) / gridDim.x * (few ? 4 * b + 1 : b + 2);
+    if (cost < best) {
+      best = cost;
+      boxes = b;
+    }
+  }
+  ProductShape s;
+  s.width = boxes * 64;
+  s.n_tiles = (N + s.width - 1) / s.width;
+  s.a_bytes = (few ? kFewRows : kRowsTile) * 128;
+  s.stage_bytes = s.a_bytes + s.width * 128 + kSfbBytes;
+  s.stages = min(kMaxStages, (int)(((uint32_t)kProductSmem - 1024 - product_fixed_smem(E)) / s.stage_bytes));
+  // TMEM: two accumulators, then 2 x 4 columns of the rows' scales and 2 x 4 for
+  // every 128 weight rows of a stage
+  s.sf_cols = 8 + (boxes == 3 ? 16 : 8);
+  s.stages = min(s.stages, (512 - 2 * s.width) / (int)s.sf_cols) & ~1;
+  return s;
 }
 
 struct ProductUnit {
@@ -150,7 +183,7 @@ __device__ __forceinline__ void load_row_scales(const ProductParams& p, const Pr
   const int lane = threadIdx.x & 31, blocks = p.K / 32, left = min(16, blocks - kb * 8);
   const uint8_t* src = p.xs + (size_t)(un.row0 + lane) * blocks + kb * 8;
   const size_t step = (size_t)32 * blocks;
-  const uint32_t dst = slot + lane * 16;
+  const uint32_t dst = slot;
   if (p.xs_align == 16) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -177,24 +210,25 @@ __device__ __forceinline__ void load_row_scales(const ProductParams& p, const Pr
 
 // One stage's scales to TMEM: 128 rows of x and CHUNKS x 128 weight rows, GROUPS of 128 elements of K.
 template <int CHUNKS, int GROUPS>
-__device__ __forceinline__ void product_scales(uint32_t ta, uint64_t adesc, uint64_t bdesc) {
+__device__ __forceinline__ void product_scales(uint32_t ta, uint32_t b_step, uint64_t adesc, uint64_t bdesc) {
 #pragma unroll
   for (int j = 0; j < GROUPS; ++j) {
     tc_cp_scales(ta + 4 * j, adesc + j * 32);
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) tc_cp_scales(ta + 8 + 8 * j + 4 * c, bdesc + c * 64 + j * 32);
+    for (int c = 0; c < CHUNKS; ++c) tc_cp_scales(ta + 8 + b_step * j + 4 * c, bdesc + c * 64 + j * 32);
   }
 }
 
-// One stage's STEPS MMAs of 64 elements of K; ta and tb are the scales' columns.
+// One stage's STEPS MMAs of 64 elements of K; ta and tb are the scales' columns, those
+// of the weights b_step apart for each 128 elements of K.
 template <int STEPS>
 __device__ __forceinline__ void product_mmas(uint32_t acc, uint64_t adesc, uint64_t bdesc, uint32_t ta, uint32_t tb,
-                                             uint32_t idesc, bool accumulate) {
+                                             uint32_t b_step, uint32_t idesc, bool accumulate) {
 #pragma unroll
   for (int kk = 0; kk < STEPS; ++kk) {
     constexpr uint32_t kPair = (2u << 4) | (2u << 29);  // the upper two of a column's four scales
     tc_mma_mxf4(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc | (kk & 1 ? kPair : 0), ta + 4 * (kk >> 1),
-                tb + 8 * (kk >> 1), kk > 0 || accumulate);
+                tb + b_step * (kk >> 1), kk > 0 || accumulate);
   }
 }
 
@@ -262,20 +296,20 @@ template <int YT, bool SWIGLU>
 __global__ void __launch_bounds__(kProductThreads, 1)
     expert_product_kernel(const __grid_constant__ ProductMaps maps, ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
-  __shared__ __align__(8) uint64_t full[kProductStages], empty[kProductStages], acc_full[2], acc_empty[2], drained;
-  __shared__ __align__(8) uint64_t scaled[kProductStages], taken[kScaleWarps][kScaleRing];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(8) uint64_t scaled[kMaxStages], taken[kScaleWarps];
   __shared__ uint32_t tmem_slot;
   __shared__ long long scan_scratch[32];
   __shared__ volatile int s_abort;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
-  uint8_t* ring = sm + (size_t)kProductStages * kProductStage;
-  uint8_t* slots = ring + kScaleWarps * kScaleRing * kScalePair;
+  uint8_t* ring = sm + kProductSmem - 1024 - product_fixed_smem(p.E);
+  uint8_t* slots = ring + kScaleWarps * kScaleStage;
   int* pre = reinterpret_cast<int*>(slots + kScaleWarps * kScaleSlots * kScalePair);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kProductStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&scaled[i], 1);
       mbar_init(&empty[i], 1);
@@ -284,7 +318,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], kProductThreads / 32 - kEpilogueWarp);
     }
-    for (int i = 0; i < kScaleWarps * kScaleRing; ++i) mbar_init(&taken[0][i], 1);
+    for (int i = 0; i < kScaleWarps; ++i) mbar_init(&taken[i], 1);
     mbar_init(&drained, 1);
     mbar_fence_init();
     s_abort = 0;
@@ -297,6 +331,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   pdl_launch_dependents();
 
   // running row tiles of the experts
+  bool few = true;
   {
     int* first = pre + p.E + 1;
     int* count = first + p.E;
@@ -314,6 +349,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (blockIdx.x == 0) set_error(p.status, MOE_ERR_BAD_ASSIST);
           n = 0;
         }
+        few = few && n <= kFewRows;
         first[e] = lo;
         count[e] = n;
       }
@@ -330,27 +366,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  few = __syncthreads_and(few);
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  const uint32_t tmem_sf = tmem + 2 * kAccCols;
-
   const int m_tiles = __shfl_sync(0xffffffffu, pre[p.E], 0), KB = (p.K + kKStage - 1) / kKStage;
-  // weight rows a unit: the width whose rounds of units cost least, a unit's
-  // cost being its weight rows and half a box for its rows and its ends
-  int boxes = 1;
-  {
-    long long best = 1ll << 62;
-    for (int b = kMaxBoxes; b >= 1; --b) {
-      const long long units = (long long)m_tiles * ((p.N + 64 * b - 1) / (64 * b));
-      const long long cost = (units + gridDim.x - 1) / gridDim.x * (2 * b + 1);
-      if (cost < best) {
-        best = cost;
-        boxes = b;
-      }
-    }
-  }
-  const int width = boxes * 64, n_tiles = (p.N + width - 1) / width;
+  const ProductShape shape = product_shape(p.N, p.E, m_tiles, few);
+  const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
+  const uint32_t stages = __shfl_sync(0xffffffffu, shape.stages, 0), a_bytes = __shfl_sync(0xffffffffu, shape.a_bytes, 0);
+  const uint32_t stage_bytes = __shfl_sync(0xffffffffu, shape.stage_bytes, 0), sf_cols = __shfl_sync(0xffffffffu, shape.sf_cols, 0);
+  const uint32_t tmem_sf = tmem + 2 * width, b_step = width > 128 ? 8 : 4;
   const int units = m_tiles * n_tiles;
   const bool whole = p.K % kKStage == 0;
   const ProductAbort ab{&s_abort, p.status, p.timeout_ns};
@@ -361,7 +385,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   // branch every descriptor took the slow way into uniform registers.
   if (warp == 0) {
     const int nt128 = (p.N + 127) / 128;
-    const CUtensorMap* mw = boxes == 3 ? &maps.w192 : boxes == 2 ? &maps.w128 : &maps.w64;
+    const CUtensorMap* mw = width == 192 ? &maps.w192 : width == 128 ? &maps.w128 : &maps.w64;
     const uint32_t sm0 = smem_u32(sm), bar0 = smem_u32(full);
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
@@ -370,28 +394,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
       const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
                 row = __shfl_sync(0xffffffffu, (int)un.row0, 0);
-      const bool few = rows <= 32;
-      const CUtensorMap* mx = few ? &maps.x32 : &maps.x128;
-      const uint32_t bytes = (uint32_t)width * 128u + (few ? 32u * 128u : kABytes) + kSfbBytes;
+      const CUtensorMap* mx = rows <= kFewRows ? &maps.x32 : &maps.x128;
+      const uint32_t bytes = ((uint32_t)width + (rows <= kFewRows ? kFewRows : kRowsTile)) * 128u + kSfbBytes;
       const int sf_row = e * nt128 + (un.n0 >> 7);
       for (int kb = 0; kb < KB; ++kb) {
         ok = __all_sync(0xffffffffu, product_wait(&empty[stage], phase, ab));
         if (!ok) break;
-        const uint32_t st = sm0 + stage * kProductStage, bar = bar0 + stage * 8;
+        const uint32_t st = sm0 + stage * stage_bytes, bar = bar0 + stage * 8;
         if (leader) {
           mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_3d(st + kABytes, mw, kb * 128, un.n0, e, bar);
+          tma_load_3d(st + a_bytes, mw, kb * 128, un.n0, e, bar);
           tma_load_2d(st, mx, kb * 128, row, bar);
-          tma_load_2d(st + kABytes + kBBytes, &maps.wsf, kb * 256, sf_row, bar);
+          tma_load_2d(st + a_bytes + width * 128, &maps.wsf, kb * 256, sf_row, bar);
         }
-        if (++stage == kProductStages) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
-    const uint64_t adesc0 = sw128_desc(sm), bdesc0 = sw128_desc(sm + kABytes);
+    const uint64_t adesc0 = sw128_desc(sm), bdesc0 = sw128_desc(sm + a_bytes);
     const bool leader = elect_one();
     const int n_step = (int)gridDim.x % n_tiles;
     int n_index = (int)blockIdx.x % n_tiles;
@@ -402,25 +425,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       n_index += n_step;
       if (n_index >= n_tiles) n_index -= n_tiles;
       const uint32_t shift = (n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
-      const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * kAccCols;
+      const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * width;
       ok = product_wait(&acc_empty[buf], ((done >> 1) & 1) ^ 1, ab);
       for (int kb = 0; kb < KB && ok; ++kb) {
         if (!ready) ok = product_wait(&full[stage], phase, ab) && product_wait(&scaled[stage], phase, ab);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t step = stage * (kProductStage >> 4), here = stage;
-        const uint32_t ta = tmem_sf + stage * kSfCols, tb = ta + 8 + shift;
-        if (++stage == kProductStages) {
+        const uint32_t step = stage * (stage_bytes >> 4), here = stage;
+        const uint32_t ta = tmem_sf + stage * sf_cols, tb = ta + 8 + shift;
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
         const bool there = mbar_test_wait(&full[stage], phase), taken_up = mbar_test_wait(&scaled[stage], phase);
         if (leader) {
           const int steps = whole || kb + 1 < KB ? 4 : (p.K - kb * kKStage + 63) / 64;
-          if (steps == 4) product_mmas<4>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
-          else if (steps == 3) product_mmas<3>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
-          else if (steps == 2) product_mmas<2>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
-          else product_mmas<1>(acc, adesc0 + step, bdesc0 + step, ta, tb, idesc, kb != 0);
+          if (steps == 4) product_mmas<4>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
+          else if (steps == 3) product_mmas<3>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
+          else if (steps == 2) product_mmas<2>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
+          else product_mmas<1>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
           tc_commit(&empty[here]);
           if (kb + 1 == KB) tc_commit(&acc_full[buf]);
         }
@@ -429,101 +452,90 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     if (leader) tc_commit(&drained);
   } else if (warp < 2 + kScaleWarps) {
-    // scales: this warp's pairs of stages are every kScaleWarps-th one
-    const int pairs = (KB + 1) / 2;
-    const uint32_t slot0 = smem_u32(slots) + (warp - 2) * kScaleSlots * kScalePair;
-    const uint8_t* my_ring = ring + (warp - 2) * kScaleRing * kScalePair;
-    const uint32_t ring0 = smem_u32(my_ring) + lane * 16;
-    const uint64_t asf0 = sf_desc(my_ring), bsf0 = sf_desc(sm + kABytes + kBBytes);
+    // scales of the stages of this warp's parity
+    const uint32_t parity = warp - 2;
+    const uint32_t slot0 = smem_u32(slots) + parity * kScaleSlots * kScalePair + lane * 16;
+    const uint8_t* my_ring = ring + parity * kScaleStage;
+    const uint32_t dst = smem_u32(my_ring) + lane * 16;
+    const uint64_t asf = sf_desc(my_ring), bsf0 = sf_desc(sm + a_bytes + width * 128);
     const bool leader = elect_one();
-    int load_u = blockIdx.x, load_pair = warp - 2;
+    int load_u = blockIdx.x, load_kb = 0;
     uint32_t load_slot = 0;
-    bool fresh = true;
     ProductUnit ahead{};
     const auto load_next = [&] {
-      while (load_pair >= pairs) {
-        load_pair -= pairs;
-        load_u += gridDim.x;
-        fresh = true;
-      }
       if (load_u < units) {
-        if (fresh) ahead = product_unit(p, pre, load_u, n_tiles, width);
-        fresh = false;
-        load_row_scales(p, ahead, load_pair * 2, slot0 + load_slot * kScalePair);
+        if (load_kb == 0) ahead = product_unit(p, pre, load_u, n_tiles, width);
+        load_row_scales(p, ahead, load_kb, slot0 + load_slot * kScalePair);
         load_slot = load_slot + 1 == kScaleSlots ? 0 : load_slot + 1;
-        load_pair += kScaleWarps;
+        load_kb += 2;
+        if (load_kb >= KB) {
+          load_kb = 0;
+          load_u += gridDim.x;
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int i = 0; i < kScaleSlots - 1; ++i) load_next();
-    uint32_t stage = 0, phase = 0, slot = 0, at = 0, at_phase = 1;
-    int turn = 0;
+    const int n_step = (int)gridDim.x % n_tiles;
+    int n_index = (int)blockIdx.x % n_tiles;
+    uint32_t stage = 0, phase = 0, slot = 0, taken_phase = 1;  // stage: of kb, which starts a pair
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const int n0 = (u % n_tiles) * width;
+      const int n0 = n_index * width;
+      n_index += n_step;
+      if (n_index >= n_tiles) n_index -= n_tiles;
       const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
-      for (int kb = 0; kb < KB && ok; kb += 2) {
-        const int here = min(2, KB - kb);  // stages of this pair
-        if (turn != warp - 2) {
-          stage += here;
-          if (stage >= kProductStages) {
-            stage -= kProductStages;
-            phase ^= 1;
-          }
-          turn = turn + 1 == kScaleWarps ? 0 : turn + 1;
-          continue;
-        }
-        turn = turn + 1 == kScaleWarps ? 0 : turn + 1;
+      for (int kb = 0; kb < KB; kb += 2) {
         load_next();
         asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
-        // the lane's own rows: word i of row c is 128-element group i of the two stages
-        uint4 v[4];
+        const uint32_t h = (stage ^ parity) & 1;  // which stage of the pair is this warp's
+        if (kb + (int)h < KB) {
+          // the lane's own rows: words 2h and 2h + 1 of row c are the stage's two 128-element groups
+          uint2 v[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w)
-                       : "r"(slot0 + slot * kScalePair + c * 512 + lane * 16));
-        slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-        ok = __all_sync(0xffffffffu, product_wait(&taken[warp - 2][at], at_phase, ab));
-        if (!ok) break;
-        // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
-        const uint32_t dst = ring0 + at * kScalePair;
-        const auto put = [&](int i, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + i * 512), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-        };
-        put(0, v[0].x, v[1].x, v[2].x, v[3].x);
-        put(1, v[0].y, v[1].y, v[2].y, v[3].y);
-        put(2, v[0].z, v[1].z, v[2].z, v[3].z);
-        put(3, v[0].w, v[1].w, v[2].w, v[3].w);
-        fence_proxy_async_smem();
-        __syncwarp();
-        for (int h = 0; h < here; ++h) {
+          for (int c = 0; c < 4; ++c)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(v[c].x), "=r"(v[c].y)
+                         : "r"(slot0 + slot * kScalePair + c * 512 + h * 8));
+          uint32_t mine = stage + h, mine_phase = phase;
+          if (mine == stages) {
+            mine = 0;
+            mine_phase ^= 1;
+          }
+          ok = __all_sync(0xffffffffu, product_wait(&taken[parity], taken_phase, ab));
+          if (!ok) break;
+          taken_phase ^= 1;
+          // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(v[0].y), "r"(v[1].y), "r"(v[2].y), "r"(v[3].y)
+                       : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
           // the weights' scales are in the stage; its TMEM columns are free since the stage was
-          ok = __all_sync(0xffffffffu, product_wait(&full[stage], phase, ab));
+          ok = __all_sync(0xffffffffu, product_wait(&full[mine], mine_phase, ab));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            const uint32_t ta = tmem_sf + stage * kSfCols;
-            const uint64_t asf = asf0 + at * (kScalePair >> 4) + h * 64, bsf = bsf0 + stage * (kProductStage >> 4);
-            if (p.K - (kb + h) * kKStage <= 128) {  // a last stage of one group
-              if (two) product_scales<2, 1>(ta, asf, bsf);
-              else product_scales<1, 1>(ta, asf, bsf);
+            const uint32_t ta = tmem_sf + mine * sf_cols;
+            const uint64_t bsf = bsf0 + mine * (stage_bytes >> 4);
+            if (p.K - (kb + (int)h) * kKStage <= 128) {  // a last stage of one group
+              if (two) product_scales<2, 1>(ta, b_step, asf, bsf);
+              else product_scales<1, 1>(ta, b_step, asf, bsf);
             } else {
-              if (two) product_scales<2, 2>(ta, asf, bsf);
-              else product_scales<1, 2>(ta, asf, bsf);
+              if (two) product_scales<2, 2>(ta, b_step, asf, bsf);
+              else product_scales<1, 2>(ta, b_step, asf, bsf);
             }
-            tc_commit(&scaled[stage]);
-            if (h + 1 == here) tc_commit(&taken[warp - 2][at]);
+            tc_commit(&scaled[mine]);
+            tc_commit(&taken[parity]);
           }
           __syncwarp();
-          if (++stage == kProductStages) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-        if (++at == kScaleRing) {
-          at = 0;
-          at_phase ^= 1;
+        slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+        stage += min(2, KB - kb);
+        if (stage >= stages) {
+          stage -= stages;
+          phase ^= 1;
         }
       }
     }
@@ -538,10 +550,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       tc_fence_after();
       const int r = 32 * q + lane;
       if (32 * q < un.rows) {
-        const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * kAccCols;
+        const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * width;
         // 64 columns at a time, the third part by the halves in turn
 #pragma unroll 1
-        for (int g = 0; g < boxes; ++g) {
+        for (int g = 0; g < width / 64; ++g) {
           const int n = un.n0 + g * 64;
           if ((g == 2 ? (int)(done & 1) : g) != half || n >= p.N) continue;
           uint32_t v[64];
@@ -699,7 +711,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   const ProductKernel kernel = y_dtype == MOE_F16    ? product_kernel<MOE_F16>(sw)
                                : y_dtype == MOE_BF16 ? product_kernel<MOE_BF16>(sw)
                                                      : product_kernel<MOE_MXFP4>(sw);
-  const size_t smem = product_smem(E);
+  const size_t smem = kProductSmem;
   int per_sm = 0;
   if (resident_blocks((const void*)kernel, kProductThreads, smem, &per_sm) != cudaSuccess || per_sm < 1)
     return MOE_ERR_CUDA;
