@@ -15,11 +15,11 @@
 //   * the weights' scales, laid out in the tensor cores' order (MOE_SF_TILED), come
 //     by one more box, 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the
 //     copy engine busy for longer than the codes did); the rows' scales lie a row
-//     after the other as dispatch wrote them: a lane brings 16 bytes of its rows
-//     (r, r + 32, ..) at a time by cp.async and stores them in that order; the same
-//     warp's tcgen05.cp takes both to TMEM and tells the MMA warp, which is left
-//     with four MMAs and one commit a stage (what it has to issue bounds a stage);
-//   * warps: 0 TMA, 1 MMA, 2 and 3 scales, 4..11 epilogue (two for each quarter of
+//     after the other as dispatch wrote them: a lane brings 8 bytes of its rows
+//     (r, r + 32, ..) by cp.async and stores them in that order; the same warp's
+//     tcgen05.cp takes both to TMEM and tells the MMA warp, which is left with four
+//     MMAs and one commit a stage (what it has to issue bounds a stage);
+//   * warps: 0 TMA, 1 MMA, 2..5 scales, 6..13 epilogue (two for each quarter of
 //     the accumulator's lanes). Two accumulators of 192 columns and the scales fill
 //     TMEM, so that the next unit's MMAs run while this one is read (256 columns
 //     would leave room for one: the hand-over then stood still for each unit);
@@ -45,7 +45,7 @@ struct ProductParams {
   void* y;                 // [W*A][C]
   uint8_t* ys;             // [W*A][ceil(C/32)], MX FP4 output
   int W, L, E, N, K, C;    // C output columns
-  int xs_align;            // bytes that a copy of row scales may take: 16, 8, 4 or 1
+  int xs_align;            // bytes that a copy of row scales may take: 8, 4 or 1
   long long A;
   int* status;
   uint64_t timeout_ns;
@@ -57,27 +57,31 @@ struct ProductMaps {
   CUtensorMap x32, x128, w64, w128, w192, wsf;
 };
 
-constexpr int kProductThreads = 384;
+constexpr int kProductThreads = 448;
 constexpr int kMaxStages = 8;
-constexpr int kEpilogueWarp = 4;             // first of the eight
+constexpr int kEpilogueWarp = 6;             // first of the eight
 constexpr int kRowsTile = 128;               // MMA M
 constexpr int kFewRows = 32;
 constexpr int kMaxBoxes = 3;                 // of 64 weight rows: MMA N <= 192
 constexpr int kKStage = 256;                 // elements of K a stage: 128 bytes a row
 constexpr uint32_t kSfbBytes = 2 * 1024;     // 2 x 128 rows x 8 scales
-// Row scales are read for pairs of stages (16 bytes a row). Two warps bring them to
-// the tensor cores, one the even and one the odd stages of the ring: the number of
-// stages is even, so that a stage's barriers have one and the same waiter, which
-// cannot be a round ahead. Each has kScaleSlots pairs under way or landed, and the
-// scales of one stage in the tensor cores' order, from which tcgen05.cp takes them.
-constexpr int kScaleWarps = 2, kScaleSlots = 3;
-constexpr uint32_t kScalePair = 128 * 16, kScaleStage = 128 * 8;
+// Four warps bring the scales to the tensor cores, each those of every fourth place
+// of the stage ring (a place's barriers have one and the same waiter, which cannot
+// be a round ahead). Each has the rows' scales of kScaleSlots stages under way or
+// landed, and of kScaleRing stages in the tensor cores' order, from which tcgen05.cp
+// takes them (it waits in line behind the MMAs). A warp needs 1200 clocks a stage.
+constexpr int kScaleWarps = 4, kScaleSlots = 3, kScaleRing = 2;
+constexpr uint32_t kScaleStage = 128 * 8;
+// An epilogue warp turns 32 rows x 64 bytes around in shared memory before it
+// stores them (rows 80 bytes apart: no bank is hit twice): stored a row a lane, every
+// store touched 32 lines, and the epilogue was what the scale warps waited for.
+constexpr uint32_t kTurnRow = 80, kTurnWarp = 32 * kTurnRow;
 constexpr size_t kProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
 
-// Shared memory behind the stages: row scales in order and under way, running
-// row tiles [E+1], first row [E], row count [E].
+// Shared memory behind the stages: row scales in order and under way, the
+// epilogue warps' turning places, running row tiles [E+1], first flat row [E], row count [E].
 __host__ __device__ inline uint32_t product_fixed_smem(int E) {
-  return (uint32_t)kScaleWarps * (kScaleStage + kScaleSlots * kScalePair) + ((3u * E + 1) * 4 + 15) / 16 * 16;
+  return (uint32_t)kScaleWarps * (kScaleRing + kScaleSlots) * kScaleStage + 8 * kTurnWarp + ((3u * E + 1) * 4 + 15) / 16 * 16;
 }
 
 // How a launch cuts its work: weight rows a unit, rows of A kept for a stage, and
@@ -91,12 +95,12 @@ struct ProductShape {
 
 __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles, bool few) {
   int boxes = 1;
-  long long best = 1ll << 62;
+  uint32_t best = 0xffffffffu;
   // the width whose rounds of units cost least: with few rows a unit streams its
   // weights (its cost is their bytes), with many it also moves its rows
   for (int b = kMaxBoxes; b >= 1; --b) {
-    const long long units = (long long)m_tiles * ((N + 64 * b - 1) / (64 * b));
-    const long long cost = (units + gridDim.x - 1) / gridDim.x * (few ? 4 * b + 1 : b + 2);
+    const uint32_t units = (uint32_t)m_tiles * (uint32_t)((N + 64 * b - 1) / (64 * b));
+    const uint32_t cost = (units + gridDim.x - 1) / gridDim.x * (uint32_t)(few ? 4 * b + 1 : b + 2);
     if (cost < best) {
       best = cost;
       boxes = b;
@@ -111,7 +115,7 @@ __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles,
   // TMEM: two accumulators, then 2 x 4 columns of the rows' scales and 2 x 4 for
   // every 128 weight rows of a stage
   s.sf_cols = 8 + (boxes == 3 ? 16 : 8);
-  s.stages = min(s.stages, (512 - 2 * s.width) / (int)s.sf_cols) & ~1;
+  s.stages = min(s.stages, (512 - 2 * s.width) / (int)s.sf_cols);
   return s;
 }
 
@@ -136,7 +140,7 @@ __device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, cons
   x.e = e;
   x.n0 = (u - mt * n_tiles) * width;
   x.rows = min(kRowsTile, count[e] - at);
-  x.row0 = (long long)(e / p.L) * p.A + first[e] + at;
+  x.row0 = first[e] + at;
   return x;
 }
 
@@ -175,35 +179,30 @@ __device__ __forceinline__ bool product_wait_warp(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, ok);
 }
 
-// The 16 scale bytes of rows lane, lane + 32, .. of a unit for stages kb and
-// kb + 1 into this lane's part of a slot, by the widest asynchronous copies that
-// the row length (K / 32 bytes) and x_scales' address align; what lies beyond the
-// row's end is left as it is, or zero where a stage's last MMA reads it.
-__device__ __forceinline__ void load_row_scales(const ProductParams& p, const ProductUnit& un, int kb, uint32_t slot) {
-  const int lane = threadIdx.x & 31, blocks = p.K / 32, left = min(16, blocks - kb * 8);
+// The 8 scale bytes of rows lane, lane + 32, .. of a unit for stage kb into this
+// lane's part of a slot, by the widest asynchronous copies that the row length
+// (K / 32 bytes) and x_scales' address align; what lies beyond the row's end is
+// left as it is, or zero where a last MMA reads it.
+__device__ __forceinline__ void load_row_scales(const ProductParams& p, const ProductUnit& un, int kb, uint32_t dst) {
+  const int lane = threadIdx.x & 31, blocks = p.K / 32, left = min(8, blocks - kb * 8);
   const uint8_t* src = p.xs + (size_t)(un.row0 + lane) * blocks + kb * 8;
   const size_t step = (size_t)32 * blocks;
-  const uint32_t dst = slot;
-  if (p.xs_align == 16) {
+  if (p.xs_align == 8) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (lane + 32 * c < un.rows)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + c * 512), "l"(src + c * step) : "memory");
-  } else if (p.xs_align > 1) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + c * 256), "l"(src + c * step) : "memory");
+  } else if (p.xs_align == 4) {
     for (int c = 0; lane + 32 * c < un.rows; ++c)
-      for (int b = 0; b < left; b += p.xs_align) {
-        if (p.xs_align == 8)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + c * 512 + b), "l"(src + c * step + b) : "memory");
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + c * 512 + b), "l"(src + c * step + b) : "memory");
-      }
+      for (int b = 0; b < left; b += 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + c * 256 + b), "l"(src + c * step + b) : "memory");
   } else {
     for (int c = 0; lane + 32 * c < un.rows; ++c)
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         uint32_t v = 0;
         for (int b = 0; b < 4; ++b)
           if (4 * i + b < left) v |= (uint32_t)__ldg(src + c * step + 4 * i + b) << (8 * b);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + c * 512 + 4 * i), "r"(v) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + c * 256 + 4 * i), "r"(v) : "memory");
       }
   }
 }
@@ -242,52 +241,69 @@ __device__ __forceinline__ uint32_t pack_y(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// CNT neighbouring results of one row from column c on.
-template <int YT, int CNT>
-__device__ __forceinline__ void store_results(const ProductParams& p, long long row, int c, const float (&v)[CNT]) {
+// 32 neighbouring results (columns c ..) of each lane's row, row0 + lane, of which the
+// first `rows` lanes' exist; the whole warp takes part.
+template <int YT>
+__device__ __forceinline__ void store_results(const ProductParams& p, uint32_t turn, long long row0, int rows, int c,
+                                              const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (c >= p.C) return;
   if (YT == MOE_MXFP4) {
+    float m = 0.f;
 #pragma unroll
-    for (int b = 0; b < CNT / 32; ++b) {
-      const int cb = c + 32 * b, n = min(32, p.C - cb);
-      if (n <= 0) return;
-      float m = 0.f;
+    for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));  // columns beyond C are zeros
+    const int se = mx_exponent(m, 2), n = min(32, p.C - c);
+    const float inv = exp2_exact(-se);
+    uint32_t q[4];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[32 * b + j]));  // columns beyond C are zeros
-      const int se = mx_exponent(m, 2);
-      const float inv = exp2_exact(-se);
-      uint32_t q[4];
+    for (int i = 0; i < 4; ++i) {
+      q[i] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          q[i] |= cvt_fp4x2(__fmul_rn(v[32 * b + 8 * i + 2 * j], inv), __fmul_rn(v[32 * b + 8 * i + 2 * j + 1], inv)) << (8 * j);
-      }
-      uint8_t* out = static_cast<uint8_t*>(p.y) + (size_t)row * (p.C / 2) + cb / 2;
-      if (n == 32 && (p.C & 31) == 0) {
+      for (int j = 0; j < 4; ++j)
+        q[i] |= cvt_fp4x2(__fmul_rn(v[8 * i + 2 * j], inv), __fmul_rn(v[8 * i + 2 * j + 1], inv)) << (8 * j);
+    }
+    if (lane < rows) {
+      const size_t row = (size_t)(row0 + lane);
+      uint8_t* out = static_cast<uint8_t*>(p.y) + row * (p.C / 2) + c / 2;
+      if ((p.C & 31) == 0) {
         st_v4(out, make_int4(q[0], q[1], q[2], q[3]));
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (2 * i < n) out[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
       }
-      p.ys[(size_t)row * ((p.C + 31) / 32) + cb / 32] = (uint8_t)(se + 127);
+      p.ys[row * ((p.C + 31) / 32) + c / 32] = (uint8_t)(se + 127);
     }
-  } else {
-    uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)row * p.C + c;
-    if ((p.C & 7) == 0) {
+  } else if ((p.C & 7) == 0) {
 #pragma unroll
-      for (int i = 0; i < CNT; i += 8)
-        if (c + i < p.C)
-          st_v4(out + i, make_int4(pack_y<YT>(v[i], v[i + 1]), pack_y<YT>(v[i + 2], v[i + 3]), pack_y<YT>(v[i + 4], v[i + 5]),
-                                   pack_y<YT>(v[i + 6], v[i + 7])));
-    } else {
+    for (int i = 0; i < 4; ++i)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(turn + lane * kTurnRow + i * 16),
+                   "r"(pack_y<YT>(v[8 * i], v[8 * i + 1])), "r"(pack_y<YT>(v[8 * i + 2], v[8 * i + 3])),
+                   "r"(pack_y<YT>(v[8 * i + 4], v[8 * i + 5])), "r"(pack_y<YT>(v[8 * i + 6], v[8 * i + 7]))
+                   : "memory");
+    __syncwarp();
+    // 8 rows x 64 bytes a store
+    const int part = (lane & 3) * 8;
+    uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)(row0 + (lane >> 2)) * p.C + c + part;
 #pragma unroll
-      for (int i = 0; i < CNT; i += 2) {
-        const uint32_t w = pack_y<YT>(v[i], v[i + 1]);
-        if (c + i < p.C) out[i] = (uint16_t)w;
-        if (c + i + 1 < p.C) out[i + 1] = (uint16_t)(w >> 16);
+    for (int i = 0; i < 4; ++i) {
+      if (8 * i >= rows) break;
+      if (8 * i + (lane >> 2) < rows && c + part < p.C) {
+        int4 w;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(turn + (8 * i + (lane >> 2)) * kTurnRow + (lane & 3) * 16));
+        st_v4(out + (size_t)(8 * i) * p.C, w);
       }
+    }
+    __syncwarp();
+  } else if (lane < rows) {
+    uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)(row0 + lane) * p.C + c;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint32_t w = pack_y<YT>(v[i], v[i + 1]);
+      if (c + i < p.C) out[i] = (uint16_t)w;
+      if (c + i + 1 < p.C) out[i + 1] = (uint16_t)(w >> 16);
     }
   }
 }
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     expert_product_kernel(const __grid_constant__ ProductMaps maps, ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
-  __shared__ __align__(8) uint64_t scaled[kMaxStages], taken[kScaleWarps];
+  __shared__ __align__(8) uint64_t scaled[kMaxStages], taken[kScaleWarps][kScaleRing];
   __shared__ uint32_t tmem_slot;
   __shared__ long long scan_scratch[32];
   __shared__ volatile int s_abort;
@@ -305,8 +321,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   uint8_t* ring = sm + kProductSmem - 1024 - product_fixed_smem(p.E);
-  uint8_t* slots = ring + kScaleWarps * kScaleStage;
-  int* pre = reinterpret_cast<int*>(slots + kScaleWarps * kScaleSlots * kScalePair);
+  uint8_t* slots = ring + kScaleWarps * kScaleRing * kScaleStage;
+  uint8_t* turn = slots + kScaleWarps * kScaleSlots * kScaleStage;
+  int* pre = reinterpret_cast<int*>(turn + 8 * kTurnWarp);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], kProductThreads / 32 - kEpilogueWarp);
     }
-    for (int i = 0; i < kScaleWarps; ++i) mbar_init(&taken[i], 1);
+    for (int i = 0; i < kScaleWarps * kScaleRing; ++i) mbar_init(&taken[0][i], 1);
     mbar_init(&drained, 1);
     mbar_fence_init();
     s_abort = 0;
@@ -350,7 +367,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           n = 0;
         }
         few = few && n <= kFewRows;
-        first[e] = lo;
+        first[e] = (int)(e / p.L * p.A) + lo;  // flat rows fit 32 bits
         count[e] = n;
       }
       const long long tiles = (n + kRowsTile - 1) / kRowsTile;
@@ -452,25 +469,31 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     if (leader) tc_commit(&drained);
   } else if (warp < 2 + kScaleWarps) {
-    // scales of the stages of this warp's parity
-    const uint32_t parity = warp - 2;
-    const uint32_t slot0 = smem_u32(slots) + parity * kScaleSlots * kScalePair + lane * 16;
-    const uint8_t* my_ring = ring + parity * kScaleStage;
-    const uint32_t dst = smem_u32(my_ring) + lane * 16;
-    const uint64_t asf = sf_desc(my_ring), bsf0 = sf_desc(sm + a_bytes + width * 128);
+    // scales of the stages in this warp's places of the ring
+    const uint32_t mine = warp - 2;
+    const uint32_t slot0 = smem_u32(slots) + mine * kScaleSlots * kScaleStage + lane * 8;
+    const uint8_t* my_ring = ring + mine * kScaleRing * kScaleStage;
+    const uint32_t dst0 = smem_u32(my_ring) + lane * 16;
+    const uint64_t asf0 = sf_desc(my_ring), bsf0 = sf_desc(sm + a_bytes + width * 128);
     const bool leader = elect_one();
     int load_u = blockIdx.x, load_kb = 0;
-    uint32_t load_slot = 0;
+    uint32_t load_slot = 0, load_stage = 0;
+    bool fresh = true;
     ProductUnit ahead{};
     const auto load_next = [&] {
-      if (load_u < units) {
-        if (load_kb == 0) ahead = product_unit(p, pre, load_u, n_tiles, width);
-        load_row_scales(p, ahead, load_kb, slot0 + load_slot * kScalePair);
-        load_slot = load_slot + 1 == kScaleSlots ? 0 : load_slot + 1;
-        load_kb += 2;
-        if (load_kb >= KB) {
+      for (bool found = false; !found && load_u < units;) {
+        if ((load_stage & (kScaleWarps - 1)) == mine) {
+          if (fresh) ahead = product_unit(p, pre, load_u, n_tiles, width);
+          fresh = false;
+          load_row_scales(p, ahead, load_kb, slot0 + load_slot * kScaleStage);
+          load_slot = load_slot + 1 == kScaleSlots ? 0 : load_slot + 1;
+          found = true;
+        }
+        if (++load_stage == stages) load_stage = 0;
+        if (++load_kb == KB) {
           load_kb = 0;
           load_u += gridDim.x;
+          fresh = true;
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -478,34 +501,30 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int i = 0; i < kScaleSlots - 1; ++i) load_next();
     const int n_step = (int)gridDim.x % n_tiles;
     int n_index = (int)blockIdx.x % n_tiles;
-    uint32_t stage = 0, phase = 0, slot = 0, taken_phase = 1;  // stage: of kb, which starts a pair
+    uint32_t stage = 0, phase = 0, slot = 0, at = 0, taken_phase = 1;
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const int n0 = n_index * width;
       n_index += n_step;
       if (n_index >= n_tiles) n_index -= n_tiles;
       const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
-      for (int kb = 0; kb < KB; kb += 2) {
-        load_next();
-        asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
-        const uint32_t h = (stage ^ parity) & 1;  // which stage of the pair is this warp's
-        if (kb + (int)h < KB) {
-          // the lane's own rows: words 2h and 2h + 1 of row c are the stage's two 128-element groups
+      for (int kb = 0; kb < KB; ++kb) {
+        if ((stage & (kScaleWarps - 1)) == mine) {
+          load_next();
+          asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
+          // the lane's own rows: word i of row c is 128-element group i
           uint2 v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                          : "=r"(v[c].x), "=r"(v[c].y)
-                         : "r"(slot0 + slot * kScalePair + c * 512 + h * 8));
-          uint32_t mine = stage + h, mine_phase = phase;
-          if (mine == stages) {
-            mine = 0;
-            mine_phase ^= 1;
-          }
-          ok = __all_sync(0xffffffffu, product_wait(&taken[parity], taken_phase, ab));
+                         : "r"(slot0 + slot * kScaleStage + c * 256));
+          slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+          ok = __all_sync(0xffffffffu, product_wait(&taken[mine][at], taken_phase, ab));
           if (!ok) break;
-          taken_phase ^= 1;
           // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
+          const uint32_t dst = dst0 + at * kScaleStage;
+          const uint64_t asf = asf0 + at * (kScaleStage >> 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
                        : "memory");
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(v[0].y), "r"(v[1].y), "r"(v[2].y), "r"(v[3].y)
@@ -513,43 +532,47 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           // the weights' scales are in the stage; its TMEM columns are free since the stage was
-          ok = __all_sync(0xffffffffu, product_wait(&full[mine], mine_phase, ab));
+          ok = __all_sync(0xffffffffu, product_wait(&full[stage], phase, ab));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            const uint32_t ta = tmem_sf + mine * sf_cols;
-            const uint64_t bsf = bsf0 + mine * (stage_bytes >> 4);
-            if (p.K - (kb + (int)h) * kKStage <= 128) {  // a last stage of one group
+            const uint32_t ta = tmem_sf + stage * sf_cols;
+            const uint64_t bsf = bsf0 + stage * (stage_bytes >> 4);
+            if (p.K - kb * kKStage <= 128) {  // a last stage of one group
               if (two) product_scales<2, 1>(ta, b_step, asf, bsf);
               else product_scales<1, 1>(ta, b_step, asf, bsf);
             } else {
               if (two) product_scales<2, 2>(ta, b_step, asf, bsf);
               else product_scales<1, 2>(ta, b_step, asf, bsf);
             }
-            tc_commit(&scaled[mine]);
-            tc_commit(&taken[parity]);
+            tc_commit(&scaled[stage]);
+            tc_commit(&taken[mine][at]);
           }
           __syncwarp();
+          if (++at == kScaleRing) {
+            at = 0;
+            taken_phase ^= 1;
+          }
         }
-        slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-        stage += min(2, KB - kb);
-        if (stage >= stages) {
-          stage -= stages;
+        if (++stage == stages) {
+          stage = 0;
           phase ^= 1;
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp >= kEpilogueWarp) {
-    const int q = warp & 3, half = (warp - kEpilogueWarp) >> 2;
+    const int q = warp & 3, half = (warp - kEpilogueWarp) >> 2;  // quarter q: lanes 32 q ..
+    const uint32_t my_turn = smem_u32(turn) + (warp - kEpilogueWarp) * kTurnWarp;
     uint32_t done = 0;
     for (int u = blockIdx.x; u < units && !s_abort; u += gridDim.x, ++done) {
       const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
       const uint32_t buf = done & 1;
       if (!product_wait_warp(&acc_full[buf], (done >> 1) & 1, ab)) break;
       tc_fence_after();
-      const int r = 32 * q + lane;
-      if (32 * q < un.rows) {
+      const int rows = min(32, un.rows - 32 * q);
+      if (rows > 0) {
+        const long long row0 = un.row0 + 32 * q;
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * width;
         // 64 columns at a time, the third part by the halves in turn
 #pragma unroll 1
@@ -559,25 +582,24 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           uint32_t v[64];
           tc_ld64(acc + g * 64, v);
           tc_wait_ld();
-          if (r < un.rows) {
-            if (SWIGLU) {
-              float h[32];
+          float h[32];
+          if (SWIGLU) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
-                // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
-                // bits that follows
-                h[j] = __fdividef(a, 1.0f + __expf(-a)) * b;
-              }
-              store_results<YT>(p, un.row0 + r, n / 2, h);
-            } else {
-              float h[64];
+            for (int j = 0; j < 32; ++j) {
+              const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
+              // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
+              // bits that follows
+              h[j] = __fdividef(a, 1.0f + __expf(-a)) * b;
+            }
+            store_results<YT>(p, my_turn, row0, rows, n / 2, h);
+          } else {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) h[j] = __uint_as_float(v[j]);
-              store_results<YT>(p, un.row0 + r, n, h);
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) h[j] = __uint_as_float(v[32 * i + j]);
+              store_results<YT>(p, my_turn, row0, rows, n + 32 * i, h);
             }
           }
-          __syncwarp();
         }
       }
       tc_fence_before();
@@ -703,7 +725,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   p.N = n;
   p.K = k;
   p.C = C;
-  p.xs_align = k % 512 == 0 && aligned(x_scales, 16) ? 16 : k % 256 == 0 && aligned(x_scales, 8) ? 8 : k % 128 == 0 ? 4 : 1;
+  p.xs_align = k % 256 == 0 && aligned(x_scales, 8) ? 8 : k % 128 == 0 ? 4 : 1;
   p.A = A;
   p.status = &static_cast<WsHeader*>(ws)->status;
   p.timeout_ns = (uint64_t)cfg->wait_timeout_us * 1000ull;
