@@ -9,9 +9,9 @@
 //     few: streaming weights from HBM takes 23 bytes a clock and SM, the MMA eats
 //     64 of them a clock, so the unused rows cost nothing that is short, and
 //     each epilogue thread has one row with neighbouring features in registers;
-//   * codes come by TMA in 128-byte-swizzled boxes, 256 elements of K a stage; a
-//     unit of few rows takes a box of 32 rows of A, the rest 128, and where every
-//     expert has few rows the stages are that much smaller and more;
+//   * codes come by TMA in 128-byte-swizzled boxes, 256 elements of K a stage, as
+//     many boxes of 32 rows of A as the unit has rows for; where every expert has
+//     few rows the stages are that much smaller and more;
 //   * the weights' scales, laid out in the tensor cores' order (MOE_SF_TILED), come
 //     by one more box, 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the
 //     copy engine busy for longer than the codes did); the rows' scales lie a row
@@ -19,8 +19,8 @@
 //     (r, r + 32, ..) by cp.async and stores them in that order; the same warp's
 //     tcgen05.cp takes both to TMEM and tells the MMA warp, which is left with four
 //     MMAs and one commit a stage (what it has to issue bounds a stage);
-//   * warps: 0 TMA, 1 MMA, 2..5 scales, 6..13 epilogue (two for each quarter of
-//     the accumulator's lanes). Two accumulators of 192 columns and the scales fill
+//   * warps: 0 TMA, 1 MMA, 2..5 scales, 6..13 epilogue (four for each of the two
+//     accumulators). Two accumulators of 192 columns and the scales fill
 //     TMEM, so that the next unit's MMAs run while this one is read (256 columns
 //     would leave room for one: the hand-over then stood still for each unit);
 //   * one persistent CTA an SM; units are dealt out round-robin over all experts
@@ -51,17 +51,17 @@ struct ProductParams {
   uint64_t timeout_ns;
 };
 
-// Boxes of 32 and 128 rows of x, of 64, 128 and 192 rows of w, and of the scales of
-// 2 x 128 rows of w: one copy a stage each.
+// Boxes of 32 rows of x, of 64, 128 and 192 rows of w, and of the scales of 2 x 128
+// rows of w; all but x's are one copy a stage.
 struct ProductMaps {
-  CUtensorMap x32, x128, w64, w128, w192, wsf;
+  CUtensorMap x, w64, w128, w192, wsf;
 };
 
 constexpr int kProductThreads = 448;
 constexpr int kMaxStages = 8;
 constexpr int kEpilogueWarp = 6;             // first of the eight
 constexpr int kRowsTile = 128;               // MMA M
-constexpr int kFewRows = 32;
+constexpr int kRowsBox = 32;
 constexpr int kMaxBoxes = 3;                 // of 64 weight rows: MMA N <= 192
 constexpr int kKStage = 256;                 // elements of K a stage: 128 bytes a row
 constexpr uint32_t kSfbBytes = 2 * 1024;     // 2 x 128 rows x 8 scales
@@ -93,14 +93,15 @@ struct ProductShape {
   uint32_t a_bytes, stage_bytes, sf_cols;
 };
 
-__device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles, bool few) {
+__device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles, int most_rows) {
   int boxes = 1;
   uint32_t best = 0xffffffffu;
-  // the width whose rounds of units cost least: with few rows a unit streams its
-  // weights (its cost is their bytes), with many it also moves its rows
+  // the width whose rounds of units cost least: where experts have one row tile, a
+  // unit streams its weights from HBM (its cost is their bytes); where they have
+  // more, its rows and weights come from L2 and a wider unit saves rows
   for (int b = kMaxBoxes; b >= 1; --b) {
     const uint32_t units = (uint32_t)m_tiles * (uint32_t)((N + 64 * b - 1) / (64 * b));
-    const uint32_t cost = (units + gridDim.x - 1) / gridDim.x * (uint32_t)(few ? 4 * b + 1 : b + 2);
+    const uint32_t cost = (units + gridDim.x - 1) / gridDim.x * (uint32_t)(most_rows <= kRowsTile ? 4 * b + 1 : b + 2);
     if (cost < best) {
       best = cost;
       boxes = b;
@@ -109,7 +110,7 @@ __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles,
   ProductShape s;
   s.width = boxes * 64;
   s.n_tiles = (N + s.width - 1) / s.width;
-  s.a_bytes = (few ? kFewRows : kRowsTile) * 128;
+  s.a_bytes = (uint32_t)min(kRowsTile, (most_rows + kRowsBox - 1) / kRowsBox * kRowsBox) * 128;
   s.stage_bytes = s.a_bytes + s.width * 128 + kSfbBytes;
   s.stages = min(kMaxStages, (int)(((uint32_t)kProductSmem - 1024 - product_fixed_smem(E)) / s.stage_bytes));
   // TMEM: two accumulators, then 2 x 4 columns of the rows' scales and 2 x 4 for
@@ -124,23 +125,42 @@ struct ProductUnit {
   long long row0;
 };
 
-// Unit u, found by a whole warp: the expert whose tiles [pre[e], pre[e+1]) hold
-// row tile mt, first among every (E/32)th expert, then among those between.
-__device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, const int* pre, int u, int n_tiles, int width) {
-  const int lane = threadIdx.x & 31;
-  const int mt = u / n_tiles, step = (p.E + 31) >> 5;
+// A CTA's units in turn: row tile mt and n-tile ni of unit u, u + gridDim.x, ..
+struct ProductCursor {
+  int u, mt, ni, m_step, n_step, n_tiles;
+  __device__ ProductCursor(int n_tiles_) : u(blockIdx.x), n_tiles(n_tiles_) {
+    mt = u / n_tiles;
+    ni = u - mt * n_tiles;
+    m_step = (int)gridDim.x / n_tiles;
+    n_step = (int)gridDim.x - m_step * n_tiles;
+  }
+  __device__ void next() {
+    u += gridDim.x;
+    mt += m_step;
+    ni += n_step;
+    if (ni >= n_tiles) {
+      ni -= n_tiles;
+      ++mt;
+    }
+  }
+};
+
+// Its expert and rows, found by a whole warp: the expert whose tiles [pre[e],
+// pre[e+1]) hold mt, first among every (E/32)th expert, then among those between.
+__device__ __forceinline__ ProductUnit product_unit(const ProductParams& p, const int* pre, const ProductCursor& at, int width) {
+  const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
   const int far = lane * step;
-  const int block = (31 - __clz(__ballot_sync(0xffffffffu, far < p.E && pre[far] <= mt))) * step;
+  const int block = (31 - __clz(__ballot_sync(0xffffffffu, far < p.E && pre[far] <= at.mt))) * step;
   const int near = block + lane;
-  const int e = block + 31 - __clz(__ballot_sync(0xffffffffu, lane < step && near < p.E && pre[near] <= mt));
+  const int e = block + 31 - __clz(__ballot_sync(0xffffffffu, lane < step && near < p.E && pre[near] <= at.mt));
   const int* first = pre + p.E + 1;
   const int* count = first + p.E;
-  const int at = (mt - pre[e]) * kRowsTile;
+  const int before = (at.mt - pre[e]) * kRowsTile;
   ProductUnit x;
   x.e = e;
-  x.n0 = (u - mt * n_tiles) * width;
-  x.rows = min(kRowsTile, count[e] - at);
-  x.row0 = first[e] + at;
+  x.n0 = at.ni * width;
+  x.rows = min(kRowsTile, count[e] - before);
+  x.row0 = first[e] + before;
   return x;
 }
 
@@ -285,17 +305,17 @@ __device__ __forceinline__ void store_results(const ProductParams& p, uint32_t t
     // 8 rows x 64 bytes a store
     const int part = (lane & 3) * 8;
     uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)(row0 + (lane >> 2)) * p.C + c + part;
+    const uint32_t from = turn + (lane >> 2) * kTurnRow + (lane & 3) * 16;
+    int4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (8 * i >= rows) break;
-      if (8 * i + (lane >> 2) < rows && c + part < p.C) {
-        int4 w;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(turn + (8 * i + (lane >> 2)) * kTurnRow + (lane & 3) * 16));
-        st_v4(out + (size_t)(8 * i) * p.C, w);
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "r"(from + i * 8 * kTurnRow));
+    const int mine = c + part < p.C ? rows - (lane >> 2) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (8 * i < mine) st_v4(out + (size_t)(8 * i) * p.C, w[i]);
     __syncwarp();
   } else if (lane < rows) {
     uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)(row0 + lane) * p.C + c;
@@ -333,7 +353,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kProductThreads / 32 - kEpilogueWarp);
+      mbar_init(&acc_empty[i], 4);
     }
     for (int i = 0; i < kScaleWarps * kScaleRing; ++i) mbar_init(&taken[0][i], 1);
     mbar_init(&drained, 1);
@@ -348,7 +368,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   pdl_launch_dependents();
 
   // running row tiles of the experts
-  bool few = true;
+  int most_rows = 0;
   {
     int* first = pre + p.E + 1;
     int* count = first + p.E;
@@ -366,7 +386,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (blockIdx.x == 0) set_error(p.status, MOE_ERR_BAD_ASSIST);
           n = 0;
         }
-        few = few && n <= kFewRows;
+        most_rows = max(most_rows, n);
         first[e] = (int)(e / p.L * p.A) + lo;  // flat rows fit 32 bits
         count[e] = n;
       }
@@ -382,12 +402,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       carry = pre[last] + (count[last] + kRowsTile - 1) / kRowsTile;
     }
   }
+  most_rows = __reduce_max_sync(0xffffffffu, most_rows);
+  if (lane == 0) scan_scratch[warp] = most_rows;
   tc_fence_before();
-  few = __syncthreads_and(few);
+  __syncthreads();
   tc_fence_after();
+  most_rows = (int)(lane < kProductThreads / 32 ? scan_scratch[lane] : 0);
+  most_rows = __reduce_max_sync(0xffffffffu, most_rows);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int m_tiles = __shfl_sync(0xffffffffu, pre[p.E], 0), KB = (p.K + kKStage - 1) / kKStage;
-  const ProductShape shape = product_shape(p.N, p.E, m_tiles, few);
+  const ProductShape shape = product_shape(p.N, p.E, m_tiles, most_rows);
   const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
   const uint32_t stages = __shfl_sync(0xffffffffu, shape.stages, 0), a_bytes = __shfl_sync(0xffffffffu, shape.a_bytes, 0);
   const uint32_t stage_bytes = __shfl_sync(0xffffffffu, shape.stage_bytes, 0), sf_cols = __shfl_sync(0xffffffffu, shape.sf_cols, 0);
@@ -407,12 +431,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
+    for (ProductCursor at(n_tiles); at.u < units && ok; at.next()) {
+      const ProductUnit un = product_unit(p, pre, at, width);
       const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
                 row = __shfl_sync(0xffffffffu, (int)un.row0, 0);
-      const CUtensorMap* mx = rows <= kFewRows ? &maps.x32 : &maps.x128;
-      const uint32_t bytes = ((uint32_t)width + (rows <= kFewRows ? kFewRows : kRowsTile)) * 128u + kSfbBytes;
+      const int a_boxes = (rows + kRowsBox - 1) / kRowsBox;
+      const uint32_t bytes = (uint32_t)(width + a_boxes * kRowsBox) * 128u + kSfbBytes;
       const int sf_row = e * nt128 + (un.n0 >> 7);
       for (int kb = 0; kb < KB; ++kb) {
         ok = __all_sync(0xffffffffu, product_wait(&empty[stage], phase, ab));
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (leader) {
           mbar_arrive_expect_tx(&full[stage], bytes);
           tma_load_3d(st + a_bytes, mw, kb * 128, un.n0, e, bar);
-          tma_load_2d(st, mx, kb * 128, row, bar);
+          for (int b = 0; b < a_boxes; ++b) tma_load_2d(st + b * (kRowsBox * 128), &maps.x, kb * 128, row + b * kRowsBox, bar);
           tma_load_2d(st + a_bytes + width * 128, &maps.wsf, kb * 256, sf_row, bar);
         }
         if (++stage == stages) {
@@ -433,14 +457,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (warp == 1) {
     const uint64_t adesc0 = sw128_desc(sm), bdesc0 = sw128_desc(sm + a_bytes);
     const bool leader = elect_one();
-    const int n_step = (int)gridDim.x % n_tiles;
-    int n_index = (int)blockIdx.x % n_tiles;
     uint32_t stage = 0, phase = 0, done = 0;
     bool ok = true, ready = false;  // the next stage was seen to be there before this one's MMAs went out
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
-      const int n0 = n_index * width, cols = min(width, (p.N - n0 + 63) & ~63);
-      n_index += n_step;
-      if (n_index >= n_tiles) n_index -= n_tiles;
+    for (ProductCursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
+      const int n0 = at.ni * width, cols = min(width, (p.N - n0 + 63) & ~63);
       const uint32_t shift = (n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
       const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * width;
       ok = product_wait(&acc_empty[buf], ((done >> 1) & 1) ^ 1, ab);
@@ -476,14 +496,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t dst0 = smem_u32(my_ring) + lane * 16;
     const uint64_t asf0 = sf_desc(my_ring), bsf0 = sf_desc(sm + a_bytes + width * 128);
     const bool leader = elect_one();
-    int load_u = blockIdx.x, load_kb = 0;
+    ProductCursor load(n_tiles);
+    int load_kb = 0;
     uint32_t load_slot = 0, load_stage = 0;
     bool fresh = true;
     ProductUnit ahead{};
     const auto load_next = [&] {
-      for (bool found = false; !found && load_u < units;) {
+      for (bool found = false; !found && load.u < units;) {
         if ((load_stage & (kScaleWarps - 1)) == mine) {
-          if (fresh) ahead = product_unit(p, pre, load_u, n_tiles, width);
+          if (fresh) ahead = product_unit(p, pre, load, width);
           fresh = false;
           load_row_scales(p, ahead, load_kb, slot0 + load_slot * kScaleStage);
           load_slot = load_slot + 1 == kScaleSlots ? 0 : load_slot + 1;
@@ -492,21 +513,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (++load_stage == stages) load_stage = 0;
         if (++load_kb == KB) {
           load_kb = 0;
-          load_u += gridDim.x;
+          load.next();
           fresh = true;
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int i = 0; i < kScaleSlots - 1; ++i) load_next();
-    const int n_step = (int)gridDim.x % n_tiles;
-    int n_index = (int)blockIdx.x % n_tiles;
-    uint32_t stage = 0, phase = 0, slot = 0, at = 0, taken_phase = 1;
+    uint32_t stage = 0, phase = 0, slot = 0, place = 0, taken_phase = 1;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const int n0 = n_index * width;
-      n_index += n_step;
-      if (n_index >= n_tiles) n_index -= n_tiles;
+    for (ProductCursor at(n_tiles); at.u < units && ok; at.next()) {
+      const int n0 = at.ni * width;
       const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
       for (int kb = 0; kb < KB; ++kb) {
         if ((stage & (kScaleWarps - 1)) == mine) {
@@ -520,11 +537,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                          : "=r"(v[c].x), "=r"(v[c].y)
                          : "r"(slot0 + slot * kScaleStage + c * 256));
           slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-          ok = __all_sync(0xffffffffu, product_wait(&taken[mine][at], taken_phase, ab));
+          ok = __all_sync(0xffffffffu, product_wait(&taken[mine][place], taken_phase, ab));
           if (!ok) break;
           // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
-          const uint32_t dst = dst0 + at * kScaleStage;
-          const uint64_t asf = asf0 + at * (kScaleStage >> 4);
+          const uint32_t dst = dst0 + place * kScaleStage;
+          const uint64_t asf = asf0 + place * (kScaleStage >> 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
                        : "memory");
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(v[0].y), "r"(v[1].y), "r"(v[2].y), "r"(v[3].y)
@@ -546,11 +563,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               else product_scales<1, 2>(ta, b_step, asf, bsf);
             }
             tc_commit(&scaled[stage]);
-            tc_commit(&taken[mine][at]);
+            tc_commit(&taken[mine][place]);
           }
           __syncwarp();
-          if (++at == kScaleRing) {
-            at = 0;
+          if (++place == kScaleRing) {
+            place = 0;
             taken_phase ^= 1;
           }
         }
@@ -562,49 +579,56 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp >= kEpilogueWarp) {
-    const int q = warp & 3, half = (warp - kEpilogueWarp) >> 2;  // quarter q: lanes 32 q ..
+    // quarter q: rows 32 q ..; four warps take the even units, four the odd ones (an
+    // accumulator each): what a unit costs a warp besides its columns, some 650
+    // clocks, then falls to it every other unit
+    const int q = warp & 3;
+    const uint32_t buf = (warp - kEpilogueWarp) >> 2;
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * width;
     const uint32_t my_turn = smem_u32(turn) + (warp - kEpilogueWarp) * kTurnWarp;
     uint32_t done = 0;
-    for (int u = blockIdx.x; u < units && !s_abort; u += gridDim.x, ++done) {
-      const ProductUnit un = product_unit(p, pre, u, n_tiles, width);
-      const uint32_t buf = done & 1;
+    for (ProductCursor at(n_tiles); at.u < units && !s_abort; at.next(), ++done) {
+      if ((done & 1) != buf) continue;
+      const ProductUnit un = product_unit(p, pre, at, width);
       if (!product_wait_warp(&acc_full[buf], (done >> 1) & 1, ab)) break;
       tc_fence_after();
-      const int rows = min(32, un.rows - 32 * q);
-      if (rows > 0) {
-        const long long row0 = un.row0 + 32 * q;
-        const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * width;
-        // 64 columns at a time, the third part by the halves in turn
+      const int rows = min(32, un.rows - 32 * q), parts = rows > 0 ? (min(width, p.N - un.n0) + 63) / 64 : 0;
 #pragma unroll 1
-        for (int g = 0; g < width / 64; ++g) {
-          const int n = un.n0 + g * 64;
-          if ((g == 2 ? (int)(done & 1) : g) != half || n >= p.N) continue;
-          uint32_t v[64];
-          tc_ld64(acc + g * 64, v);
-          tc_wait_ld();
-          float h[32];
-          if (SWIGLU) {
+      for (int g = 0; g < parts; ++g) {  // 64 columns
+        const int n = un.n0 + g * 64;
+        uint32_t v[64];
+        tc_ld64(acc + g * 64, v);
+        tc_wait_ld();
+        if (g + 1 == parts) {
+          // the last part is in registers: the accumulator goes back before it is stored
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        }
+        float h[32];
+        if (SWIGLU) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
-              // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
-              // bits that follows
-              h[j] = __fdividef(a, 1.0f + __expf(-a)) * b;
-            }
-            store_results<YT>(p, my_turn, row0, rows, n / 2, h);
-          } else {
+          for (int j = 0; j < 32; ++j) {
+            const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
+            // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
+            // bits that follows
+            h[j] = __fdividef(a, 1.0f + __expf(-a)) * b;
+          }
+          store_results<YT>(p, my_turn, un.row0 + 32 * q, rows, n / 2, h);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < 2; ++i) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) h[j] = __uint_as_float(v[32 * i + j]);
-              store_results<YT>(p, my_turn, row0, rows, n + 32 * i, h);
-            }
+            for (int j = 0; j < 32; ++j) h[j] = __uint_as_float(v[32 * i + j]);
+            store_results<YT>(p, my_turn, un.row0 + 32 * q, rows, n + 32 * i, h);
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (parts == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      }
     }
   }
 
@@ -710,7 +734,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   const auto map_w = [&](CUtensorMap* m, unsigned box) {
     return product_map(m, w, row_bytes, (unsigned long long)n, (unsigned long long)E, box);
   };
-  if (!product_map(&maps.x32, x, row_bytes, rows, 0, 32) || !product_map(&maps.x128, x, row_bytes, rows, 0, 128) ||
+  if (!product_map(&maps.x, x, row_bytes, rows, 0, kRowsBox) ||
       !scale_map(&maps.wsf, w_scales, (unsigned long long)(k + 127) / 128 * 512, (unsigned long long)E * ((n + 127) / 128)) ||
       !map_w(&maps.w64, 64) || !map_w(&maps.w128, 128) || !map_w(&maps.w192, 192))
     return MOE_ERR_CUDA;
