@@ -1,8 +1,17 @@
 // Routing scores to expert ids and weights (moe_route) and the gradient of the
 // weights (moe_route_backward); include/moe_experts.h has the formulas.
 //
-// One warp a token, its keys and scores in shared memory: softmax statistics,
-// group values and each of the topk argmax steps are warp reductions.
+// One warp a token, a lane holding E / 32 neighbouring experts (rounded up to a power
+// of two) in registers, in one load. Picking the K largest keys one by one costs a
+// warp-wide argmax and a rescan each; instead
+//   * the K-th largest of the 32 lanes' maxima (K times one redux) bounds the K-th
+//     largest key from below, since at least K keys are not below it;
+//   * the keys that reach it, mostly little more than K of them, are listed in shared
+//     memory by ballots, one a lane comes back, and each counts the keys ahead of it
+//     (larger, or equal with a lower index): its rank is its place in the output.
+// More than 32 such keys (ties, large K) are picked one by one. Groups of experts that
+// do not fall on lanes, and more than 512 experts (their keys and scores would not fit
+// the registers), take route_any_kernel, which keeps the row in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -25,17 +34,18 @@ struct RouterParams {
   void* grad_logits;
   long long stride, grad_stride;
   int T, E, K, G, KG, top2, sigmoid, renorm;
+  int vec, vec_out;  // whole lanes at once: E = 32 * EPL and rows aligned for it
   float scaling;
 };
 
 // Keys as unsigned integers that order like the floats: -inf (masked and NaN
 // keys) stays above 0, which stands for an expert that cannot be picked.
 constexpr uint32_t kMaskedKey = 0x007fffffu;
-__device__ __forceinline__ uint32_t ordered_key(float f) {
-  if (f != f) return kMaskedKey;
+__device__ __forceinline__ uint32_t ordered_number(float f) {
   const uint32_t b = __float_as_uint(__fadd_rn(f, 0.f));  // -0 and +0 are equal keys
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t ordered_key(float f) { return f == f ? ordered_number(f) : kMaskedKey; }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
@@ -68,7 +78,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float sigmoid_of(float x) { return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x))); }
+// 1 / (1 + exp(-x)); the reciprocal rounded to nearest is the division's result.
+__device__ __forceinline__ float sigmoid_of(float x) { return __frcp_rn(__fadd_rn(1.f, expf(-x))); }
 
 // The index of the largest key among a lane's best (key, index) pairs, the
 // lowest index among equal keys.
@@ -79,7 +90,7 @@ __device__ __forceinline__ int warp_argmax(uint32_t key, int index, uint32_t* be
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kRouterWarps * 32) route_scores_kernel(RouterParams p) {
+__global__ void __launch_bounds__(kRouterWarps * 32) route_any_kernel(RouterParams p) {
   extern __shared__ uint32_t rsm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* key = rsm + warp * (2 * p.E + p.G);
@@ -178,64 +189,341 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_scores_kernel(RouterP
   }
 }
 
-template <int DT>
+// A lane's EPL neighbouring logits; past the row's end they read as masked.
+template <int DT, int EPL>
+__device__ __forceinline__ void load_lane(const void* row, int E, bool vec, float (&x)[EPL]) {
+  const int e0 = (threadIdx.x & 31) * EPL;
+  constexpr int kBytes = EPL * (DT == MOE_F32 ? 4 : 2);
+  if (vec) {
+    alignas(16) uint32_t w[(kBytes + 3) / 4];
+    const uint8_t* q = static_cast<const uint8_t*>(row) + (size_t)e0 * (DT == MOE_F32 ? 4 : 2);
+    if (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) *reinterpret_cast<int4*>(&w[i * 4]) = ld_nc_v4(q + i * 16);
+    } else if (kBytes == 8) {
+      *reinterpret_cast<uint2*>(&w[0]) = __ldg(reinterpret_cast<const uint2*>(q));
+    } else if (kBytes == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(q));
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if (DT == MOE_F32) x[j] = __uint_as_float(w[j]);
+      else if (DT == MOE_BF16) x[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+      else x[j] = __half2float(__ushort_as_half((uint16_t)(w[j / 2] >> (16 * (j & 1)))));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) x[j] = e0 + j < E ? load_logit<DT>(row, e0 + j) : -INFINITY;
+  }
+}
+
+// A warp's keys and scores by expert, and the candidates among them: index, then key
+// and inverted index (the order of these pairs is the order of the picks).
+template <int EPL>
+struct RouteScratch {
+  uint32_t key[32 * EPL];
+  float score[32 * EPL];
+  unsigned long long order[32];
+  int list[32];
+};
+
+template <int DT, int EPL>
+__global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p) {
+  __shared__ alignas(16) RouteScratch<EPL> scratch[kRouterWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * EPL;
+  const int mine = min(EPL, max(0, p.E - e0));  // experts of this lane
+  RouteScratch<EPL>& sc = scratch[warp];
+  const bool by_score = p.bias || p.top2;
+  pdl_wait();
+  pdl_launch_dependents();
+  float bias[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) bias[j] = p.bias && j < mine ? __ldg(p.bias + e0 + j) : 0.f;
+  for (long long t = (long long)blockIdx.x * kRouterWarps + warp; t < p.T; t += (long long)gridDim.x * kRouterWarps) {
+    float s[EPL];  // logits, then scores (softmax without a score in the key: their numerators)
+    uint32_t key[EPL];
+    load_lane<DT, EPL>(logit_row<DT>(p.logits, t, p.stride), p.E, p.vec, s);
+    float sum = 1.f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = fmaxf(s[j], -INFINITY);  // NaN becomes -inf
+    if (!by_score) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = ordered_number(s[j]);
+    }
+    if (p.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const float x = s[j];
+        s[j] = sigmoid_of(x);  // of -inf: 0
+        if (by_score) {
+          const uint32_t k = ordered_key(__fadd_rn(s[j], bias[j]));
+          key[j] = x == -INFINITY ? kMaskedKey : k;
+        }
+      }
+    } else {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) top = fmaxf(top, s[j]);
+      top = warp_max(top);
+      sum = 0.f;
+      uint32_t masked = 0;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        masked |= (s[j] == -INFINITY ? 1u : 0u) << j;
+        // exp(-inf) is 0; a row without experts and +inf leave no number in the difference
+        const float d = __fsub_rn(s[j], top);
+        s[j] = d == d ? expf(d) : s[j] == top && top > 0.f ? 1.f : 0.f;
+        sum = __fadd_rn(sum, s[j]);
+      }
+      sum = warp_sum(sum);
+      if (by_score) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          s[j] = sum > 0.f ? __fdiv_rn(s[j], sum) : 0.f;
+          const uint32_t k = ordered_key(__fadd_rn(s[j], bias[j]));
+          key[j] = masked >> j & 1 ? kMaskedKey : k;
+        }
+        sum = 1.f;
+      }
+    }
+    if (!p.vec) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (j >= mine) key[j] = 0;  // past the last expert: not to be picked
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
+    if (p.G > 1) {
+      // 32 / G lanes a group
+      uint32_t second = 0;
+      if (p.top2) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          second = max(second, min(a, key[j]));
+          a = max(a, key[j]);
+        }
+      }
+      uint32_t value = best;
+      for (int o = 16 / p.G; o; o >>= 1) {
+        const uint32_t v = __shfl_xor_sync(kAll, value, o), w = __shfl_xor_sync(kAll, second, o);
+        second = max(max(second, w), min(value, v));
+        value = max(value, v);
+      }
+      if (p.top2 && second > kMaskedKey) value = ordered_key(__fadd_rn(key_value(value), key_value(second)));
+      const uint32_t group = (uint32_t)lane & ~(uint32_t)(32 / p.G - 1);  // its first lane
+      bool open = false;
+      for (int i = 0; i < p.KG; ++i) {
+        const uint32_t m = __reduce_max_sync(kAll, value);
+        if (group == (uint32_t)(__ffs(__ballot_sync(kAll, value == m)) - 1)) {
+          open = true;
+          value = 0;
+        }
+      }
+      if (!open) {
+        best = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = 0;
+      }
+    }
+    uint32_t bound = 1, live = best;
+    for (int k = 0; k < p.K; ++k) {
+      const uint32_t m = __reduce_max_sync(kAll, live);
+      bound = max(m, 1u);  // 0: fewer lanes than picks; then every key that may be picked
+      if (m == 0) break;
+      if (live == m) live = 0;
+    }
+    uint32_t in = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) in |= (key[j] >= bound ? 1u : 0u) << j;
+    // keys and scores to shared memory, candidates' indexes listed a round a lane's next one
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) {
+      if (EPL >= 4) {
+        *reinterpret_cast<uint4*>(&sc.key[e0 + j]) = make_uint4(key[j], key[(j + 1) % EPL], key[(j + 2) % EPL], key[(j + 3) % EPL]);
+        *reinterpret_cast<float4*>(&sc.score[e0 + j]) = make_float4(s[j], s[(j + 1) % EPL], s[(j + 2) % EPL], s[(j + 3) % EPL]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) sc.key[e0 + i] = key[i], sc.score[e0 + i] = s[i];
+      }
+    }
+    int count = 0;
+    for (uint32_t who; (who = __ballot_sync(kAll, in != 0)) != 0 && count <= 32;) {
+      const int at = count + __popc(who & lanemask_lt());
+      if (in && at < 32) sc.list[at] = e0 + __ffs(in) - 1;
+      in &= in - 1;
+      count += __popc(who);
+    }
+    __syncwarp();
+    int rank = 32, id = 0;
+    float score = 0.f;
+    if (count <= 32) {
+      unsigned long long own = 0;
+      if (lane < count) {
+        id = sc.list[lane];
+        score = sc.score[id];
+        own = ((unsigned long long)sc.key[id] << 32) | (uint32_t)~id;
+      }
+      sc.order[lane] = own;
+      __syncwarp();
+      rank = 0;
+      for (int i = 0; i < count; i += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sc.order[i]);
+        rank += (o.x > own) + (o.y > own);
+      }
+      if (lane >= count) rank = 32;
+    } else {
+      for (int k = 0; k < p.K; ++k) {
+        uint32_t b = 0, m;
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if (key[j] > b) b = key[j], at = e0 + j;
+        const int e = warp_argmax(b, at, &m);
+        if (lane == k) rank = k, id = e, score = sc.score[e];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if (e0 + j == e) key[j] = 0;
+      }
+    }
+    __syncwarp();
+    const bool picked = rank < p.K;
+    if (!p.sigmoid && !by_score) score = sum > 0.f ? __fdiv_rn(score, sum) : 0.f;
+    float w = score;
+    if (p.renorm) {
+      const float total = warp_sum(picked ? score : 0.f);
+      w = total > 0.f ? __fdiv_rn(score, total) : 0.f;
+    }
+    if (picked) {
+      p.ids[t * p.K + rank] = id;
+      p.weights[t * p.K + rank] = __fmul_rn(w, p.scaling);
+    }
+  }
+}
+
+// A lane's EPL neighbouring gradients.
+template <int DT, int EPL>
+__device__ __forceinline__ void store_lane(void* row, int E, bool vec, const float (&x)[EPL]) {
+  const int e0 = (threadIdx.x & 31) * EPL;
+  constexpr int kBytes = EPL * (DT == MOE_F32 ? 4 : 2);
+  if (vec) {
+    alignas(16) uint32_t w[(kBytes + 3) / 4] = {};
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if (DT == MOE_F32) w[j] = __float_as_uint(x[j]);
+      else if (DT == MOE_BF16) w[j / 2] |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[j])) << (16 * (j & 1));
+      else w[j / 2] |= (uint32_t)__half_as_ushort(__float2half_rn(x[j])) << (16 * (j & 1));
+    }
+    uint8_t* q = static_cast<uint8_t*>(row) + (size_t)e0 * (DT == MOE_F32 ? 4 : 2);
+    if (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) st_v4(q + i * 16, *reinterpret_cast<int4*>(&w[i * 4]));
+    } else if (kBytes == 8) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[kBytes == 8 ? 1 : 0]);
+    } else if (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(q) = w[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(q) = (uint16_t)w[0];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (e0 + j < E) store_logit<DT>(row, e0 + j, x[j]);
+  }
+}
+
+// The gradient: a warp writes a token's whole row (zeros, or the softmax's share in
+// every expert), then the lanes that hold its picks write theirs over it. Bound by
+// the row's bytes: each logit is read once at most, each gradient written once.
+template <int DT, int EPL>
 __global__ void __launch_bounds__(kRouterWarps * 32) route_grad_kernel(RouterParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  for (long long t = (long long)blockIdx.x * kRouterWarps + warp; t < p.T; t += (long long)gridDim.x * kRouterWarps) {
-    const void* row = logit_row<DT>(p.logits, t, p.stride);
+  const bool dense = !p.sigmoid && !p.renorm;
+  const long long step = (long long)gridDim.x * kRouterWarps;
+  // a token's row, picks and their gradients are loaded while the one before is worked
+  // on, its chosen logits at the end of that
+  long long t = (long long)blockIdx.x * kRouterWarps + warp;
+  float ahead[EPL];
+  int id_ahead = -1;
+  float g_ahead = 0.f, raw_ahead = -INFINITY;
+  const auto load = [&](long long k) {
+    if (k >= p.T) return;
+    if (dense) load_lane<DT, EPL>(logit_row<DT>(p.logits, k, p.stride), p.E, p.vec, ahead);
+    if (lane < p.K) {
+      id_ahead = __ldg(p.ids_in + k * p.K + lane);
+      g_ahead = __ldg(p.grad + k * p.K + lane);
+    }
+  };
+  const auto load_chosen = [&](long long k) {
+    if (k < p.T && (unsigned)id_ahead < (unsigned)p.E) raw_ahead = load_logit<DT>(logit_row<DT>(p.logits, k, p.stride), id_ahead);
+  };
+  load(t);
+  load_chosen(t);
+  for (; t < p.T; t += step) {
     uint8_t* out = static_cast<uint8_t*>(p.grad_logits) + t * p.grad_stride * (DT == MOE_F32 ? 4 : 2);
-    int id = lane < p.K ? p.ids_in[t * p.K + lane] : -1;
-    if (id >= p.E) id = -1;
-    const float g = id >= 0 ? __fmul_rn(p.grad[t * p.K + lane], p.scaling) : 0.f;
-    const float raw = id >= 0 ? load_logit<DT>(row, id) : -INFINITY;
-    const float x = raw == raw ? raw : -INFINITY;
-    float top = -INFINITY, sum = 0.f, d = 0.f;
+    float v[EPL];
+    if (dense) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) v[j] = ahead[j];
+    }
+    const int id = lane < p.K && (unsigned)id_ahead < (unsigned)p.E ? id_ahead : -1;
+    const float g = id >= 0 ? __fmul_rn(g_ahead, p.scaling) : 0.f;
+    const float x = id >= 0 ? fmaxf(raw_ahead, -INFINITY) : -INFINITY;  // NaN becomes -inf
+    load(t + step);
+    float d;
     if (p.sigmoid) {
-      const float s = x == -INFINITY ? 0.f : sigmoid_of(x);
-      const float other = x == -INFINITY ? 1.f : sigmoid_of(-x);  // 1 - s without the cancellation near s = 1
+      const float s = sigmoid_of(x), other = sigmoid_of(-x);  // 1 - s without the cancellation near s = 1
       if (p.renorm) {
         const float total = warp_sum(s);
         const float r = total > 0.f ? __fdiv_rn(s, total) : 0.f;
-        const float mean = warp_sum(g * r);
-        d = r * (g - mean) * other;
+        d = r * (g - warp_sum(g * r)) * other;
       } else {
         d = g * s * other;
       }
     } else {
       // the chosen logits alone when renormalised, else the whole row
-      if (p.renorm) {
-        top = warp_max(x);
-      } else {
-        for (int e = lane; e < p.E; e += 32) {
-          const float v = load_logit<DT>(row, e);
-          top = fmaxf(top, v);
+      float top = x, sum = 0.f;
+      if (dense) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          v[j] = fmaxf(v[j], -INFINITY);
+          top = fmaxf(top, v[j]);
         }
-        top = warp_max(top);
-        for (int e = lane; e < p.E; e += 32) {
-          const float v = load_logit<DT>(row, e);
-          sum += v == -INFINITY || v != v ? 0.f : v == top ? 1.f : expf(v - top);
-        }
-        sum = warp_sum(sum);
       }
-      const float v = x == -INFINITY ? 0.f : x == top ? 1.f : expf(x - top);
-      if (p.renorm) sum = warp_sum(v);
-      const float r = sum > 0.f ? __fdiv_rn(v, sum) : 0.f;
+      top = warp_max(top);
+      const float mine = x == -INFINITY ? 0.f : x == top ? 1.f : expf(x - top);
+      if (dense) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          v[j] = v[j] == -INFINITY ? 0.f : v[j] == top ? 1.f : expf(v[j] - top);
+          sum += v[j];
+        }
+      } else {
+        sum = mine;
+      }
+      sum = warp_sum(sum);
+      const float r = sum > 0.f ? __fdiv_rn(mine, sum) : 0.f;
       const float mean = warp_sum(g * r);
       d = r * (g - mean);
-      if (!p.renorm) {
-        for (int e = lane; e < p.E; e += 32) {
-          const float l = load_logit<DT>(row, e);
-          const float ve = l == -INFINITY || l != l ? 0.f : l == top ? 1.f : expf(l - top);
-          store_logit<DT>(out, e, sum > 0.f ? -mean * __fdiv_rn(ve, sum) : 0.f);
-        }
+      if (dense) {
+        const float share = sum > 0.f ? -__fdiv_rn(mean, sum) : 0.f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) v[j] *= share;
       }
     }
-    if (p.sigmoid || p.renorm)
-      for (int e = lane; e < p.E; e += 32) store_logit<DT>(out, e, 0.f);
+    if (!dense) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) v[j] = 0.f;
+    }
+    store_lane<DT, EPL>(out, p.E, p.vec_out, v);
     __syncwarp();
     if (id >= 0) store_logit<DT>(out, id, d);
+    load_chosen(t + step);
   }
 }
 
@@ -276,6 +564,41 @@ RouterParams params_of(const moe_router_config_t* c) {
 
 typedef void (*RouterKernel)(RouterParams);
 
+// Experts a lane: the least power of two that 32 lanes cover E with.
+int lane_experts(int E) {
+  int n = 1;
+  while (32 * n < E) n *= 2;
+  return n;
+}
+
+template <int DT>
+RouterKernel route_of(int epl) {
+  switch (epl) {
+    case 1: return route_kernel<DT, 1>;
+    case 2: return route_kernel<DT, 2>;
+    case 4: return route_kernel<DT, 4>;
+    case 8: return route_kernel<DT, 8>;
+    default: return route_kernel<DT, 16>;
+  }
+}
+template <int DT>
+RouterKernel route_grad_of(int epl) {
+  switch (epl) {
+    case 1: return route_grad_kernel<DT, 1>;
+    case 2: return route_grad_kernel<DT, 2>;
+    case 4: return route_grad_kernel<DT, 4>;
+    case 8: return route_grad_kernel<DT, 8>;
+    case 16: return route_grad_kernel<DT, 16>;
+    default: return route_grad_kernel<DT, 32>;
+  }
+}
+
+// Whether a lane's EPL elements load or store at once.
+bool whole_lanes(const void* base, int64_t stride, int E, int epl, int es) {
+  const size_t bytes = (size_t)epl * es, align = bytes < 16 ? bytes : 16;
+  return E == 32 * epl && aligned_to(base, align) && (size_t)stride * es % align == 0;
+}
+
 moe_status_t launch(RouterKernel kernel, const RouterParams& p, size_t smem, void* stream) {
   const int nsm = num_sms_of_current_device();
   int per_sm = 0;
@@ -307,11 +630,20 @@ extern "C" moe_status_t moe_route(const moe_router_config_t* rc, const void* log
   p.bias = bias;
   p.ids = expert_ids;
   p.weights = expert_scales;
-  const size_t smem = (size_t)kRouterWarps * (2 * p.E + p.G) * 4;
-  return launch(rc->logits_dtype == MOE_F32   ? route_scores_kernel<MOE_F32>
-                : rc->logits_dtype == MOE_F16 ? route_scores_kernel<MOE_F16>
-                                              : route_scores_kernel<MOE_BF16>,
-                p, smem, stream);
+  const int epl = lane_experts(p.E);
+  p.vec = whole_lanes(logits, p.stride, p.E, epl, (int)es);
+  // over 512 experts, or groups that do not fall on lanes
+  if (epl > 16 || (p.G > 1 && (p.E != 32 * epl || 32 % p.G))) {
+    const size_t smem = (size_t)kRouterWarps * (2 * p.E + p.G) * 4;
+    return launch(rc->logits_dtype == MOE_F32   ? route_any_kernel<MOE_F32>
+                  : rc->logits_dtype == MOE_F16 ? route_any_kernel<MOE_F16>
+                                                : route_any_kernel<MOE_BF16>,
+                  p, smem, stream);
+  }
+  return launch(rc->logits_dtype == MOE_F32   ? route_of<MOE_F32>(epl)
+                : rc->logits_dtype == MOE_F16 ? route_of<MOE_F16>(epl)
+                                              : route_of<MOE_BF16>(epl),
+                p, 0, stream);
 }
 
 extern "C" moe_status_t moe_route_backward(const moe_router_config_t* rc, const void* logits,
@@ -333,8 +665,11 @@ extern "C" moe_status_t moe_route_backward(const moe_router_config_t* rc, const 
   p.grad = grad_scales;
   p.grad_logits = grad_logits;
   p.grad_stride = grad_stride;
-  return launch(rc->logits_dtype == MOE_F32   ? route_grad_kernel<MOE_F32>
-                : rc->logits_dtype == MOE_F16 ? route_grad_kernel<MOE_F16>
-                                              : route_grad_kernel<MOE_BF16>,
+  const int epl = lane_experts(p.E);
+  p.vec = whole_lanes(logits, p.stride, p.E, epl, (int)es);
+  p.vec_out = whole_lanes(grad_logits, grad_stride, p.E, epl, (int)es);
+  return launch(rc->logits_dtype == MOE_F32   ? route_grad_of<MOE_F32>(epl)
+                : rc->logits_dtype == MOE_F16 ? route_grad_of<MOE_F16>(epl)
+                                              : route_grad_of<MOE_BF16>(epl),
                 p, 0, stream);
 }
