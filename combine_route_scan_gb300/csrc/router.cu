@@ -2,16 +2,21 @@
 // weights (moe_route_backward); include/moe_experts.h has the formulas.
 //
 // One warp a token, a lane holding E / 32 neighbouring experts (rounded up to a power
-// of two) in registers, in one load. Picking the K largest keys one by one costs a
-// warp-wide argmax and a rescan each; instead
-//   * the K-th largest of the 32 lanes' maxima (K times one redux) bounds the K-th
-//     largest key from below, since at least K keys are not below it;
+// of two) in registers, in one load; bound by instructions. The keys of all experts
+// are needed, the weights of the picks alone: keys come from the fast exponential and
+// reciprocal (within 2^-21 of the formula; equal logits and biases give equal keys),
+// and the lanes that end up with a pick compute its weight with expf and IEEE
+// division. Picking the K largest keys one by one costs a warp-wide argmax and a
+// rescan each (73 us where this takes 57, 65521 tokens x 256 experts); instead
+//   * the K-th largest of the 32 lanes' maxima, or a little less, bounds the K-th
+//     largest key from below, since at least K keys are not below it: found by
+//     halving an interval of keys, a ballot a step;
 //   * the keys that reach it, mostly little more than K of them, are listed in shared
 //     memory by ballots, one a lane comes back, and each counts the keys ahead of it
 //     (larger, or equal with a lower index): its rank is its place in the output.
 // More than 32 such keys (ties, large K) are picked one by one. Groups of experts that
-// do not fall on lanes, and more than 512 experts (their keys and scores would not fit
-// the registers), take route_any_kernel, which keeps the row in shared memory.
+// do not fall on lanes, and more than 512 experts (their keys would not fit the
+// registers), take route_any_kernel, which keeps the row in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -219,12 +224,16 @@ __device__ __forceinline__ void load_lane(const void* row, int E, bool vec, floa
   }
 }
 
-// A warp's keys and scores by expert, and the candidates among them: index, then key
+// Steps that narrow the bound: the first halves a range of keys that a few score
+// values span, so that it ends at the K-th lane, or one or two candidates early.
+constexpr int kBoundSteps = 12;
+
+// A warp's keys and logits by expert, and the candidates among them: index, then key
 // and inverted index (the order of these pairs is the order of the picks).
 template <int EPL>
 struct RouteScratch {
   uint32_t key[32 * EPL];
-  float score[32 * EPL];
+  float x[32 * EPL];
   unsigned long long order[32];
   int list[32];
 };
@@ -242,50 +251,43 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
 #pragma unroll
   for (int j = 0; j < EPL; ++j) bias[j] = p.bias && j < mine ? __ldg(p.bias + e0 + j) : 0.f;
   for (long long t = (long long)blockIdx.x * kRouterWarps + warp; t < p.T; t += (long long)gridDim.x * kRouterWarps) {
-    float s[EPL];  // logits, then scores (softmax without a score in the key: their numerators)
+    float x[EPL];
     uint32_t key[EPL];
-    load_lane<DT, EPL>(logit_row<DT>(p.logits, t, p.stride), p.E, p.vec, s);
-    float sum = 1.f;
+    load_lane<DT, EPL>(logit_row<DT>(p.logits, t, p.stride), p.E, p.vec, x);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = fmaxf(s[j], -INFINITY);  // NaN becomes -inf
+    for (int j = 0; j < EPL; ++j) x[j] = fmaxf(x[j], -INFINITY);  // NaN becomes -inf
+    float top = -INFINITY, sum = 1.f;
     if (!by_score) {
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) key[j] = ordered_number(s[j]);
+      for (int j = 0; j < EPL; ++j) key[j] = ordered_number(x[j]);
     }
     if (p.sigmoid) {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        const float x = s[j];
-        s[j] = sigmoid_of(x);  // of -inf: 0
-        if (by_score) {
-          const uint32_t k = ordered_key(__fadd_rn(s[j], bias[j]));
-          key[j] = x == -INFINITY ? kMaskedKey : k;
-        }
-      }
-    } else {
-      float top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) top = fmaxf(top, s[j]);
-      top = warp_max(top);
-      sum = 0.f;
-      uint32_t masked = 0;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        masked |= (s[j] == -INFINITY ? 1u : 0u) << j;
-        // exp(-inf) is 0; a row without experts and +inf leave no number in the difference
-        const float d = __fsub_rn(s[j], top);
-        s[j] = d == d ? expf(d) : s[j] == top && top > 0.f ? 1.f : 0.f;
-        sum = __fadd_rn(sum, s[j]);
-      }
-      sum = warp_sum(sum);
       if (by_score) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-          s[j] = sum > 0.f ? __fdiv_rn(s[j], sum) : 0.f;
-          const uint32_t k = ordered_key(__fadd_rn(s[j], bias[j]));
-          key[j] = masked >> j & 1 ? kMaskedKey : k;
+          const float s = __fdividef(1.f, 1.f + __expf(-x[j]));
+          key[j] = x[j] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(s, bias[j]));
         }
-        sum = 1.f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) top = fmaxf(top, x[j]);
+      top = warp_max(top);
+      sum = 0.f;
+      float v[EPL];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        // exp(-inf) is 0; a row without experts and +inf leave no number in the difference
+        const float d = __fsub_rn(x[j], top);
+        v[j] = d == d ? expf(d) : top > 0.f ? 1.f : 0.f;
+        sum = __fadd_rn(sum, v[j]);
+      }
+      sum = warp_sum(sum);
+      if (by_score) {
+        const float share = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          key[j] = x[j] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(__fmul_rn(v[j], share), bias[j]));
       }
     }
     if (!p.vec) {
@@ -329,25 +331,31 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
         for (int j = 0; j < EPL; ++j) key[j] = 0;
       }
     }
-    uint32_t bound = 1, live = best;
-    for (int k = 0; k < p.K; ++k) {
-      const uint32_t m = __reduce_max_sync(kAll, live);
-      bound = max(m, 1u);  // 0: fewer lanes than picks; then every key that may be picked
-      if (m == 0) break;
-      if (live == m) live = 0;
+    uint32_t bound = 1;  // fewer lanes than picks: every key that may be picked
+    if (__popc(__ballot_sync(kAll, best != 0)) >= p.K) {
+      uint32_t high = __reduce_max_sync(kAll, best), low = __reduce_min_sync(kAll, best ? best : 0xffffffffu);
+      bound = low;  // reached by K lanes and more; high by fewer, or itself the bound
+      for (int i = 0; i < kBoundSteps && low < high; ++i) {
+        const uint32_t mid = low + (high - low) / 2 + 1;
+        const int reach = __popc(__ballot_sync(kAll, best >= mid));
+        if (reach >= p.K) low = mid;
+        else high = mid - 1;
+        if (reach == p.K) break;
+      }
+      bound = low;
     }
     uint32_t in = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) in |= (key[j] >= bound ? 1u : 0u) << j;
-    // keys and scores to shared memory, candidates' indexes listed a round a lane's next one
+    // keys and logits to shared memory, candidates' indexes listed a round a lane's next one
 #pragma unroll
     for (int j = 0; j < EPL; j += 4) {
       if (EPL >= 4) {
         *reinterpret_cast<uint4*>(&sc.key[e0 + j]) = make_uint4(key[j], key[(j + 1) % EPL], key[(j + 2) % EPL], key[(j + 3) % EPL]);
-        *reinterpret_cast<float4*>(&sc.score[e0 + j]) = make_float4(s[j], s[(j + 1) % EPL], s[(j + 2) % EPL], s[(j + 3) % EPL]);
+        *reinterpret_cast<float4*>(&sc.x[e0 + j]) = make_float4(x[j], x[(j + 1) % EPL], x[(j + 2) % EPL], x[(j + 3) % EPL]);
       } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) sc.key[e0 + i] = key[i], sc.score[e0 + i] = s[i];
+        for (int i = 0; i < EPL; ++i) sc.key[e0 + i] = key[i], sc.x[e0 + i] = x[i];
       }
     }
     int count = 0;
@@ -359,12 +367,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
     }
     __syncwarp();
     int rank = 32, id = 0;
-    float score = 0.f;
     if (count <= 32) {
       unsigned long long own = 0;
       if (lane < count) {
         id = sc.list[lane];
-        score = sc.score[id];
         own = ((unsigned long long)sc.key[id] << 32) | (uint32_t)~id;
       }
       sc.order[lane] = own;
@@ -383,15 +389,22 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
         for (int j = 0; j < EPL; ++j)
           if (key[j] > b) b = key[j], at = e0 + j;
         const int e = warp_argmax(b, at, &m);
-        if (lane == k) rank = k, id = e, score = sc.score[e];
+        if (lane == k) rank = k, id = e;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
           if (e0 + j == e) key[j] = 0;
       }
     }
-    __syncwarp();
     const bool picked = rank < p.K;
-    if (!p.sigmoid && !by_score) score = sum > 0.f ? __fdiv_rn(score, sum) : 0.f;
+    const float at = sc.x[id];
+    __syncwarp();
+    float score;
+    if (p.sigmoid) {
+      score = sigmoid_of(at);  // of -inf: 0
+    } else {
+      const float d = __fsub_rn(at, top);
+      score = sum > 0.f ? __fdiv_rn(d == d ? expf(d) : top > 0.f ? 1.f : 0.f, sum) : 0.f;
+    }
     float w = score;
     if (p.renorm) {
       const float total = warp_sum(picked ? score : 0.f);

@@ -64,8 +64,9 @@ typedef struct {
  *   bias          NULL or [E] fp32; it moves the choice, not the weights
  *   expert_ids    [T][K] int32 (moe_dispatch's expert_ids, with T = W * bs)
  *   expert_scales [T][K] fp32  (moe_dispatch's and moe_combine's expert_scales)
- * Ordering by the logits matters where scores round to the same number; scores
- * are computed by expf and IEEE division, without approximate instructions. */
+ * Weights are computed in fp32 with expf and IEEE division. Keys that hold scores
+ * are within 2^-21 of the formula's (experts of equal logit and bias have equal
+ * keys): experts whose keys are nearer than that may be chosen either way. */
 moe_status_t moe_route(const moe_router_config_t* rc, const void* logits, const float* bias, int32_t* expert_ids,
                        float* expert_scales, void* stream);
 
