@@ -46,6 +46,7 @@ NOALLOC_MAX_PICKS = 262144
 
 MOE_F32, MOE_MXFP4 = 3, 4
 FLOAT_CODE = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
+FLOAT_TYPE = {code: dtype for dtype, code in FLOAT_CODE.items()}
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2_SUM = 0, 1
 SF_ROWS, SF_TILED = 0, 1
@@ -156,10 +157,18 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# torch.cuda.current_stream() builds a Stream object, 3 us of every call; these give its handle
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    """The stream's handle; None is the current stream of the current device."""
     if stream is None:
+        if _current_raw_stream is not None and torch.cuda.is_initialized():
+            return _current_raw_stream(_current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(code: int, what: str):
@@ -257,23 +266,26 @@ def combine_noalloc(cfg: MoeConfig, expert_out, assist_info, ep_recv_count, expe
                                      _ptr(x_out), _ptr(status), _stream(stream)), "moe_combine_noalloc")
 
 
-def _rows_ptr(t: torch.Tensor, rows: int, cols: int, stride: int, what: str):
+def _rows_ptr(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, stride: int, what: str):
     """Address of a tensor of `rows` contiguous rows of `cols` elements, `stride` apart."""
     if t.is_contiguous():
-        ok = rows < 2 or stride == cols
+        ok = stride == cols or rows < 2
     else:
         ok = t.dim() == 2 and t.stride(1) == 1 and (t.stride(0) == stride or rows < 2)
-    if not ok or t.dim() < 1 or t.shape[-1] != cols or t.numel() != rows * cols:
-        raise ValueError(f"{what}: expected {rows} contiguous rows of {cols} elements, {stride} apart")
+    if not ok or t.dtype is not dtype or t.numel() != rows * cols or (t.shape[-1] if t.dim() else 0) != cols:
+        raise ValueError(f"{what}: expected {rows} contiguous rows of {cols} elements of {dtype}, {stride} apart")
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
     return t.data_ptr()
 
 
 def _typed_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, n: int, what: str):
-    if t is not None and (t.dtype != dtype or t.numel() != n):
-        raise ValueError(f"{what}: expected {n} elements of {dtype}")
-    return _ptr(t)
+    """Address of a contiguous CUDA tensor of n elements of dtype (None: of none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: expected {n} contiguous elements of {dtype} on the GPU")
+    return t.data_ptr()
 
 
 def route(rc: RouterConfig, logits, bias, expert_ids, expert_scales, stream=None):
@@ -281,9 +293,7 @@ def route(rc: RouterConfig, logits, bias, expert_ids, expert_scales, stream=None
     fp32 [E] -> expert_ids int32 and expert_scales fp32 [tokens, K], as dispatch
     and combine take them (with any leading axes, such as [W, bs, K])."""
     T, E, K = rc.tokens, rc.expert_num, rc.topk
-    if FLOAT_CODE.get(logits.dtype) != rc.logits_dtype:
-        raise ValueError("logits: not of the configuration's type")
-    _check(lib().moe_route(ctypes.byref(rc), _rows_ptr(logits, T, E, rc.logits_stride, "logits"),
+    _check(lib().moe_route(ctypes.byref(rc), _rows_ptr(logits, FLOAT_TYPE.get(rc.logits_dtype), T, E, rc.logits_stride, "logits"),
                            _typed_ptr(bias, torch.float32, E, "bias"),
                            _typed_ptr(expert_ids, torch.int32, T * K, "expert_ids"),
                            _typed_ptr(expert_scales, torch.float32, T * K, "expert_scales"), _stream(stream)),
@@ -294,13 +304,12 @@ def route_backward(rc: RouterConfig, logits, expert_ids, grad_scales, grad_logit
     """moe_route_backward: the gradient of route's weights, written to
     grad_logits (of the logits' shape and type; its rows may be strided)."""
     T, E, K = rc.tokens, rc.expert_num, rc.topk
-    if FLOAT_CODE.get(logits.dtype) != rc.logits_dtype or grad_logits.dtype != logits.dtype:
-        raise ValueError("logits, grad_logits: not of the configuration's type")
-    gs = grad_logits.stride(-2) if grad_logits.dim() == 2 and grad_logits.shape[0] > 1 else E
-    _check(lib().moe_route_backward(ctypes.byref(rc), _rows_ptr(logits, T, E, rc.logits_stride, "logits"),
+    dtype = FLOAT_TYPE.get(rc.logits_dtype)
+    gs = E if grad_logits.is_contiguous() or T < 2 else grad_logits.stride(0)
+    _check(lib().moe_route_backward(ctypes.byref(rc), _rows_ptr(logits, dtype, T, E, rc.logits_stride, "logits"),
                                     _typed_ptr(expert_ids, torch.int32, T * K, "expert_ids"),
                                     _typed_ptr(grad_scales, torch.float32, T * K, "grad_scales"),
-                                    _rows_ptr(grad_logits, T, E, gs, "grad_logits"), gs, _stream(stream)),
+                                    _rows_ptr(grad_logits, dtype, T, E, gs, "grad_logits"), gs, _stream(stream)),
            "moe_route_backward")
 
 
@@ -312,16 +321,20 @@ def mx_quantize(x, codes, scales, layout: int = SF_ROWS, stream=None):
     """moe_mx_quantize: x [rows, cols] or [experts, rows, cols] (contiguous
     rows, any strides between them) -> codes uint8 [..., cols / 2] and scales
     uint8 (alloc_mx sizes both)."""
-    if x.dim() not in (2, 3) or x.dtype not in FLOAT_CODE or not x.is_cuda:
+    shape, dt = x.shape, FLOAT_CODE.get(x.dtype)
+    if len(shape) not in (2, 3) or dt is None or not x.is_cuda:
         raise ValueError("x: expected a 2D or 3D CUDA tensor of float32, float16 or bfloat16")
-    E, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
-    if cols > 1 and x.stride(-1) != 1:
+    rows, cols = shape[-2:]
+    E = shape[0] if len(shape) == 3 else 1
+    stride = x.stride()
+    if cols > 1 and stride[-1] != 1:
         raise ValueError("x: expected contiguous rows")
-    rs = x.stride(-2) if rows > 1 else cols
-    _check(lib().moe_mx_quantize(x.data_ptr(), FLOAT_CODE[x.dtype], E, rows, cols, rs, x.stride(0) if x.dim() == 3 else 0,
-                                 layout, _typed_ptr(codes, torch.uint8, E * rows * (cols // 2), "codes"),
-                                 _typed_ptr(scales, torch.uint8, mx_scale_bytes(E, rows, cols, layout), "scales"),
-                                 _stream(stream)), "moe_mx_quantize")
+    blocks = -(-cols // 32)
+    scale_bytes = E * rows * blocks if layout == SF_ROWS else E * -(-rows // 128) * -(-blocks // 4) * 512
+    _check(lib().moe_mx_quantize(x.data_ptr(), dt, E, rows, cols, stride[-2] if rows > 1 else cols,
+                                 stride[0] if len(shape) == 3 else 0, layout,
+                                 _typed_ptr(codes, torch.uint8, E * rows * (cols // 2), "codes"),
+                                 _typed_ptr(scales, torch.uint8, scale_bytes, "scales"), _stream(stream)), "moe_mx_quantize")
 
 
 def expert_product(cfg: MoeConfig, x, x_scales, ep_recv_count, w, w_scales, y, y_scales=None,

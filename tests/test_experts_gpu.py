@@ -580,7 +580,7 @@ def test_refusals():
         M.mx_quantize(x, codes, scales[:, :1])
     with pytest.raises(ValueError):
         M.mx_quantize(x.t(), codes, scales)
-    assert code(M.mx_quantize, x[:, :63], codes[:, :31].contiguous(), torch.empty(0, dtype=torch.uint8, device="cuda")) == "INVALID_ARG"
+    assert code(M.mx_quantize, x[:, :63], codes[:, :31].contiguous(), scales) == "INVALID_ARG"  # an odd number of columns
 
     pr = Product(2, 8, 2, [3, 4, 5, 6], 64, 64, seed=2)
     x, xs, ep, wt, wsf = pr.device()
