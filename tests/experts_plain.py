@@ -88,11 +88,12 @@ def route_gradient(logits, ids, grad, sigmoid, renorm, scaling):
 
 def nearest_code(m):
     """E2M1 code of magnitudes m: the nearest value, ties to the even code, saturating."""
-    m = np.minimum(np.asarray(m, dtype=np.float64), 6.0)
-    d = np.abs(m[..., None] - MAGNITUDES)
-    low = d.argmin(-1)  # the lower of two that are equally near
-    tie = np.take_along_axis(d, np.minimum(low + 1, 7)[..., None], -1)[..., 0] == d.min(-1)
-    return (low + (tie & (low % 2 == 1) & (low < 7))).astype(np.uint8)
+    m = np.asarray(m, dtype=np.float64)
+    code = np.zeros(m.shape, dtype=np.uint8)
+    for c in range(7):  # past the middle between codes c and c + 1; the middle itself goes to the even one
+        middle = (MAGNITUDES[c] + MAGNITUDES[c + 1]) / 2
+        code += m >= middle if c % 2 else m > middle
+    return code
 
 
 def quantize(x):

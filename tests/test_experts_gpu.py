@@ -441,6 +441,14 @@ PRODUCT_CASES = [
     (4, 16, 3, [5, 1, 0, 9, 32, 2, 7, 1], 1024, 128, True),
     (2, 4, 1, [4, 4], 96, 7168, True),
     (8, 1, 8, [0] * 15 + [1], 1024, 2048, True),
+    # several units a CTA, with one, two, three and five stages each (the ring's places shift from unit to unit)
+    (2, 75, 2, [150, 5, 140, 129], 8200, 96, False),
+    (2, 75, 2, [150, 5, 140, 129], 8192, 512, True),
+    (2, 75, 2, [150, 5, 140, 129], 8192, 768, True),
+    (2, 75, 2, [150, 5, 140, 129], 4104, 1184, False),
+    # every expert with few rows, many units a CTA
+    (2, 20, 2, [16, 5, 9, 40], 16384, 768, False),
+    (2, 20, 2, [31, 1, 32, 7], 12288, 1280, True),
 ]
 
 
