@@ -27,6 +27,8 @@
 namespace crs {
 
 constexpr int kRouterWarps = 4;
+constexpr int kPairTokens = 4096;  // from here on two tokens a warp
+constexpr int kBoundSteps = 12;    // halvings of the interval that a bound on the picks' keys is sought in
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct RouterParams {
@@ -39,6 +41,7 @@ struct RouterParams {
   void* grad_logits;
   long long stride, grad_stride;
   int T, E, K, G, KG, top2, sigmoid, renorm;
+  int T_step;        // tokens a warp takes at once
   int vec, vec_out;  // whole lanes at once: E = 32 * EPL and rows aligned for it
   float scaling;
 };
@@ -196,8 +199,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_any_kernel(RouterPara
 
 // A lane's EPL neighbouring logits; past the row's end they read as masked.
 template <int DT, int EPL>
-__device__ __forceinline__ void load_lane(const void* row, int E, bool vec, float (&x)[EPL]) {
-  const int e0 = (threadIdx.x & 31) * EPL;
+__device__ __forceinline__ void load_lane(const void* row, int E, bool vec, int lane, float (&x)[EPL]) {
+  const int e0 = lane * EPL;
   constexpr int kBytes = EPL * (DT == MOE_F32 ? 4 : 2);
   if (vec) {
     alignas(16) uint32_t w[(kBytes + 3) / 4];
@@ -224,10 +227,6 @@ __device__ __forceinline__ void load_lane(const void* row, int E, bool vec, floa
   }
 }
 
-// Steps that narrow the bound: the first halves a range of keys that a few score
-// values span, so that it ends at the K-th lane, or one or two candidates early.
-constexpr int kBoundSteps = 12;
-
 // A warp's keys and logits by expert, and the candidates among them: index, then key
 // and inverted index (the order of these pairs is the order of the picks).
 template <int EPL>
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
   for (long long t = (long long)blockIdx.x * kRouterWarps + warp; t < p.T; t += (long long)gridDim.x * kRouterWarps) {
     float x[EPL];
     uint32_t key[EPL];
-    load_lane<DT, EPL>(logit_row<DT>(p.logits, t, p.stride), p.E, p.vec, x);
+    load_lane<DT, EPL>(logit_row<DT>(p.logits, t, p.stride), p.E, p.vec, lane, x);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) x[j] = fmaxf(x[j], -INFINITY);  // NaN becomes -inf
     float top = -INFINITY, sum = 1.f;
@@ -417,6 +416,252 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
   }
 }
 
+// Two tokens a warp, 16 lanes each (E = 16 EPL, K <= 16): what a token costs beside
+// its experts' keys, rather more than half, is then spent once for two. The steps are
+// route_kernel's; where that asks the whole warp, the halves use shuffles within
+// themselves, and ranks by counting in place of repeated maxima. 65521 tokens: 256
+// experts in 8 groups 57 -> 44 us, 128 without groups 44 -> 26 us (64 registers; with
+// the 96 that the compiler would take, 56 us). Below some 4096 tokens there are warps
+// enough for one token each, and those are done sooner.
+// A lane's experts lie kRow words from the next lane's (no bank conflicts).
+template <int EPL>
+struct PairScratch {
+  static constexpr int kRow = EPL >= 8 ? EPL + 4 : EPL;
+  static __device__ __forceinline__ int place(int e) { return e / EPL * kRow + e % EPL; }
+  uint32_t key[2][16 * kRow];
+  float x[2][16 * kRow];
+  unsigned long long order[2][16];
+  int list[2][16];
+};
+
+__device__ __forceinline__ float half_max(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+template <int DT, int EPL>
+__global__ void __launch_bounds__(kRouterWarps * 32, 8) route_pair_kernel(RouterParams p) {
+  __shared__ alignas(16) PairScratch<EPL> scratch[kRouterWarps];
+  using Scratch = PairScratch<EPL>;
+  __shared__ alignas(16) float bias[16 * Scratch::kRow];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, hl = lane & 15, e0 = hl * EPL, s0 = hl * PairScratch<EPL>::kRow;
+  const uint32_t half_lanes = 0xffffu << (16 * half), below = lanemask_lt() & half_lanes;
+  PairScratch<EPL>& sc = scratch[warp];
+  const bool by_score = p.bias || p.top2;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int e = threadIdx.x; e < 16 * EPL; e += kRouterWarps * 32) bias[Scratch::place(e)] = p.bias ? __ldg(p.bias + e) : 0.f;
+  __syncthreads();
+  const bool plenty = 16 * p.KG / p.G >= 2 * p.K;  // open lanes for each pick
+  const long long pairs = ((long long)p.T + 1) / 2;
+  for (long long w = (long long)blockIdx.x * kRouterWarps + warp; w < pairs; w += (long long)gridDim.x * kRouterWarps) {
+    const bool there = 2 * w + half < p.T;  // an odd last token is done twice and stored once
+    const long long t = there ? 2 * w + half : p.T - 1;
+    float x[EPL];
+    uint32_t key[EPL];
+    if (DT == MOE_F32 && EPL == 16) {
+      // 64 bytes a lane: loaded 16 bytes a lane in turn and handed over in shared memory
+      const float* row = static_cast<const float*>(logit_row<DT>(p.logits, t, p.stride));
+      float4 v[EPL / 4];
+#pragma unroll
+      for (int i = 0; i < EPL / 4; ++i) {
+        const int4 w4 = ld_nc_v4(row + i * 64 + hl * 4);
+        v[i] = make_float4(fmaxf(__int_as_float(w4.x), -INFINITY), fmaxf(__int_as_float(w4.y), -INFINITY),
+                           fmaxf(__int_as_float(w4.z), -INFINITY), fmaxf(__int_as_float(w4.w), -INFINITY));
+      }
+#pragma unroll
+      for (int i = 0; i < EPL / 4; ++i) *reinterpret_cast<float4*>(&sc.x[half][Scratch::place(i * 64 + hl * 4)]) = v[i];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < EPL; j += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(&sc.x[half][s0 + j]);
+        x[j] = a.x, x[j + 1] = a.y, x[j + 2] = a.z, x[j + 3] = a.w;
+      }
+    } else {
+      load_lane<DT, EPL>(logit_row<DT>(p.logits, t, p.stride), p.E, true, hl, x);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) x[j] = fmaxf(x[j], -INFINITY);  // NaN becomes -inf
+#pragma unroll
+      for (int j = 0; j < EPL; j += 4) *reinterpret_cast<float4*>(&sc.x[half][s0 + j]) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    }
+    float top = -INFINITY, sum = 1.f;
+    if (!by_score) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) key[j] = ordered_number(x[j]);
+    }
+    if (p.sigmoid) {
+      if (by_score) {
+#pragma unroll
+        for (int j = 0; j < EPL; j += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(&bias[s0 + j]);
+          const float bj[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float s = __fdividef(1.f, 1.f + __expf(-x[j + i]));
+            key[j + i] = x[j + i] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(s, bj[i]));
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) top = fmaxf(top, x[j]);
+      top = half_max(top);
+      sum = 0.f;
+      float v[EPL];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const float d = __fsub_rn(x[j], top);
+        v[j] = d == d ? expf(d) : top > 0.f ? 1.f : 0.f;
+        sum = __fadd_rn(sum, v[j]);
+      }
+      sum = half_sum(sum);
+      if (by_score) {
+        const float share = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          key[j] = x[j] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(__fmul_rn(v[j], share), bias[s0 + j]));
+      }
+    }
+    uint32_t best = 0, next = 0;  // the lane's two largest
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      next = max(next, min(best, key[j]));
+      best = max(best, key[j]);
+    }
+    if (p.G > 1) {
+      // 16 / G lanes a group
+      uint32_t second = next, value = best;
+      const int lanes = 16 / p.G;
+      for (int o = lanes / 2; o; o >>= 1) {
+        const uint32_t v = __shfl_xor_sync(kAll, value, o), w2 = __shfl_xor_sync(kAll, second, o);
+        second = max(max(second, w2), min(value, v));
+        value = max(value, v);
+      }
+      if (p.top2 && second > kMaskedKey) value = ordered_key(__fadd_rn(key_value(value), key_value(second)));
+      int ahead = 0;  // groups that come first
+      for (int o = lanes; o < 16; o += lanes) {
+        const uint32_t v = __shfl_xor_sync(kAll, value, o);
+        ahead += v > value || (v == value && (hl ^ o) < hl);
+      }
+      if (ahead >= p.KG) {
+        best = next = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) key[j] = 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4) *reinterpret_cast<uint4*>(&sc.key[half][s0 + j]) = make_uint4(key[j], key[j + 1], key[j + 2], key[j + 3]);
+    uint32_t bound;
+    if (plenty) {
+      // the least of the K largest lanes' maxima, each lane counting those ahead of its own
+      int ahead = 0;
+#pragma unroll
+      for (int o = 1; o < 16; ++o) ahead += __shfl_xor_sync(kAll, best, o) > best;
+      bound = best && ahead < p.K ? best : 0xffffffffu;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) bound = min(bound, __shfl_xor_sync(kAll, bound, o));
+    } else {
+      // that K of the lanes' two largest reach it, found by halving (the few lanes of the open groups have too
+      // few maxima); 1, and so every open key, where there are fewer
+      uint32_t high = best, low = next ? next : best ? best : 0xffffffffu;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) {
+        high = max(high, __shfl_xor_sync(kAll, high, o));
+        low = min(low, __shfl_xor_sync(kAll, low, o));
+      }
+      const auto reach = [&](uint32_t v) {
+        return __popc(__ballot_sync(kAll, best >= v) & half_lanes) + __popc(__ballot_sync(kAll, next >= v) & half_lanes);
+      };
+      bool going = reach(1) >= p.K;
+      if (!going) low = 1;
+      for (int i = 0; i < kBoundSteps; ++i) {
+        going = going && low < high;
+        if (!__any_sync(kAll, going)) break;
+        const uint32_t mid = low + (high - low) / 2 + 1;
+        const int n = reach(mid);
+        if (going) {
+          if (n >= p.K) low = mid;
+          else high = mid - 1;
+          going = n < p.K || n > p.K + 1;
+        }
+      }
+      bound = low;
+    }
+    uint32_t in = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) in |= (key[j] >= bound ? 1u : 0u) << j;
+    int count = 0;
+    for (uint32_t who; (who = __ballot_sync(kAll, in != 0)) != 0;) {
+      const int at = count + __popc(who & below);
+      if (in && at < 16) sc.list[half][at] = e0 + __ffs(in) - 1;
+      in &= in - 1;
+      count += __popc(who & half_lanes);
+    }
+    __syncwarp();
+    int rank = 16, id = 0;
+    const int most = max(count, __shfl_xor_sync(kAll, count, 16));
+    if (most <= 16) {
+      unsigned long long own = 0;
+      if (hl < count) {
+        id = sc.list[half][hl];
+        own = ((unsigned long long)sc.key[half][Scratch::place(id)] << 32) | (uint32_t)~id;
+      }
+      sc.order[half][hl] = own;
+      __syncwarp();
+      rank = 0;
+      for (int i = 0; i < most; i += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sc.order[half][i]);
+        rank += (o.x > own) + (o.y > own);
+      }
+      if (hl >= count) rank = 16;
+    } else {
+      for (int k = 0; k < p.K; ++k) {
+        unsigned long long b = 0;  // the largest pair of key and inverted index
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const unsigned long long c = ((unsigned long long)key[j] << 32) | (uint32_t) ~(e0 + j);
+          if (key[j] && c > b) b = c;
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+          const unsigned long long c = __shfl_xor_sync(kAll, b, o);
+          if (c > b) b = c;
+        }
+        const int e = (int)~(uint32_t)b;
+        if (hl == k) rank = k, id = e;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if (e0 + j == e) key[j] = 0;
+      }
+    }
+    const bool picked = rank < p.K;
+    const float at = sc.x[half][Scratch::place(id)];
+    __syncwarp();
+    float score;
+    if (p.sigmoid) {
+      score = sigmoid_of(at);  // of -inf: 0
+    } else {
+      const float d = __fsub_rn(at, top);
+      score = sum > 0.f ? __fdiv_rn(d == d ? expf(d) : top > 0.f ? 1.f : 0.f, sum) : 0.f;
+    }
+    float w8 = score;
+    if (p.renorm) {
+      const float total = half_sum(picked ? score : 0.f);
+      w8 = total > 0.f ? __fdiv_rn(score, total) : 0.f;
+    }
+    if (picked && there) {
+      p.ids[t * p.K + rank] = id;
+      p.weights[t * p.K + rank] = __fmul_rn(w8, p.scaling);
+    }
+  }
+}
+
 // A lane's EPL neighbouring gradients.
 template <int DT, int EPL>
 __device__ __forceinline__ void store_lane(void* row, int E, bool vec, const float (&x)[EPL]) {
@@ -466,7 +711,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_grad_kernel(RouterPar
   float g_ahead = 0.f, raw_ahead = -INFINITY;
   const auto load = [&](long long k) {
     if (k >= p.T) return;
-    if (dense) load_lane<DT, EPL>(logit_row<DT>(p.logits, k, p.stride), p.E, p.vec, ahead);
+    if (dense) load_lane<DT, EPL>(logit_row<DT>(p.logits, k, p.stride), p.E, p.vec, lane, ahead);
     if (lane < p.K) {
       id_ahead = __ldg(p.ids_in + k * p.K + lane);
       g_ahead = __ldg(p.grad + k * p.K + lane);
@@ -563,6 +808,7 @@ bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 RouterParams params_of(const moe_router_config_t* c) {
   RouterParams p{};
   p.T = c->tokens;
+  p.T_step = 1;
   p.E = c->expert_num;
   p.K = c->topk;
   p.G = c->group_num;
@@ -595,6 +841,10 @@ RouterKernel route_of(int epl) {
   }
 }
 template <int DT>
+RouterKernel route_pair_of(int epl) {
+  return epl == 4 ? route_pair_kernel<DT, 4> : epl == 8 ? route_pair_kernel<DT, 8> : route_pair_kernel<DT, 16>;
+}
+template <int DT>
 RouterKernel route_grad_of(int epl) {
   switch (epl) {
     case 1: return route_grad_kernel<DT, 1>;
@@ -607,9 +857,9 @@ RouterKernel route_grad_of(int epl) {
 }
 
 // Whether a lane's EPL elements load or store at once.
-bool whole_lanes(const void* base, int64_t stride, int E, int epl, int es) {
+bool whole_lanes(const void* base, int64_t stride, int E, int epl, int es, int lanes = 32) {
   const size_t bytes = (size_t)epl * es, align = bytes < 16 ? bytes : 16;
-  return E == 32 * epl && aligned_to(base, align) && (size_t)stride * es % align == 0;
+  return E == lanes * epl && aligned_to(base, align) && (size_t)stride * es % align == 0;
 }
 
 moe_status_t launch(RouterKernel kernel, const RouterParams& p, size_t smem, void* stream) {
@@ -617,7 +867,8 @@ moe_status_t launch(RouterKernel kernel, const RouterParams& p, size_t smem, voi
   int per_sm = 0;
   if (nsm <= 0 || resident_blocks((const void*)kernel, kRouterWarps * 32, smem, &per_sm) != cudaSuccess || per_sm < 1)
     return MOE_ERR_CUDA;
-  const long long need = ((long long)p.T + kRouterWarps - 1) / kRouterWarps, most = (long long)nsm * per_sm;
+  const int tokens = kRouterWarps * p.T_step;
+  const long long need = ((long long)p.T + tokens - 1) / tokens, most = (long long)nsm * per_sm;
   PdlLaunch L(dim3((unsigned)(need < most ? need : most)), dim3(kRouterWarps * 32), smem,
               static_cast<cudaStream_t>(stream));
   if (cudaLaunchKernelEx(&L.cfg, kernel, p) != cudaSuccess) return MOE_ERR_CUDA;
@@ -645,6 +896,15 @@ extern "C" moe_status_t moe_route(const moe_router_config_t* rc, const void* log
   p.weights = expert_scales;
   const int epl = lane_experts(p.E);
   p.vec = whole_lanes(logits, p.stride, p.E, epl, (int)es);
+  const int pair_epl = 2 * epl;
+  if (p.T >= kPairTokens && p.K <= 16 && pair_epl >= 4 && pair_epl <= 16 && 16 % p.G == 0 &&
+      whole_lanes(logits, p.stride, p.E, pair_epl, (int)es, 16)) {
+    p.T_step = 2;
+    return launch(rc->logits_dtype == MOE_F32   ? route_pair_of<MOE_F32>(pair_epl)
+                  : rc->logits_dtype == MOE_F16 ? route_pair_of<MOE_F16>(pair_epl)
+                                                : route_pair_of<MOE_BF16>(pair_epl),
+                  p, 0, stream);
+  }
   // over 512 experts, or groups that do not fall on lanes
   if (epl > 16 || (p.G > 1 && (p.E != 32 * epl || 32 % p.G))) {
     const size_t smem = (size_t)kRouterWarps * (2 * p.E + p.G) * 4;
