@@ -13,12 +13,13 @@
 //     many boxes of 32 rows of A as the unit has rows for; where every expert has
 //     few rows the stages are that much smaller and more;
 //   * the weights' scales, laid out in the tensor cores' order (MOE_SF_TILED), come
-//     by one more box, 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the
-//     copy engine busy for longer than the codes did); the rows' scales lie a row
+//     in boxes of 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the copy
+//     engine busy for longer than the codes did); the rows' scales lie a row
 //     after the other as dispatch wrote them: a lane brings 8 bytes of its rows
 //     (r, r + 32, ..) by cp.async and stores them in that order; the same warp's
-//     tcgen05.cp takes both to TMEM and tells the MMA warp, which is left with four
-//     MMAs and one commit a stage (what it has to issue bounds a stage);
+//     tcgen05.cp takes both to TMEM, and its commit arrives on the barrier of the
+//     stage's codes, so that the MMA warp is left with one wait, four MMAs and one
+//     commit a stage (what it has to issue bounds a stage);
 //   * warps: 0 TMA, 1 MMA, 2..5 scales, 6..13 epilogue (four for each of the two
 //     accumulators). Two accumulators of 192 columns and the scales fill
 //     TMEM, so that the next unit's MMAs run while this one is read (256 columns
@@ -67,27 +68,29 @@ constexpr int kKStage = 256;                 // elements of K a stage: 128 bytes
 constexpr uint32_t kSfbBytes = 2 * 1024;     // 2 x 128 rows x 8 scales
 // Four warps bring the scales to the tensor cores, each those of every fourth place
 // of the stage ring (a place's barriers have one and the same waiter, which cannot
-// be a round ahead). Each has the rows' scales of kScaleSlots stages under way or
-// landed, and of kScaleRing stages in the tensor cores' order, from which tcgen05.cp
-// takes them (it waits in line behind the MMAs). A warp needs 1200 clocks a stage.
-constexpr int kScaleWarps = 4, kScaleSlots = 3, kScaleRing = 2;
-constexpr uint32_t kScaleStage = 128 * 8;
+// be a round ahead). They have rings of their own, so that a stage's scales are in
+// TMEM when its codes arrive: with them in the stages, a stage's way from its release
+// through copy, tcgen05.cp and their barriers back to the MMA took 2600 clocks, a
+// third of which were the scales'. A slot holds the rows' scales (a lane's 8 bytes
+// of its rows) and the weights'; one stage ahead of the present one is under way.
+constexpr int kScaleWarps = 4, kScaleSlots = 2;
+constexpr uint32_t kScaleStage = 128 * 8, kScaleSlot = kScaleStage + kSfbBytes;
 // An epilogue warp turns 32 rows x 64 bytes around in shared memory before it
 // stores them (rows 80 bytes apart: no bank is hit twice): stored a row a lane, every
 // store touched 32 lines, and the epilogue was what the scale warps waited for.
 constexpr uint32_t kTurnRow = 80, kTurnWarp = 32 * kTurnRow;
 constexpr size_t kProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
 
-// Shared memory behind the stages: row scales in order and under way, the
-// epilogue warps' turning places, running row tiles [E+1], first flat row [E], row count [E].
+// Shared memory behind the stages: row scales in order, scales under way (copies want
+// them on 128 bytes), the epilogue warps' turning places, running row tiles [E+1],
+// first flat row [E], row count [E].
 __host__ __device__ inline uint32_t product_fixed_smem(int E) {
-  return (uint32_t)kScaleWarps * (kScaleRing + kScaleSlots) * kScaleStage + 8 * kTurnWarp + ((3u * E + 1) * 4 + 15) / 16 * 16;
+  static_assert(kProductSmem % 128 == 0 && kScaleSlot % 128 == 0 && kTurnWarp % 128 == 0, "copies' places");
+  return (uint32_t)kScaleWarps * (kScaleStage + kScaleSlots * kScaleSlot) + 8 * kTurnWarp + ((3u * E + 1) * 4 + 127) / 128 * 128;
 }
 
 // How a launch cuts its work: weight rows a unit, rows of A kept for a stage, and
-// as many stages as shared memory holds (the way of a stage from its release
-// through the copies, tcgen05.cp and their barriers back to the MMA takes some
-// 2600 clocks, which the others have to cover).
+// as many stages as shared memory holds.
 struct ProductShape {
   int width, n_tiles, stages;
   uint32_t a_bytes, stage_bytes, sf_cols;
@@ -111,7 +114,7 @@ __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles,
   s.width = boxes * 64;
   s.n_tiles = (N + s.width - 1) / s.width;
   s.a_bytes = (uint32_t)min(kRowsTile, (most_rows + kRowsBox - 1) / kRowsBox * kRowsBox) * 128;
-  s.stage_bytes = s.a_bytes + s.width * 128 + kSfbBytes;
+  s.stage_bytes = s.a_bytes + s.width * 128;
   s.stages = min(kMaxStages, (int)(((uint32_t)kProductSmem - 1024 - product_fixed_smem(E)) / s.stage_bytes));
   // TMEM: two accumulators, then 2 x 4 columns of the rows' scales and 2 x 4 for
   // every 128 weight rows of a stage
@@ -172,7 +175,7 @@ struct ProductAbort {
 
 // A wait of the pipeline, bounded by `limit` once it has lasted a while: reading
 // the global timer at every wait that has to wait at all cost more than the wait.
-__device__ __forceinline__ bool product_wait(uint64_t* bar, uint32_t parity, const ProductAbort& a) {
+__device__ __forceinline__ bool product_wait(uint32_t bar, uint32_t parity, const ProductAbort& a) {
 #pragma unroll 1
   for (int it = 0; it < 64; ++it)
     if (mbar_try_wait(bar, parity)) return true;
@@ -193,7 +196,7 @@ __device__ __forceinline__ bool product_wait(uint64_t* bar, uint32_t parity, con
 
 // The same for a whole warp: one lane asks, so that waiting warps leave the
 // shared-memory pipe to those at work.
-__device__ __forceinline__ bool product_wait_warp(uint64_t* bar, uint32_t parity, const ProductAbort& a) {
+__device__ __forceinline__ bool product_wait_warp(uint32_t bar, uint32_t parity, const ProductAbort& a) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = product_wait(bar, parity, a);
   return __all_sync(0xffffffffu, ok);
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     expert_product_kernel(const __grid_constant__ ProductMaps maps, ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
-  __shared__ __align__(8) uint64_t scaled[kMaxStages], taken[kScaleWarps][kScaleRing];
+  __shared__ __align__(8) uint64_t landed[kScaleWarps][kScaleSlots], taken[kScaleWarps];
   __shared__ uint32_t tmem_slot;
   __shared__ long long scan_scratch[32];
   __shared__ volatile int s_abort;
@@ -341,21 +344,21 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   uint8_t* ring = sm + kProductSmem - 1024 - product_fixed_smem(p.E);
-  uint8_t* slots = ring + kScaleWarps * kScaleRing * kScaleStage;
-  uint8_t* turn = slots + kScaleWarps * kScaleSlots * kScaleStage;
+  uint8_t* slots = ring + kScaleWarps * kScaleStage;
+  uint8_t* turn = slots + kScaleWarps * kScaleSlots * kScaleSlot;
   int* pre = reinterpret_cast<int*>(turn + 8 * kTurnWarp);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&scaled[i], 1);
+      mbar_init(&full[i], 2);  // the codes' copies, and the scales' tcgen05.cp
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
     }
-    for (int i = 0; i < kScaleWarps * kScaleRing; ++i) mbar_init(&taken[0][i], 1);
+    for (int i = 0; i < kScaleWarps * kScaleSlots; ++i) mbar_init(&landed[0][i], 1);
+    for (int i = 0; i < kScaleWarps; ++i) mbar_init(&taken[i], 1);
     mbar_init(&drained, 1);
     mbar_fence_init();
     s_abort = 0;
@@ -418,6 +421,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const uint32_t tmem_sf = tmem + 2 * width, b_step = width > 128 ? 8 : 4;
   const int units = m_tiles * n_tiles;
   const bool whole = p.K % kKStage == 0;
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   const ProductAbort ab{&s_abort, p.status, p.timeout_ns};
 
   // Every role walks the same units and stages. The copying and the multiplying warp
@@ -425,9 +429,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   // elected lane issuing: their instructions bound a stage, and under a divergent
   // branch every descriptor took the slow way into uniform registers.
   if (warp == 0) {
-    const int nt128 = (p.N + 127) / 128;
     const CUtensorMap* mw = width == 192 ? &maps.w192 : width == 128 ? &maps.w128 : &maps.w64;
-    const uint32_t sm0 = smem_u32(sm), bar0 = smem_u32(full);
+    const uint32_t sm0 = smem_u32(sm);
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
     bool ok = true;
@@ -436,17 +439,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
                 row = __shfl_sync(0xffffffffu, (int)un.row0, 0);
       const int a_boxes = (rows + kRowsBox - 1) / kRowsBox;
-      const uint32_t bytes = (uint32_t)(width + a_boxes * kRowsBox) * 128u + kSfbBytes;
-      const int sf_row = e * nt128 + (un.n0 >> 7);
+      const uint32_t bytes = (uint32_t)(width + a_boxes * kRowsBox) * 128u;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = __all_sync(0xffffffffu, product_wait(&empty[stage], phase, ab));
+        ok = __all_sync(0xffffffffu, product_wait(empty0 + stage * 8, phase, ab));
         if (!ok) break;
-        const uint32_t st = sm0 + stage * stage_bytes, bar = bar0 + stage * 8;
+        const uint32_t st = sm0 + stage * stage_bytes, bar = full0 + stage * 8;
         if (leader) {
           mbar_arrive_expect_tx(&full[stage], bytes);
           tma_load_3d(st + a_bytes, mw, kb * 128, un.n0, e, bar);
           for (int b = 0; b < a_boxes; ++b) tma_load_2d(st + b * (kRowsBox * 128), &maps.x, kb * 128, row + b * kRowsBox, bar);
-          tma_load_2d(st + a_bytes + width * 128, &maps.wsf, kb * 256, sf_row, bar);
         }
         if (++stage == stages) {
           stage = 0;
@@ -463,9 +464,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int n0 = at.ni * width, cols = min(width, (p.N - n0 + 63) & ~63);
       const uint32_t shift = (n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
       const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * width;
-      ok = product_wait(&acc_empty[buf], ((done >> 1) & 1) ^ 1, ab);
+      ok = product_wait(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
       for (int kb = 0; kb < KB && ok; ++kb) {
-        if (!ready) ok = product_wait(&full[stage], phase, ab) && product_wait(&scaled[stage], phase, ab);
+        if (!ready) ok = product_wait(full0 + stage * 8, phase, ab);
         if (!ok) break;
         tc_fence_after();
         const uint32_t step = stage * (stage_bytes >> 4), here = stage;
@@ -474,27 +475,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           stage = 0;
           phase ^= 1;
         }
-        const bool there = mbar_test_wait(&full[stage], phase), taken_up = mbar_test_wait(&scaled[stage], phase);
+        ready = mbar_test_wait(full0 + stage * 8, phase);
         if (leader) {
           const int steps = whole || kb + 1 < KB ? 4 : (p.K - kb * kKStage + 63) / 64;
           if (steps == 4) product_mmas<4>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
           else if (steps == 3) product_mmas<3>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
           else if (steps == 2) product_mmas<2>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
           else product_mmas<1>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
-          tc_commit(&empty[here]);
+          tc_commit(empty0 + here * 8);
           if (kb + 1 == KB) tc_commit(&acc_full[buf]);
         }
-        ready = there && taken_up;
       }
     }
     if (leader) tc_commit(&drained);
   } else if (warp < 2 + kScaleWarps) {
     // scales of the stages in this warp's places of the ring
     const uint32_t mine = warp - 2;
-    const uint32_t slot0 = smem_u32(slots) + mine * kScaleSlots * kScaleStage + lane * 8;
-    const uint8_t* my_ring = ring + mine * kScaleRing * kScaleStage;
-    const uint32_t dst0 = smem_u32(my_ring) + lane * 16;
-    const uint64_t asf0 = sf_desc(my_ring), bsf0 = sf_desc(sm + a_bytes + width * 128);
+    const uint8_t* my_slots = slots + mine * kScaleSlots * kScaleSlot;
+    const uint8_t* my_ring = ring + mine * kScaleStage;
+    const uint32_t slot0 = smem_u32(my_slots), dst = smem_u32(my_ring) + lane * 16;
+    const uint64_t asf = sf_desc(my_ring), bsf0 = sf_desc(my_slots + kScaleStage);
+    const int nt128 = (p.N + 127) / 128;
     const bool leader = elect_one();
     ProductCursor load(n_tiles);
     int load_kb = 0;
@@ -506,8 +507,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if ((load_stage & (kScaleWarps - 1)) == mine) {
           if (fresh) ahead = product_unit(p, pre, load, width);
           fresh = false;
-          load_row_scales(p, ahead, load_kb, slot0 + load_slot * kScaleStage);
-          load_slot = load_slot + 1 == kScaleSlots ? 0 : load_slot + 1;
+          const uint32_t to = slot0 + load_slot * kScaleSlot;
+          load_row_scales(p, ahead, load_kb, to + lane * 8);
+          if (leader) {
+            mbar_arrive_expect_tx(&landed[mine][load_slot], kSfbBytes);
+            tma_load_2d(to + kScaleStage, &maps.wsf, load_kb * 256, ahead.e * nt128 + (ahead.n0 >> 7),
+                        smem_u32(&landed[mine][load_slot]));
+          }
+          load_slot ^= 1;
           found = true;
         }
         if (++load_stage == stages) load_stage = 0;
@@ -519,14 +526,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int i = 0; i < kScaleSlots - 1; ++i) load_next();
-    uint32_t stage = 0, phase = 0, slot = 0, place = 0, taken_phase = 1;
+    load_next();
+    uint32_t stage = 0, phase = 1, slot = 0, landed_phase = 0, taken_phase = 1;
     bool ok = true;
     for (ProductCursor at(n_tiles); at.u < units && ok; at.next()) {
       const int n0 = at.ni * width;
       const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
       for (int kb = 0; kb < KB; ++kb) {
         if ((stage & (kScaleWarps - 1)) == mine) {
+          // tcgen05.cp has taken the stage before: its slot and the ordered scales are free
+          ok = __all_sync(0xffffffffu, product_wait(smem_u32(&taken[mine]), taken_phase, ab));
+          if (!ok) break;
+          taken_phase ^= 1;
           load_next();
           asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
           // the lane's own rows: word i of row c is 128-element group i
@@ -535,26 +546,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           for (int c = 0; c < 4; ++c)
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                          : "=r"(v[c].x), "=r"(v[c].y)
-                         : "r"(slot0 + slot * kScaleStage + c * 256));
-          slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-          ok = __all_sync(0xffffffffu, product_wait(&taken[mine][place], taken_phase, ab));
-          if (!ok) break;
+                         : "r"(slot0 + slot * kScaleSlot + lane * 8 + c * 256));
           // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
-          const uint32_t dst = dst0 + place * kScaleStage;
-          const uint64_t asf = asf0 + place * (kScaleStage >> 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
                        : "memory");
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(v[0].y), "r"(v[1].y), "r"(v[2].y), "r"(v[3].y)
                        : "memory");
           fence_proxy_async_smem();
           __syncwarp();
-          // the weights' scales are in the stage; its TMEM columns are free since the stage was
-          ok = __all_sync(0xffffffffu, product_wait(&full[stage], phase, ab));
+          // the weights' scales are there, and the MMAs of the round before are done with the TMEM columns
+          ok = product_wait(smem_u32(&landed[mine][slot]), landed_phase, ab) && product_wait(empty0 + stage * 8, phase, ab);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
             const uint32_t ta = tmem_sf + stage * sf_cols;
-            const uint64_t bsf = bsf0 + stage * (stage_bytes >> 4);
+            const uint64_t bsf = bsf0 + slot * (kScaleSlot >> 4);
             if (p.K - kb * kKStage <= 128) {  // a last stage of one group
               if (two) product_scales<2, 1>(ta, b_step, asf, bsf);
               else product_scales<1, 1>(ta, b_step, asf, bsf);
@@ -562,14 +569,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               if (two) product_scales<2, 2>(ta, b_step, asf, bsf);
               else product_scales<1, 2>(ta, b_step, asf, bsf);
             }
-            tc_commit(&scaled[stage]);
-            tc_commit(&taken[mine][place]);
+            tc_commit(&full[stage]);
+            tc_commit(&taken[mine]);
           }
           __syncwarp();
-          if (++place == kScaleRing) {
-            place = 0;
-            taken_phase ^= 1;
-          }
+          slot ^= 1;
+          landed_phase ^= slot == 0;
         }
         if (++stage == stages) {
           stage = 0;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (ProductCursor at(n_tiles); at.u < units && !s_abort; at.next(), ++done) {
       if ((done & 1) != buf) continue;
       const ProductUnit un = product_unit(p, pre, at, width);
-      if (!product_wait_warp(&acc_full[buf], (done >> 1) & 1, ab)) break;
+      if (!product_wait_warp(smem_u32(&acc_full[buf]), (done >> 1) & 1, ab)) break;
       tc_fence_after();
       const int rows = min(32, un.rows - 32 * q), parts = rows > 0 ? (min(width, p.N - un.n0) + 63) / 64 : 0;
 #pragma unroll 1
