@@ -230,30 +230,6 @@ __device__ __forceinline__ void load_row_scales(const ProductParams& p, const Pr
   }
 }
 
-// One stage's scales to TMEM: 128 rows of x and CHUNKS x 128 weight rows, GROUPS of 128 elements of K.
-template <int CHUNKS, int GROUPS>
-__device__ __forceinline__ void product_scales(uint32_t ta, uint32_t b_step, uint64_t adesc, uint64_t bdesc) {
-#pragma unroll
-  for (int j = 0; j < GROUPS; ++j) {
-    tc_cp_scales(ta + 4 * j, adesc + j * 32);
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) tc_cp_scales(ta + 8 + b_step * j + 4 * c, bdesc + c * 64 + j * 32);
-  }
-}
-
-// One stage's STEPS MMAs of 64 elements of K; ta and tb are the scales' columns, those
-// of the weights b_step apart for each 128 elements of K.
-template <int STEPS>
-__device__ __forceinline__ void product_mmas(uint32_t acc, uint64_t adesc, uint64_t bdesc, uint32_t ta, uint32_t tb,
-                                             uint32_t b_step, uint32_t idesc, bool accumulate) {
-#pragma unroll
-  for (int kk = 0; kk < STEPS; ++kk) {
-    constexpr uint32_t kPair = (2u << 4) | (2u << 29);  // the upper two of a column's four scales
-    tc_mma_mxf4(acc, adesc + 2 * kk, bdesc + 2 * kk, idesc | (kk & 1 ? kPair : 0), ta + 4 * (kk >> 1),
-                tb + b_step * (kk >> 1), kk > 0 || accumulate);
-  }
-}
-
 template <int YT>
 __device__ __forceinline__ uint32_t pack_y(float lo, float hi) {
   if (YT == MOE_F16) {
@@ -424,10 +400,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
   const ProductAbort ab{&s_abort, p.status, p.timeout_ns};
 
-  // Every role walks the same units and stages. The copying and the multiplying warp
-  // run theirs with all lanes on values that the compiler can see are uniform, one
-  // elected lane issuing: their instructions bound a stage, and under a divergent
-  // branch every descriptor took the slow way into uniform registers.
+  // Every role walks the same units and stages. The copying, scaling and multiplying
+  // warps run theirs with all lanes on values that the compiler can see are uniform,
+  // one elected lane's instructions predicated: what the MMA warp has to issue bounds a
+  // stage. Under a divergent branch every descriptor took the slow way into uniform
+  // registers, and coming together again cost 120 clocks.
   if (warp == 0) {
     const CUtensorMap* mw = width == 192 ? &maps.w192 : width == 128 ? &maps.w128 : &maps.w64;
     const uint32_t sm0 = smem_u32(sm);
@@ -459,14 +436,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint64_t adesc0 = sw128_desc(sm), bdesc0 = sw128_desc(sm + a_bytes);
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 0, done = 0;
-    bool ok = true, ready = false;  // the next stage was seen to be there before this one's MMAs went out
+    bool ok = true;
     for (ProductCursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
       const int n0 = at.ni * width, cols = min(width, (p.N - n0 + 63) & ~63);
       const uint32_t shift = (n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
       const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * width;
       ok = product_wait(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
       for (int kb = 0; kb < KB && ok; ++kb) {
-        if (!ready) ok = product_wait(full0 + stage * 8, phase, ab);
+        ok = product_wait(full0 + stage * 8, phase, ab);
         if (!ok) break;
         tc_fence_after();
         const uint32_t step = stage * (stage_bytes >> 4), here = stage;
@@ -475,16 +452,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           stage = 0;
           phase ^= 1;
         }
-        ready = mbar_test_wait(full0 + stage * 8, phase);
-        if (leader) {
-          const int steps = whole || kb + 1 < KB ? 4 : (p.K - kb * kKStage + 63) / 64;
-          if (steps == 4) product_mmas<4>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
-          else if (steps == 3) product_mmas<3>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
-          else if (steps == 2) product_mmas<2>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
-          else product_mmas<1>(acc, adesc0 + step, bdesc0 + step, ta, tb, b_step, idesc, kb != 0);
-          tc_commit(empty0 + here * 8);
-          if (kb + 1 == KB) tc_commit(&acc_full[buf]);
+        const int steps = whole || kb + 1 < KB ? 4 : (p.K - kb * kKStage + 63) / 64;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          constexpr uint32_t kPair = (2u << 4) | (2u << 29);  // the upper two of a column's four scales
+          tc_mma_mxf4_if(leader && kk < steps, acc, adesc0 + step + 2 * kk, bdesc0 + step + 2 * kk, idesc | (kk & 1 ? kPair : 0),
+                         ta + 4 * (kk >> 1), tb + b_step * (kk >> 1), kk > 0 || kb > 0);
         }
+        tc_commit_if(leader, empty0 + here * 8);
+        tc_commit_if(leader && kb + 1 == KB, smem_u32(&acc_full[buf]));
       }
     }
     if (leader) tc_commit(&drained);
@@ -559,20 +535,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          if (leader) {
-            const uint32_t ta = tmem_sf + stage * sf_cols;
-            const uint64_t bsf = bsf0 + slot * (kScaleSlot >> 4);
-            if (p.K - kb * kKStage <= 128) {  // a last stage of one group
-              if (two) product_scales<2, 1>(ta, b_step, asf, bsf);
-              else product_scales<1, 1>(ta, b_step, asf, bsf);
-            } else {
-              if (two) product_scales<2, 2>(ta, b_step, asf, bsf);
-              else product_scales<1, 2>(ta, b_step, asf, bsf);
-            }
-            tc_commit(&full[stage]);
-            tc_commit(&taken[mine]);
+          const uint32_t ta = tmem_sf + stage * sf_cols;
+          const uint64_t bsf = bsf0 + slot * (kScaleSlot >> 4);
+          const bool more = p.K - kb * kKStage > 128;  // than one 128-element group
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool go = leader && (j == 0 || more);
+            tc_cp_scales_if(go, ta + 4 * j, asf + j * 32);
+            tc_cp_scales_if(go, ta + 8 + b_step * j, bsf + j * 32);
+            tc_cp_scales_if(go && two, ta + 8 + b_step * j + 4, bsf + 64 + j * 32);
           }
-          __syncwarp();
+          tc_commit_if(leader, full0 + stage * 8);
+          tc_commit_if(leader, smem_u32(&taken[mine]));
           slot ^= 1;
           landed_phase ^= slot == 0;
         }

@@ -53,6 +53,15 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) { tc_commit(smem_u32(bar)); }
+// The same where `go` holds: predicated, so that a whole warp can run through an issue loop without branching.
+__device__ __forceinline__ void tc_commit_if(bool go, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"((uint32_t)go),
+      "r"(bar)
+      : "memory");
+}
 
 // 32 lanes x 16 consecutive 32-bit columns of TMEM -> 16 registers per thread.
 __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -104,15 +113,17 @@ __device__ __forceinline__ void bulk_load(uint32_t smem, const void* gmem, uint3
                : "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T on E2M1 codes, K = 64, one E8M0 scale
-// for 32 elements from the TMEM columns sfa and sfb, fp32 accumulator.
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                            uint32_t sfb, uint32_t accumulate) {
+// Where `go` holds, D[tmem] (+)= A[smem desc] * B[smem desc]^T on E2M1 codes, K = 64, one
+// E8M0 scale for 32 elements from the TMEM columns sfa and sfb, fp32 accumulator.
+__device__ __forceinline__ void tc_mma_mxf4_if(bool go, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate), "r"((uint32_t)go)
       : "memory");
 }
 
@@ -122,10 +133,15 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int n) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 7) << 27);
 }
 
-// 512 bytes of scales (32 lanes x 16 bytes) from shared memory to 4 TMEM columns,
-// repeated over the four quarters of the lanes; in order with this thread's MMAs.
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+// Where `go` holds, 512 bytes of scales (32 lanes x 16 bytes) from shared memory to 4
+// TMEM columns, repeated over the four quarters of the lanes.
+__device__ __forceinline__ void tc_cp_scales_if(bool go, uint32_t taddr, uint64_t sdesc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(sdesc), "r"((uint32_t)go)
+      : "memory");
 }
 
 // Descriptor of those 512 bytes: no swizzle, 8-row groups of 128 bytes one after the other.
