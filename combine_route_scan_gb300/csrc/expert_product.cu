@@ -473,88 +473,86 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint64_t asf = sf_desc(my_ring), bsf0 = sf_desc(my_slots + kScaleStage);
     const int nt128 = (p.N + 127) / 128;
     const bool leader = elect_one();
-    ProductCursor load(n_tiles);
-    int load_kb = 0;
-    uint32_t load_slot = 0, load_stage = 0;
+    // from one of its places to the next one's stage; true where that is in the ring's next round
+    const auto hop = [&](ProductCursor& at, int& kb, uint32_t& place, bool& moved) {
+      const bool around = place + kScaleWarps >= stages;
+      kb += around ? (int)(stages - place + mine) : kScaleWarps;
+      place = around ? mine : place + kScaleWarps;
+      while (kb >= KB) {
+        kb -= KB;
+        at.next();
+        moved = true;
+      }
+      return around;
+    };
+    const auto first = [&](ProductCursor& at, int& kb) {
+      for (kb = (int)mine; kb >= KB; kb -= KB) at.next();
+    };
+    ProductCursor load(n_tiles), at(n_tiles);
+    int load_kb, kb;
+    uint32_t load_slot = 0, load_stage = mine;
     bool fresh = true;
     ProductUnit ahead{};
+    first(load, load_kb);
+    first(at, kb);
     const auto load_next = [&] {
-      for (bool found = false; !found && load.u < units;) {
-        if ((load_stage & (kScaleWarps - 1)) == mine) {
-          if (fresh) ahead = product_unit(p, pre, load, width);
-          fresh = false;
-          const uint32_t to = slot0 + load_slot * kScaleSlot;
-          load_row_scales(p, ahead, load_kb, to + lane * 8);
-          if (leader) {
-            mbar_arrive_expect_tx(&landed[mine][load_slot], kSfbBytes);
-            tma_load_2d(to + kScaleStage, &maps.wsf, load_kb * 256, ahead.e * nt128 + (ahead.n0 >> 7),
-                        smem_u32(&landed[mine][load_slot]));
-          }
-          load_slot ^= 1;
-          found = true;
+      if (load.u < units) {
+        if (fresh) ahead = product_unit(p, pre, load, width);
+        fresh = false;
+        const uint32_t to = slot0 + load_slot * kScaleSlot, bar = smem_u32(&landed[mine][load_slot]);
+        load_row_scales(p, ahead, load_kb, to + lane * 8);
+        if (leader) {
+          mbar_arrive_expect_tx(&landed[mine][load_slot], kSfbBytes);
+          tma_load_2d(to + kScaleStage, &maps.wsf, load_kb * 256, ahead.e * nt128 + (ahead.n0 >> 7), bar);
         }
-        if (++load_stage == stages) load_stage = 0;
-        if (++load_kb == KB) {
-          load_kb = 0;
-          load.next();
-          fresh = true;
-        }
+        __syncwarp();
+        load_slot ^= 1;
+        hop(load, load_kb, load_stage, fresh);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     load_next();
-    uint32_t stage = 0, phase = 1, slot = 0, landed_phase = 0, taken_phase = 1;
-    bool ok = true;
-    for (ProductCursor at(n_tiles); at.u < units && ok; at.next()) {
+    uint32_t stage = mine, phase = 1, slot = 0, landed_phase = 0, taken_phase = 1;
+    for (bool moved; at.u < units; phase ^= hop(at, kb, stage, moved)) {
+      // tcgen05.cp has taken the stage before: its slot and the ordered scales are free
+      if (!__all_sync(0xffffffffu, product_wait(smem_u32(&taken[mine]), taken_phase, ab))) break;
+      taken_phase ^= 1;
+      load_next();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
+      // the lane's own rows: word i of row c is 128-element group i
+      uint2 v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(v[c].x), "=r"(v[c].y)
+                     : "r"(slot0 + slot * kScaleSlot + lane * 8 + c * 256));
+      // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
+                   : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(v[0].y), "r"(v[1].y), "r"(v[2].y), "r"(v[3].y)
+                   : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      // the weights' scales are there, and the MMAs of the round before are done with the TMEM columns
+      const bool ok = product_wait(smem_u32(&landed[mine][slot]), landed_phase, ab) && product_wait(empty0 + stage * 8, phase, ab);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
       const int n0 = at.ni * width;
       const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
-      for (int kb = 0; kb < KB; ++kb) {
-        if ((stage & (kScaleWarps - 1)) == mine) {
-          // tcgen05.cp has taken the stage before: its slot and the ordered scales are free
-          ok = __all_sync(0xffffffffu, product_wait(smem_u32(&taken[mine]), taken_phase, ab));
-          if (!ok) break;
-          taken_phase ^= 1;
-          load_next();
-          asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
-          // the lane's own rows: word i of row c is 128-element group i
-          uint2 v[4];
+      const bool more = p.K - kb * kKStage > 128;  // than one 128-element group
+      const uint32_t ta = tmem_sf + stage * sf_cols;
+      const uint64_t bsf = bsf0 + slot * (kScaleSlot >> 4);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(v[c].x), "=r"(v[c].y)
-                         : "r"(slot0 + slot * kScaleSlot + lane * 8 + c * 256));
-          // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
-                       : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512), "r"(v[0].y), "r"(v[1].y), "r"(v[2].y), "r"(v[3].y)
-                       : "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          // the weights' scales are there, and the MMAs of the round before are done with the TMEM columns
-          ok = product_wait(smem_u32(&landed[mine][slot]), landed_phase, ab) && product_wait(empty0 + stage * 8, phase, ab);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ta = tmem_sf + stage * sf_cols;
-          const uint64_t bsf = bsf0 + slot * (kScaleSlot >> 4);
-          const bool more = p.K - kb * kKStage > 128;  // than one 128-element group
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const bool go = leader && (j == 0 || more);
-            tc_cp_scales_if(go, ta + 4 * j, asf + j * 32);
-            tc_cp_scales_if(go, ta + 8 + b_step * j, bsf + j * 32);
-            tc_cp_scales_if(go && two, ta + 8 + b_step * j + 4, bsf + 64 + j * 32);
-          }
-          tc_commit_if(leader, full0 + stage * 8);
-          tc_commit_if(leader, smem_u32(&taken[mine]));
-          slot ^= 1;
-          landed_phase ^= slot == 0;
-        }
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1;
-        }
+      for (int j = 0; j < 2; ++j) {
+        const bool go = leader && (j == 0 || more);
+        tc_cp_scales_if(go, ta + 4 * j, asf + j * 32);
+        tc_cp_scales_if(go, ta + 8 + b_step * j, bsf + j * 32);
+        tc_cp_scales_if(go && two, ta + 8 + b_step * j + 4, bsf + 64 + j * 32);
       }
+      tc_commit_if(leader, full0 + stage * 8);
+      tc_commit_if(leader, smem_u32(&taken[mine]));
+      slot ^= 1;
+      landed_phase ^= slot == 0;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp >= kEpilogueWarp) {
