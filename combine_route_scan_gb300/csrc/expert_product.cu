@@ -241,17 +241,19 @@ __device__ __forceinline__ uint32_t pack_y(float lo, float hi) {
 }
 
 // 32 neighbouring results (columns c ..) of each lane's row, row0 + lane, of which the
-// first `rows` lanes' exist; the whole warp takes part.
+// first `rows` lanes' exist; the whole warp takes part. Rows that 16-byte stores fit
+// leave as such, others an element (or a byte of codes) a lane, row by row.
 template <int YT>
 __device__ __forceinline__ void store_results(const ProductParams& p, uint32_t turn, long long row0, int rows, int c,
                                               const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   if (c >= p.C) return;
-  if (YT == MOE_MXFP4) {
+  const uint32_t own = turn + lane * kTurnRow;
+  if constexpr (YT == MOE_MXFP4) {
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));  // columns beyond C are zeros
-    const int se = mx_exponent(m, 2), n = min(32, p.C - c);
+    const int se = mx_exponent(m, 2);
     const float inv = exp2_exact(-se);
     uint32_t q[4];
 #pragma unroll
@@ -261,49 +263,55 @@ __device__ __forceinline__ void store_results(const ProductParams& p, uint32_t t
       for (int j = 0; j < 4; ++j)
         q[i] |= cvt_fp4x2(__fmul_rn(v[8 * i + 2 * j], inv), __fmul_rn(v[8 * i + 2 * j + 1], inv)) << (8 * j);
     }
-    if (lane < rows) {
-      const size_t row = (size_t)(row0 + lane);
-      uint8_t* out = static_cast<uint8_t*>(p.y) + row * (p.C / 2) + c / 2;
-      if ((p.C & 31) == 0) {
-        st_v4(out, make_int4(q[0], q[1], q[2], q[3]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (2 * i < n) out[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+    uint8_t* out = static_cast<uint8_t*>(p.y) + (size_t)row0 * (p.C / 2) + c / 2;
+    if (lane < rows) p.ys[(size_t)(row0 + lane) * ((p.C + 31) / 32) + c / 32] = (uint8_t)(se + 127);
+    if ((p.C & 31) == 0) {
+      if (lane < rows) st_v4(out + (size_t)lane * (p.C / 2), make_int4(q[0], q[1], q[2], q[3]));
+    } else {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(own), "r"(q[0]), "r"(q[1]), "r"(q[2]), "r"(q[3]) : "memory");
+      __syncwarp();
+      const int b = lane & 15, last = c / 2 + b < p.C / 2 ? rows : 0;
+#pragma unroll 4
+      for (int r = lane >> 4; r < last; r += 2) {
+        uint32_t w;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w) : "r"(turn + r * kTurnRow + b));
+        out[(size_t)r * (p.C / 2) + b] = (uint8_t)w;
       }
-      p.ys[row * ((p.C + 31) / 32) + c / 32] = (uint8_t)(se + 127);
+      __syncwarp();
     }
-  } else if ((p.C & 7) == 0) {
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(turn + lane * kTurnRow + i * 16),
-                   "r"(pack_y<YT>(v[8 * i], v[8 * i + 1])), "r"(pack_y<YT>(v[8 * i + 2], v[8 * i + 3])),
-                   "r"(pack_y<YT>(v[8 * i + 4], v[8 * i + 5])), "r"(pack_y<YT>(v[8 * i + 6], v[8 * i + 7]))
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(own + i * 16), "r"(pack_y<YT>(v[8 * i], v[8 * i + 1])),
+                   "r"(pack_y<YT>(v[8 * i + 2], v[8 * i + 3])), "r"(pack_y<YT>(v[8 * i + 4], v[8 * i + 5])),
+                   "r"(pack_y<YT>(v[8 * i + 6], v[8 * i + 7]))
                    : "memory");
     __syncwarp();
-    // 8 rows x 64 bytes a store
-    const int part = (lane & 3) * 8;
-    uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)(row0 + (lane >> 2)) * p.C + c + part;
-    const uint32_t from = turn + (lane >> 2) * kTurnRow + (lane & 3) * 16;
-    int4 w[4];
+    uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)row0 * p.C + c;
+    if ((p.C & 7) == 0) {
+      // 8 rows x 64 bytes a store
+      const int part = (lane & 3) * 8, r0 = lane >> 2;
+      int4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "r"(from + i * 8 * kTurnRow));
-    const int mine = c + part < p.C ? rows - (lane >> 2) : 0;
+      for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                     : "r"(turn + (8 * i + r0) * kTurnRow + (lane & 3) * 16));
+      const int last = c + part < p.C ? rows : 0;
+      out += (size_t)r0 * p.C + part;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (8 * i < mine) st_v4(out + (size_t)(8 * i) * p.C, w[i]);
-    __syncwarp();
-  } else if (lane < rows) {
-    uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)(row0 + lane) * p.C + c;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const uint32_t w = pack_y<YT>(v[i], v[i + 1]);
-      if (c + i < p.C) out[i] = (uint16_t)w;
-      if (c + i + 1 < p.C) out[i + 1] = (uint16_t)(w >> 16);
+      for (int i = 0; i < 4; ++i)
+        if (8 * i + r0 < last) st_v4(out + (size_t)(8 * i) * p.C, w[i]);
+    } else {
+      const int last = c + lane < p.C ? rows : 0;
+#pragma unroll 4
+      for (int r = 0; r < last; ++r) {
+        uint16_t w;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(turn + r * kTurnRow + lane * 2));
+        out[(size_t)r * p.C + lane] = w;
+      }
     }
+    __syncwarp();
   }
 }
 

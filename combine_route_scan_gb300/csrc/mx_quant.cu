@@ -7,8 +7,9 @@
 // 16 blocks in a row; the block's maximum takes one shuffle, and four blocks' scale
 // bytes leave as one word. The next 16 elements are loaded before the present ones
 // are worked on. (Eight elements a lane spent as many instructions on addresses as
-// on them: 223 us for 128 x 1024 x 2048 bf16.) Rows that 16-byte loads do not fit go
-// through mx_quantize_kernel, a thread a block.
+// on them: 223 us for 128 x 1024 x 2048 bf16.) Rows that 16-byte loads do not fit, or
+// that end inside a block, go through mx_quantize_pairs_kernel: a warp takes 16 blocks
+// of a row, two at a time, a pair of elements a lane.
 #include "../../include/moe_experts.h"
 #include "quant_common.cuh"
 
@@ -35,35 +36,70 @@ __device__ __forceinline__ size_t mx_scale_at(const MxQuantParams& p, long long 
   return (((size_t)e * nt + r / 128) * bt + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4;
 }
 
-// One thread a block; with tiled scales the threads beyond the edges of the
-// last tiles write their zero bytes.
-template <int DT>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(MxQuantParams p) {
+// The zero bytes beyond the edges of the last tiles (MOE_SF_TILED).
+__device__ __forceinline__ void mx_pad_tiles(const MxQuantParams& p) {
+  const long long rows4 = (p.rows + 127) / 128 * 128, blocks4 = (p.blocks + 3) / 4 * 4;
+  const long long below = (rows4 - p.rows) * blocks4, beside = p.rows * (blocks4 - p.blocks);
+  const long long pad = (below + beside) * p.experts;
+  for (long long k = blockIdx.x * 256ll + threadIdx.x; k < pad; k += gridDim.x * 256ll) {
+    const long long e = k / (below + beside), o = k % (below + beside);
+    if (o < below) p.scales[mx_scale_at(p, e, p.rows + o / blocks4, (int)(o % blocks4))] = 0;
+    else p.scales[mx_scale_at(p, e, (o - below) / (blocks4 - p.blocks), p.blocks + (int)((o - below) % (blocks4 - p.blocks)))] = 0;
+  }
+}
+
+// Two neighbouring elements; PAIRED: aligned for one load.
+template <int DT, bool PAIRED>
+__device__ __forceinline__ float2 mx_load_pair(const void* x, size_t i) {
+  if (!PAIRED) return make_float2(mx_load<DT>(x, i), mx_load<DT>(x, i + 1));
+  if (DT == MOE_F32) return __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(x) + i));
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x) + i));
+  if (DT == MOE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <int DT, bool PAIRED>
+__global__ void __launch_bounds__(256) mx_quantize_pairs_kernel(MxQuantParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const long long rows = p.tiled ? (p.rows + 127) / 128 * 128 : p.rows;
-  const long long blocks = p.tiled ? (p.blocks + 3) / 4 * 4 : p.blocks;
-  const long long total = p.experts * rows * blocks;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int b = (int)(i % blocks);
-    const long long r = i / blocks % rows, e = i / blocks / rows;
-    const size_t at = mx_scale_at(p, e, r, b);
-    if (r >= p.rows || b >= p.blocks) {
-      p.scales[at] = 0;
-      continue;
+  constexpr int kSteps = 8;  // of two blocks
+  const int lane = threadIdx.x & 31;
+  const int parts = (p.blocks + 2 * kSteps - 1) / (2 * kSteps);
+  const long long total = p.experts * p.rows * parts;
+  for (long long i = (blockIdx.x * 256ll + threadIdx.x) >> 5; i < total; i += gridDim.x * 8ll) {
+    const long long row = i / parts, e = row / p.rows, r = row - e * p.rows;
+    const int b0 = (int)(i - row * parts) * 2 * kSteps;
+    const size_t from = (size_t)(e * p.expert_stride + r * p.row_stride);
+    float2 v[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int c = (b0 + 2 * s) * 32 + lane * 2;
+      v[s] = c < p.cols ? mx_load_pair<DT, PAIRED>(p.x, from + c) : make_float2(0.f, 0.f);
     }
-    const size_t from = (size_t)(e * p.expert_stride + r * p.row_stride) + (size_t)b * 32;
-    const int n = min(32, p.cols - b * 32);
-    float m = 0.f;
-    for (int j = 0; j < n; ++j) m = fmaxf(m, fabsf(mx_load<DT>(p.x, from + j)));
-    const int se = mx_exponent(m, 2);
+    uint8_t* out = p.codes + (size_t)row * (p.cols / 2) + b0 * 16 + lane;
+    // the maxima of the half warp's 8 blocks, halving the blocks that a lane looks after each time: a lane ends
+    // up with one, of step 4 bit 0 + 2 bit 1 + bit 2 of its number
+    float m[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) m[s] = fmaxf(fabsf(v[s].x), fabsf(v[s].y));
+#pragma unroll
+    for (int o = 1, n = kSteps / 2; n; o *= 2, n /= 2) {
+      const bool upper = lane & o;
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+        m[k] = fmaxf(upper ? m[k + n] : m[k], __shfl_xor_sync(0xffffffffu, upper ? m[k] : m[k + n], o));
+    }
+    const int se = mx_exponent(fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 8)), 2);
     const float inv = exp2_exact(-se);
-    uint8_t* out = p.codes + ((size_t)e * p.rows + r) * (p.cols / 2) + (size_t)b * 16;
-    for (int j = 0; j < n; j += 2)
-      out[j / 2] = (uint8_t)cvt_fp4x2(__fmul_rn(mx_load<DT>(p.x, from + j), inv),
-                                      __fmul_rn(mx_load<DT>(p.x, from + j + 1), inv));
-    p.scales[at] = (uint8_t)(se + 127);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const float f = __shfl_sync(0xffffffffu, inv, (lane & 16) | (s >> 2) | (s & 2) | (s & 1) << 2);
+      if ((b0 + 2 * s) * 32 + lane * 2 < p.cols) out[s * 32] = (uint8_t)cvt_fp4x2(__fmul_rn(v[s].x, f), __fmul_rn(v[s].y, f));
+    }
+    const int b = b0 + 2 * (4 * (lane & 1) + (lane & 2) + (lane >> 2 & 1)) + (lane >> 4);
+    if (!(lane & 8) && b < p.blocks) p.scales[mx_scale_at(p, e, r, b)] = (uint8_t)(se + 127);
   }
+  if (p.tiled) mx_pad_tiles(p);
 }
 
 // 16 elements as loaded, and as fp32 pairs.
@@ -169,22 +205,12 @@ __global__ void __launch_bounds__(256) mx_quantize_vec_kernel(MxQuantParams p) {
       *sf = (uint8_t)(se + 127);
     }
   }
-  if (TILED) {
-    // the zero bytes beyond the edges of the last tiles
-    const int rows4 = nt * 128, blocks4 = bt * 4;
-    const long long below = (long long)(rows4 - rows) * blocks4, beside = (long long)rows * (blocks4 - blocks);
-    const long long pad = (below + beside) * p.experts;
-    for (long long k = blockIdx.x * 256ll + threadIdx.x; k < pad; k += gridDim.x * 256ll) {
-      const long long ke = k / (below + beside), o = k % (below + beside);
-      if (o < below) p.scales[mx_scale_at(p, ke, rows + o / blocks4, (int)(o % blocks4))] = 0;
-      else p.scales[mx_scale_at(p, ke, (o - below) / (blocks4 - blocks), blocks + (int)((o - below) % (blocks4 - blocks)))] = 0;
-    }
-  }
+  if (TILED) mx_pad_tiles(p);
 }
 
 template <int DT>
-void (*mx_kernel(bool vec, bool tiled, bool strided))(MxQuantParams) {
-  if (!vec) return mx_quantize_kernel<DT>;
+void (*mx_kernel(bool vec, bool paired, bool tiled, bool strided))(MxQuantParams) {
+  if (!vec) return paired ? mx_quantize_pairs_kernel<DT, true> : mx_quantize_pairs_kernel<DT, false>;
   if (tiled) return strided ? mx_quantize_vec_kernel<DT, true, true> : mx_quantize_vec_kernel<DT, true, false>;
   return strided ? mx_quantize_vec_kernel<DT, false, true> : mx_quantize_vec_kernel<DT, false, false>;
 }
@@ -218,14 +244,14 @@ extern "C" moe_status_t moe_mx_quantize(const void* x, int32_t x_dtype, int32_t 
   const int es = x_dtype == MOE_F32 ? 4 : 2;
   const bool vec = cols % 32 == 0 && (uintptr_t)x % 16 == 0 && row_stride * es % 16 == 0 &&
                    (experts == 1 || expert_stride * es % 16 == 0) && (uintptr_t)codes % 8 == 0 && (uintptr_t)scales % 4 == 0;
+  const bool paired = (uintptr_t)x % (2 * es) == 0 && (rows == 1 || row_stride % 2 == 0) && (experts == 1 || expert_stride % 2 == 0);
   const bool strided = (rows > 1 && row_stride != cols) || (experts > 1 && expert_stride != rows * cols);
-  const auto kernel = x_dtype == MOE_F32   ? mx_kernel<MOE_F32>(vec, p.tiled, strided)
-                      : x_dtype == MOE_F16 ? mx_kernel<MOE_F16>(vec, p.tiled, strided)
-                                           : mx_kernel<MOE_BF16>(vec, p.tiled, strided);
+  const auto kernel = x_dtype == MOE_F32   ? mx_kernel<MOE_F32>(vec, paired, p.tiled, strided)
+                      : x_dtype == MOE_F16 ? mx_kernel<MOE_F16>(vec, paired, p.tiled, strided)
+                                           : mx_kernel<MOE_BF16>(vec, paired, p.tiled, strided);
   int per_sm = 0;
   if (resident_blocks((const void*)kernel, 256, 0, &per_sm) != cudaSuccess || per_sm < 1) return MOE_ERR_CUDA;
-  const long long items = vec ? (long long)experts * rows * p.blocks * 2
-                              : (long long)moe_mx_scale_bytes(experts, rows, cols, sf_layout);
+  const long long items = vec ? (long long)experts * rows * p.blocks * 2 : (long long)experts * rows * ((p.blocks + 15) / 16) * 32;
   const long long need = (items + 255) / 256, most = (long long)nsm * per_sm;
   PdlLaunch L(dim3((unsigned)(need < most ? need : most)), dim3(256), 0, static_cast<cudaStream_t>(stream));
   if (cudaLaunchKernelEx(&L.cfg, kernel, p) != cudaSuccess) return MOE_ERR_CUDA;
