@@ -125,6 +125,35 @@ def test_route(case):
     check_route(x, bias, K, G, KG, sigmoid, top2, renorm, 2.5, DT[dt], pad)
 
 
+@pytest.mark.parametrize("case", [
+    # large batches take two tokens a warp: E, K, G, KG, sigmoid, top2, bias, renorm, dtype
+    (256, 8, 8, 4, True, True, True, True, "f32"), (256, 16, 1, 1, False, False, False, True, "bf16"),
+    (128, 8, 1, 1, False, False, False, True, "bf16"), (128, 6, 4, 2, False, False, True, False, "f16"),
+    (64, 6, 1, 1, True, False, True, True, "f32"), (64, 4, 16, 4, True, True, False, False, "bf16"),
+    (256, 2, 2, 1, False, True, False, True, "f16"), (60, 4, 1, 1, False, False, False, True, "f32")],
+    ids=lambda c: "-".join(map(str, c)))
+def test_route_large_batches(case):
+    E, K, G, KG, sigmoid, top2, with_bias, renorm, dt = case
+    T = 4099  # an odd last token
+    rng = np.random.default_rng(E + K)
+    bias = np.round(rng.uniform(-0.1, 0.1, E), 3).astype(np.float32) if with_bias else None
+    some = separated_logits(rng, 48, E, DT[dt], bias, sigmoid, K, G, KG, top2 and G > 1, masked=E // 16)
+    x = some[rng.integers(0, len(some), T)]  # the checked tokens at any place of a warp
+    x[-1] = some[0]
+    if not with_bias and not top2:
+        x[1::7] = rounded(rng.integers(-2, 3, x[1::7].shape) * 0.5, DT[dt])  # many equal keys
+        x[5::64] = -np.inf
+    ids, w = run_route(x, bias, K, G, KG, sigmoid, top2, renorm, 2.5, DT[dt])
+    want = {}
+    for t in range(T):
+        key = x[t].tobytes()
+        if key not in want:
+            want[key] = P.route_token(x[t], bias, K, G, KG, sigmoid, top2 and G > 1, renorm, 2.5)
+        ri, rw = want[key]
+        assert np.array_equal(ids[t], ri), (t, ids[t], ri)
+        assert (np.abs(w[t] - rw) <= 128 * EPS * np.abs(rw) + 1e-37).all(), t  # spans of 20 and sums of 256 at most
+
+
 @pytest.mark.parametrize("E,K,G,KG", [(64, 8, 1, 1), (256, 8, 8, 4), (100, 10, 5, 2), (1024, 32, 4, 2)])
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_route_ties_go_to_the_lowest_index(E, K, G, KG, dt):
@@ -219,6 +248,23 @@ def test_route_backward(sigmoid, renorm, T, E, K, dt, pad):
         tol = (2 * (fin.max() - fin.min()) + E / 32 + 48) * EPS * size
         assert (np.abs(got[t] - want) <= tol * np.maximum(P.scores(x[t], sigmoid)[0], 1e-30) * (
             1.0 if not renorm else 1.0 / max(P.scores(x[t], sigmoid)[0][ids[t]].sum(), 1e-30)) + HALF_ULP[dt] * np.abs(want) + 1e-7 * (dt == "f16")).all(), t
+
+
+@pytest.mark.parametrize("sigmoid,renorm", list(itertools.product((False, True), (False, True))))
+@pytest.mark.parametrize("E,K,dt", [(256, 8, "f32"), (256, 16, "bf16"), (128, 8, "f16"), (64, 6, "f32"), (128, 4, "bf16")])
+def test_route_backward_large_batches(sigmoid, renorm, E, K, dt):
+    T = 4097
+    rng = np.random.default_rng(E + K)
+    x = rounded(rng.standard_normal((T, E)) * 2, DT[dt])
+    x[7::50, : E // 4] = -np.inf
+    x[9] = -np.inf
+    ids = np.argsort(-x, axis=1, kind="stable")[:, :K].astype(np.int32)
+    grad = rng.standard_normal((T, K)).astype(np.float32)
+    got = run_grad(x, ids, grad, sigmoid, renorm, 1.5, DT[dt])
+    for t in [*range(0, 40), *range(T - 40, T), *rng.integers(0, T, 60)]:
+        want = P.route_gradient(x[t], ids[t], grad[t], sigmoid, renorm, 1.5)
+        # probabilities and shares are at most 1; terms of size |g|, each some 64 roundings and spans of 20 at most
+        assert np.allclose(got[t], want, rtol=HALF_ULP[dt], atol=128 * EPS * 3 * np.abs(grad[t]).max() + 6e-8 * (dt == "f16")), t
 
 
 @pytest.mark.parametrize("sigmoid,renorm", list(itertools.product((False, True), (False, True))))
