@@ -84,10 +84,13 @@ constexpr size_t kProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and
 // Shared memory behind the stages: row scales in order, scales under way (copies want
 // them on 128 bytes), the epilogue warps' turning places, running row tiles [E+1],
 // first flat row [E], row count [E].
-__host__ __device__ inline uint32_t product_fixed_smem(int E) {
-  static_assert(kProductSmem % 128 == 0 && kScaleSlot % 128 == 0 && kTurnWarp % 128 == 0, "copies' places");
+__host__ __device__ constexpr uint32_t product_fixed_smem(int E) {
   return (uint32_t)kScaleWarps * (kScaleStage + kScaleSlots * kScaleSlot) + 8 * kTurnWarp + ((3u * E + 1) * 4 + 127) / 128 * 128;
 }
+
+static_assert(kProductSmem % 128 == 0 && kScaleSlot % 128 == 0 && kTurnWarp % 128 == 0, "copies' places");
+static_assert((kProductSmem - 1024 - product_fixed_smem(1024)) / ((kRowsTile + kMaxBoxes * 64) * 128) >= kScaleWarps,
+              "every scale warp has a place in the smallest ring");
 
 // How a launch cuts its work: weight rows a unit, rows of A kept for a stage, and
 // as many stages as shared memory holds.
@@ -99,12 +102,16 @@ struct ProductShape {
 __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles, int most_rows) {
   int boxes = 1;
   uint32_t best = 0xffffffffu;
-  // the width whose rounds of units cost least: where experts have one row tile, a
-  // unit streams its weights from HBM (its cost is their bytes); where they have
-  // more, its rows and weights come from L2 and a wider unit saves rows
+  // The width whose rounds of units cost least: where experts have a row tile or two,
+  // a unit streams its weights from HBM (its cost is their bytes); where they have
+  // many, its rows and weights come from L2 and a wider unit saves rows. Measured
+  // with 64 / 128 / 192 weight rows: 8 rows of 8 experts 5.9 / 6.2 / 6.9 us, 32 rows an
+  // expert 30.9 / 27.6 / 28.7 us, 128 rows (k 7168) 239 / 184 / 188 us, 1024 rows 224 /
+  // 137 / 124 us.
+  const bool streams = m_tiles < 3 * E;
   for (int b = kMaxBoxes; b >= 1; --b) {
     const uint32_t units = (uint32_t)m_tiles * (uint32_t)((N + 64 * b - 1) / (64 * b));
-    const uint32_t cost = (units + gridDim.x - 1) / gridDim.x * (uint32_t)(most_rows <= kRowsTile ? 4 * b + 1 : b + 2);
+    const uint32_t cost = (units + gridDim.x - 1) / gridDim.x * (uint32_t)(streams ? 4 * b + 1 : b + 2);
     if (cost < best) {
       best = cost;
       boxes = b;
