@@ -48,6 +48,7 @@ struct ProductParams {
   int W, L, E, N, K, C;    // C output columns
   int xs_align;            // bytes that a copy of row scales may take: 8, 4 or 1
   long long A;
+  long long most_tiles;    // of 128 rows, with counts that dispatch can write
   int* status;
   uint64_t timeout_ns;
 };
@@ -387,8 +388,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const long long tiles = (n + kRowsTile - 1) / kRowsTile;
       const long long before = carry + block_exclusive_scan(tiles, scan_scratch);
       if (e < p.E) {
-        pre[e] = (int)before;
-        if (e == p.E - 1) pre[p.E] = (int)(before + tiles);
+        pre[e] = (int)min(before, 1ll << 30);
+        if (e == p.E - 1) pre[p.E] = (int)min(before + tiles, 1ll << 30);
       }
       __syncthreads();
       // the last expert of this pass carries on
@@ -404,7 +405,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   most_rows = (int)(lane < kProductThreads / 32 ? scan_scratch[lane] : 0);
   most_rows = __reduce_max_sync(0xffffffffu, most_rows);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  const int m_tiles = __shfl_sync(0xffffffffu, pre[p.E], 0), KB = (p.K + kKStage - 1) / kKStage;
+  // overlapping experts (counts that fall and rise again, reported above) can have more
+  // row tiles than the units' numbers hold: then none is worked on
+  const int m_tiles = pre[p.E] <= p.most_tiles ? __shfl_sync(0xffffffffu, pre[p.E], 0) : 0, KB = (p.K + kKStage - 1) / kKStage;
   const ProductShape shape = product_shape(p.N, p.E, m_tiles, most_rows);
   const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
   const uint32_t stages = __shfl_sync(0xffffffffu, shape.stages, 0), a_bytes = __shfl_sync(0xffffffffu, shape.a_bytes, 0);
@@ -603,8 +606,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           for (int j = 0; j < 32; ++j) {
             const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
             // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
-            // bits that follows
-            h[j] = __fdividef(a, 1.0f + __expf(-a)) * b;
+            // bits that follows; the divisor stays within [1, 2], where the fast division holds (as a / (1 + exp(-a)),
+            // gates below -87 came out as 0, whatever they were to be multiplied by)
+            const float t = __expf(-fabsf(a));
+            h[j] = __fdividef(a < 0.f ? a * t : a, 1.0f + t) * b;
           }
           store_results<YT>(p, my_turn, un.row0 + 32 * q, rows, n / 2, h);
         } else {
@@ -700,16 +705,16 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   int64_t A = 0;
   const moe_status_t st = moe_get_workspace_size(cfg, &need, &A);
   if (st != MOE_OK) return st;
-  if (n < 1 || k < 1 || epilogue < MOE_EPI_NONE || epilogue > MOE_EPI_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if (n < 1 || k < 1 || k > (1 << 30) || epilogue < MOE_EPI_NONE || epilogue > MOE_EPI_SWIGLU) return MOE_ERR_INVALID_ARG;
   if (k % 32) return MOE_ERR_UNSUPPORTED;
   const int E = cfg->moe_expert_num, W = cfg->ep_world_size;
   if (epilogue == MOE_EPI_SWIGLU && n % 2) return MOE_ERR_INVALID_ARG;
   const int C = epilogue == MOE_EPI_SWIGLU ? n / 2 : n;
   if (y_dtype != MOE_F16 && y_dtype != MOE_BF16 && y_dtype != MOE_MXFP4) return MOE_ERR_INVALID_ARG;
   if (y_dtype == MOE_MXFP4 ? C % 2 != 0 || !y_scales : y_scales != nullptr) return MOE_ERR_INVALID_ARG;
-  // units of 128 rows x 64 weight rows are counted in 32 bits
-  if ((long long)E * n >= 2147483647LL || ((long long)W * A / kRowsTile + E) * ((n + 63) / 64) >= 2147483647LL)
-    return MOE_ERR_INVALID_ARG;
+  // units of 128 rows x 64 weight rows are counted in 32 bits, and a CTA looks some of its units ahead
+  const long long most_tiles = (long long)W * A / kRowsTile + E, most_units = most_tiles * ((n + 63LL) / 64);
+  if ((long long)E * n >= 2147483647LL || most_units >= 2147483647LL - 65536) return MOE_ERR_INVALID_ARG;
   if (!ep_recv_count) return MOE_ERR_INVALID_ARG;
   if (A > 0 && (!x || !x_scales || !w || !w_scales || !y)) return MOE_ERR_INVALID_ARG;
   auto aligned = [](const void* p, size_t a) { return ((uintptr_t)p % a) == 0; };
@@ -743,6 +748,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   p.C = C;
   p.xs_align = k % 256 == 0 && aligned(x_scales, 8) ? 8 : k % 128 == 0 ? 4 : 1;
   p.A = A;
+  p.most_tiles = most_tiles;
   p.status = &static_cast<WsHeader*>(ws)->status;
   p.timeout_ns = (uint64_t)cfg->wait_timeout_us * 1000ull;
   const bool sw = epilogue == MOE_EPI_SWIGLU;
@@ -754,8 +760,7 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
   if (resident_blocks((const void*)kernel, kProductThreads, smem, &per_sm) != cudaSuccess || per_sm < 1)
     return MOE_ERR_CUDA;
   // a unit is at least 64 weight rows of an expert's tile: no more CTAs than that
-  const long long most = ((long long)W * A / kRowsTile + E) * ((n + 63) / 64);
-  PdlLaunch L(dim3((unsigned)(most < nsm ? most : nsm)), dim3(kProductThreads), smem, static_cast<cudaStream_t>(stream));
+  PdlLaunch L(dim3((unsigned)(most_units < nsm ? most_units : nsm)), dim3(kProductThreads), smem, static_cast<cudaStream_t>(stream));
   if (cudaLaunchKernelEx(&L.cfg, kernel, maps, p) != cudaSuccess) return MOE_ERR_CUDA;
   note_launches(1);
   return MOE_OK;

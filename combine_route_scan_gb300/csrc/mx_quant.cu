@@ -137,14 +137,16 @@ __global__ void __launch_bounds__(256) mx_quantize_vec_kernel(MxQuantParams p) {
   pdl_launch_dependents();
   constexpr int kEs = DT == MOE_F32 ? 4 : 2;
   const int lane = threadIdx.x & 31, half = lane & 1;
-  const int rows = (int)p.rows, blocks = p.blocks;
+  const unsigned rows = (unsigned)p.rows;  // with a step added, and rounded up, beyond 31 bits
+  const int blocks = p.blocks;
   const long long total = (long long)p.experts * rows * blocks;
   const long long step = gridDim.x * 128ll;
   long long i = blockIdx.x * 128ll + (threadIdx.x >> 1);
-  int b = 0, r = 0, e = 0, db = 0, dr = 0, de = 0;
+  int b = 0, e = 0, db = 0, de = 0;
+  unsigned r = 0, dr = 0;
   if (TILED || STRIDED) {
-    b = (int)(i % blocks), r = (int)(i / blocks % rows), e = (int)(i / blocks / rows);
-    db = (int)(step % blocks), dr = (int)(step / blocks % rows), de = (int)(step / blocks / rows);
+    b = (int)(i % blocks), r = (unsigned)(i / blocks % rows), e = (int)(i / blocks / rows);
+    db = (int)(step % blocks), dr = (unsigned)(step / blocks % rows), de = (int)(step / blocks / rows);
   }
   const auto advance = [&] {
     b += db;
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(256) mx_quantize_vec_kernel(MxQuantParams p) {
     return x + (STRIDED ? (size_t)(e * p.expert_stride + r * p.row_stride + b * 32) : (size_t)k * 32) * kEs;
   };
   const bool words = (blocks & 3) == 0;  // four blocks from a multiple of 4 on are in one row, and four neighbouring pairs
-  const int nt = (rows + 127) >> 7, bt = (blocks + 3) >> 2;
+  const int nt = (int)((rows + 127) >> 7), bt = (blocks + 3) >> 2;
   MxVec<DT> next{};
   if (i < total) next.load(from(i));
   for (long long first = i - (lane >> 1); first < total; first += step, i += step) {

@@ -793,8 +793,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32, LANES == 16 ? 6 : 1) route_
       for (int j = 0; j < EPL; ++j) v[j] = fmaxf(ahead[j], -INFINITY);  // NaN becomes -inf
     }
     const int id = there && lane < p.K && (unsigned)id_ahead < (unsigned)p.E ? id_ahead : -1;
-    const float g = id >= 0 ? __fmul_rn(g_ahead, p.scaling) : 0.f;
     const float x = id >= 0 ? fmaxf(raw_ahead, -INFINITY) : -INFINITY;
+    // a masked pick's weight is 0 whatever the logits: nothing of its gradient, infinite or NaN, reaches the others
+    const float g = x > -INFINITY ? __fmul_rn(g_ahead, p.scaling) : 0.f;
     load(t + step);
     float d;
     if (p.sigmoid) {

@@ -79,7 +79,8 @@ moe_status_t moe_route(const moe_router_config_t* rc, const void* logits, const 
  * at the chosen experts, zero elsewhere, and
  *   softmax, not renormalised  d_e = s_e * (g_e - sum_j g_j s_j), g_e = 0 where e
  *                              was not chosen, at every expert.
- * Masked experts get zero. expert_ids as moe_route gave them; an id outside
+ * Masked experts get zero, and what grad_scales holds at masked picks (infinities
+ * and NaN included) is not used. expert_ids as moe_route gave them; an id outside
  * [0, E) is passed over, ids repeated in a token give unspecified values.
  * group_num, topk_group and group_score are checked as in moe_route and not
  * used otherwise.
@@ -135,7 +136,7 @@ enum {
  *
  *   cfg           the dispatch's configuration: W, bs, topk, E, wait_timeout_us and
  *                 the workspace size are taken from it; h, types and modes are not
- *   k             elements of a row: a multiple of 32 (cfg->h for rows of moe_dispatch,
+ *   k             elements of a row: a multiple of 32, at most 2^30 (cfg->h for rows of moe_dispatch,
  *                 the intermediate size for rows of this function's MOE_MXFP4 output)
  *   x             [W][A][k / 2] codes (A from moe_get_workspace_size), 16-byte aligned
  *   x_scales      [W][A][k / 32] E8M0 bytes, 4-byte aligned
@@ -150,7 +151,9 @@ enum {
  *   ws            the workspace that the dispatch used (it holds the status word)
  * Rows at or beyond ep_recv_count[d][L*W-1] are left untouched. A count that is
  * negative, decreasing or above A is reported as MOE_ERR_BAD_ASSIST, and that
- * expert's rows are passed over; a wait that ran out as MOE_ERR_TIMEOUT. */
+ * expert's rows are passed over (all rows, where the counts left overlap to more
+ * 128-row tiles than counts of dispatch can have); a wait that ran out as
+ * MOE_ERR_TIMEOUT. */
 moe_status_t moe_expert_product(const moe_config_t* cfg, const void* x, const uint8_t* x_scales,
                                 const int32_t* ep_recv_count, const void* w, const uint8_t* w_scales, int32_t n,
                                 int32_t k, int32_t epilogue, int32_t y_dtype, void* y, uint8_t* y_scales, void* ws,

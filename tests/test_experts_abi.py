@@ -64,6 +64,20 @@ def test_refusals_without_a_gpu(lib):
     assert L.moe_expert_product(ctypes.byref(cfg), None, None, None, None, None, 64, 64, 0, 2, None, None, None, 0, None) == 1
 
 
+def test_product_refuses_rows_and_units_beyond_its_numbers(lib):
+    import torch
+    L = lib.lib()
+    cfg = lib.config(2, 4, 64, 2, 4, torch.bfloat16)
+    aligned = 1 << 20  # no call gets as far as to use these
+    call = lambda n, k: L.moe_expert_product(ctypes.byref(cfg), aligned, aligned, aligned, aligned, aligned, n, k, 0, 2,  # noqa: E731
+                                             aligned, None, aligned, 0, None)
+    assert call(64, 1 << 30) == call(64, 64) == 3  # the workspace's size is refused, and nothing before it
+    assert call(64, (1 << 30) + 32) == 1 and call(64, (1 << 31) - 32) == 1
+    assert call(1 << 29, 64) == 1
+    cfg.bs = 1 << 20  # 65540 row tiles at most: a CTA's next unit has to fit 32 bits too
+    assert call(32766 * 64, 64) == 1 and call(32764 * 64, 64) == 3
+
+
 def test_binding_refuses_cpu_tensors(lib):
     import torch
     rc = lib.router_config(4, 64, 8, torch.float32)

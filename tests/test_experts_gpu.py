@@ -307,6 +307,26 @@ def test_route_backward_masked_rows_and_foreign_ids():
     assert np.allclose(got[3], want, rtol=0, atol=8 * EPS)
 
 
+@pytest.mark.parametrize("T,E", [(5, 40), (3, 128), (4160, 128)])
+@pytest.mark.parametrize("sigmoid,renorm", list(itertools.product((False, True), (False, True))))
+def test_route_backward_passes_over_gradients_of_masked_picks(sigmoid, renorm, T, E):
+    """Infinities and NaN there (a loss of the weights' logarithms has them) reach no other expert."""
+    rng = np.random.default_rng(21)
+    K = 4
+    x = np.full((T, E), -np.inf)
+    x[:, 7:9] = rounded(rng.standard_normal((T, 2)), torch.float32)
+    ids = np.tile(np.array([8, 0, 7, 1], dtype=np.int32), (T, 1))
+    grad = rng.standard_normal((T, K)).astype(np.float32)
+    clean = grad.copy()
+    grad[:, 1], grad[:, 3] = np.inf, np.nan
+    clean[:, [1, 3]] = 0
+    got = run_grad(x, ids, grad, sigmoid, renorm, 1.5, torch.float32)
+    for t in range(0, T, 1 + T // 64):
+        want = P.route_gradient(x[t], ids[t], clean[t], sigmoid, renorm, 1.5)
+        assert np.allclose(got[t], want, rtol=HALF_ULP["f32"], atol=128 * EPS * 3 * np.abs(clean[t]).max()), t
+    assert np.isfinite(got).all() and (np.delete(got, [7, 8], 1) == 0).all()
+
+
 # ------------------------------------------------------------------ MX FP4 quantisation
 
 def run_quantize(x, dtype, layout, pad=0):
@@ -588,6 +608,41 @@ def test_product_reports_bad_counts(bad):
     else:
         ep[0, 3] = ep[0, 1] - 1
     run_product(pr, "bf16", False, expect="BAD_ASSIST", ep=ep)
+
+
+def test_product_passes_over_counts_that_overlap_many_times():
+    """Counts that fall to zero and rise again at every other expert give some thousand row tiles, of a
+    hundred that the units are numbered for."""
+    pr = Product(2, 128, 4, [1] * 128, 64, 64, seed=3)
+    ep = np.zeros((2, 64, 2), dtype=np.int32)
+    ep[:, ::2] = pr.A
+    y, _ = run_product(pr, "bf16", False, expect="BAD_ASSIST", ep=ep.reshape(2, 128))
+    assert bool((y == 777.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp4"])
+def test_product_swiglu_of_large_negative_gates(dtype):
+    """silu(-88) is 5e-37: next to an up value of 2^100 and more it still counts. A gate of -inf is out of range
+    of the inputs; one of -2^20 gives zero."""
+    pr = Product(2, 4, 2, [3, 2, 0, 1], 4, 64, seed=4)
+    pr.xc[:], pr.xs[:] = 0, 127
+    pr.xc[..., 0] = 0x22  # 1, 1
+    gate, up = np.zeros((2, 64)), np.zeros((2, 64))
+    gate[0, :2], gate[1, 0] = (-64, -24), -(2.0 ** 20)
+    up[0, 0], up[1, 0] = 2.0 ** 120, 2.0 ** 60
+    codes, s = P.quantize(np.stack([gate[0], up[0], gate[1], up[1]]))
+    pr.wc[:], pr.ws[:] = P.pack(codes), s
+    y, ys = run_product(pr, dtype, True)
+    want = -88.0 * np.exp(-88.0) / (1 + np.exp(-88.0)) * 2.0 ** 120
+    for d, lo, hi in pr.ranges:
+        if dtype == "fp4":
+            got = P.values(P.unpack(y[d, lo:hi].cpu().numpy()), ys[d, lo:hi].cpu().numpy())
+            err = 2.0 ** -3  # half a step of 1 at 4 and above, or of 0.5 at 2 and above
+        else:
+            got, err = y[d, lo:hi].double().cpu().numpy(), HALF_ULP[dtype]
+        # exp's result is below the normal numbers: 2^-149 of 2^-127, and 88 / 2^23 of its value
+        assert (np.abs(got[:, 0] - want) <= (err + 2.0 ** -16) * abs(want)).all(), (got[:, 0], want)
+        assert (got[:, 1] == 0).all()
 
 
 def test_product_of_no_tokens():
