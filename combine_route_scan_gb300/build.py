@@ -2,7 +2,8 @@
 
 Each .cu file compiles to its own object in parallel with nvcc, then nvcc links
 them into combine_route_scan_gb300/_build/libcrs_moe.so. The CUDA runtime is
-linked statically. No cmake.
+linked statically. No cmake. Beside it _build/_bind.so, the native part of the
+binding (csrc/bind.cpp, g++), is built.
 
 ``build(observer=True)`` builds the flag-observer test variant
 (_build/observer/libcrs_moe.so, ``-DMOE_FLAG_OBSERVER``): the dispatch payload
@@ -26,9 +27,11 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -38,6 +41,8 @@ CHECKED_DIR = os.path.join(OUT_DIR, "checked")
 CHECKED_LIB = os.path.join(CHECKED_DIR, "libcrs_moe.so")
 OBSERVER_DIR = os.path.join(OUT_DIR, "observer")
 OBSERVER_LIB = os.path.join(OBSERVER_DIR, "libcrs_moe.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(OUT_DIR, "_bind.so")
 PHASE_DIR = os.path.join(OUT_DIR, "phase")
 PHASE_LIB = os.path.join(PHASE_DIR, "libcrs_moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -63,12 +68,36 @@ def _inputs_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _bind_stale() -> bool:
+    files = [BIND_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h"))]
+    return not os.path.exists(BIND) or os.path.getmtime(BIND) < max(os.path.getmtime(f) for f in files)
+
+
+def build_bind() -> str:
+    """The CPython module _build/_bind.so, against the headers of Python, CUDA and torch."""
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    tmp = BIND + f".tmp{os.getpid()}"
+    os.makedirs(OUT_DIR, exist_ok=True)
+    cmd = [os.environ.get("CXX") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-I{torch_dir}/include",
+           f"-I{torch_dir}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))}/include", BIND_SRC, "-o", tmp,
+           f"-L{torch_dir}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None, checked: bool = False,
           observer: bool = False, phase: bool = False) -> str:
     out_dir, lib = ((CHECKED_DIR, CHECKED_LIB) if checked else (OBSERVER_DIR, OBSERVER_LIB) if observer else
                     (PHASE_DIR, PHASE_LIB) if phase else (OUT_DIR, LIB))
     os.makedirs(out_dir, exist_ok=True)
+    bind = force or _bind_stale()
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _inputs_mtime():
+        if bind:
+            build_bind()
         return lib
     cc = nvcc()
     flags = (NVCC_FLAGS + list(extra_flags or []) + (["-DMOE_BOUNDS_CHECK"] if checked else []) +
@@ -87,7 +116,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, checked:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        other = ex.submit(build_bind) if bind else None
         objs = list(ex.map(compile_one, sources()))
+        if other:
+            other.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

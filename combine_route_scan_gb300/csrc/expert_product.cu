@@ -15,8 +15,8 @@
 //   * the weights' scales, laid out in the tensor cores' order (MOE_SF_TILED), come
 //     in boxes of 2 x 1 KB for 256 rows (untiled bulk copies of 1 KB kept the copy
 //     engine busy for longer than the codes did); the rows' scales lie a row
-//     after the other as dispatch wrote them: a lane brings 8 bytes of its rows
-//     (r, r + 32, ..) by cp.async and stores them in that order; the same warp's
+//     after the other as dispatch wrote them: a lane loads 8 bytes of its rows
+//     (r, r + 32, ..) and stores them in that order; the same warp's
 //     tcgen05.cp takes both to TMEM, and its commit arrives on the barrier of the
 //     stage's codes, so that the MMA warp is left with one wait, four MMAs and one
 //     commit a stage (what it has to issue bounds a stage);
@@ -53,10 +53,10 @@ struct ProductParams {
   uint64_t timeout_ns;
 };
 
-// Boxes of 32 rows of x, of 64, 128 and 192 rows of w, and of the scales of 2 x 128
-// rows of w; all but x's are one copy a stage.
+// Boxes of 32 rows of x, of 64 rows of w and of the scales of 2 x 128 rows of w. (A stage's
+// rows in one box each, with a map for every size, took the same time.)
 struct ProductMaps {
-  CUtensorMap x, w64, w128, w192, wsf;
+  CUtensorMap x, w, wsf;
 };
 
 constexpr int kProductThreads = 448;
@@ -72,10 +72,10 @@ constexpr uint32_t kSfbBytes = 2 * 1024;     // 2 x 128 rows x 8 scales
 // be a round ahead). They have rings of their own, so that a stage's scales are in
 // TMEM when its codes arrive: with them in the stages, a stage's way from its release
 // through copy, tcgen05.cp and their barriers back to the MMA took 2600 clocks, a
-// third of which were the scales'. A slot holds the rows' scales (a lane's 8 bytes
-// of its rows) and the weights'; one stage ahead of the present one is under way.
+// third of which were the scales'. One stage ahead of the present one is under way: the
+// weights' scales in a slot, the rows' in registers.
 constexpr int kScaleWarps = 4, kScaleSlots = 2;
-constexpr uint32_t kScaleStage = 128 * 8, kScaleSlot = kScaleStage + kSfbBytes;
+constexpr uint32_t kScaleStage = 128 * 8;
 // An epilogue warp turns 32 rows x 64 bytes around in shared memory before it
 // stores them (rows 80 bytes apart: no bank is hit twice): stored a row a lane, every
 // store touched 32 lines, and the epilogue was what the scale warps waited for.
@@ -86,10 +86,10 @@ constexpr size_t kProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and
 // them on 128 bytes), the epilogue warps' turning places, running row tiles [E+1],
 // first flat row [E], row count [E].
 __host__ __device__ constexpr uint32_t product_fixed_smem(int E) {
-  return (uint32_t)kScaleWarps * (kScaleStage + kScaleSlots * kScaleSlot) + 8 * kTurnWarp + ((3u * E + 1) * 4 + 127) / 128 * 128;
+  return (uint32_t)kScaleWarps * (kScaleStage + kScaleSlots * kSfbBytes) + 8 * kTurnWarp + ((3u * E + 1) * 4 + 127) / 128 * 128;
 }
 
-static_assert(kProductSmem % 128 == 0 && kScaleSlot % 128 == 0 && kTurnWarp % 128 == 0, "copies' places");
+static_assert(kProductSmem % 128 == 0 && kScaleStage % 128 == 0 && kTurnWarp % 128 == 0, "copies' places");
 static_assert((kProductSmem - 1024 - product_fixed_smem(1024)) / ((kRowsTile + kMaxBoxes * 64) * 128) >= kScaleWarps,
               "every scale warp has a place in the smallest ring");
 
@@ -107,7 +107,7 @@ __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles,
   // a unit streams its weights from HBM (its cost is their bytes); where they have
   // many, its rows and weights come from L2 and a wider unit saves rows. Measured
   // with 64 / 128 / 192 weight rows: 8 rows of 8 experts 5.9 / 6.2 / 6.9 us, 32 rows an
-  // expert 30.9 / 27.6 / 28.7 us, 128 rows (k 7168) 239 / 184 / 188 us, 1024 rows 224 /
+  // expert 30.9 / 27.6 / 28.7 us, 128 rows (k 7168) 239 / 182 / 188 us, 1024 rows 224 /
   // 137 / 124 us.
   const bool streams = m_tiles < 3 * E;
   for (int b = kMaxBoxes; b >= 1; --b) {
@@ -210,31 +210,42 @@ __device__ __forceinline__ bool product_wait_warp(uint32_t bar, uint32_t parity,
   return __all_sync(0xffffffffu, ok);
 }
 
-// The 8 scale bytes of rows lane, lane + 32, .. of a unit for stage kb into this
-// lane's part of a slot, by the widest asynchronous copies that the row length
-// (K / 32 bytes) and x_scales' address align; what lies beyond the row's end is
-// left as it is, or zero where a last MMA reads it.
-__device__ __forceinline__ void load_row_scales(const ProductParams& p, const ProductUnit& un, int kb, uint32_t dst) {
+// The same where all lanes ask, for the warps that others wait for: nothing of it diverges
+// when the phase is there at once.
+__device__ __forceinline__ bool product_wait_all(uint32_t bar, uint32_t parity, const ProductAbort& a) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, product_wait(bar, parity, a));
+}
+
+// The 8 scale bytes of rows lane, lane + 32, .. of a unit for stage kb, by the widest loads
+// that the row length (K / 32 bytes) and x_scales' address align; zeros beyond the
+// row's end and the unit's rows.
+__device__ __forceinline__ void load_row_scales(const ProductParams& p, const ProductUnit& un, int kb, uint2 (&v)[4]) {
   const int lane = threadIdx.x & 31, blocks = p.K / 32, left = min(8, blocks - kb * 8);
   const uint8_t* src = p.xs + (size_t)(un.row0 + lane) * blocks + kb * 8;
   const size_t step = (size_t)32 * blocks;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = make_uint2(0, 0);
   if (p.xs_align == 8) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (lane + 32 * c < un.rows)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + c * 256), "l"(src + c * step) : "memory");
+      if (lane + 32 * c < un.rows) v[c] = __ldg(reinterpret_cast<const uint2*>(src + c * step));
   } else if (p.xs_align == 4) {
-    for (int c = 0; lane + 32 * c < un.rows; ++c)
-      for (int b = 0; b < left; b += 4)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + c * 256 + b), "l"(src + c * step + b) : "memory");
-  } else {
-    for (int c = 0; lane + 32 * c < un.rows; ++c)
-      for (int i = 0; i < 2; ++i) {
-        uint32_t v = 0;
-        for (int b = 0; b < 4; ++b)
-          if (4 * i + b < left) v |= (uint32_t)__ldg(src + c * step + 4 * i + b) << (8 * b);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + c * 256 + 4 * i), "r"(v) : "memory");
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < un.rows) {
+        v[c].x = __ldg(reinterpret_cast<const uint32_t*>(src + c * step));
+        if (left > 4) v[c].y = __ldg(reinterpret_cast<const uint32_t*>(src + c * step) + 1);
       }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < un.rows)
+        for (int b = 0; b < left; ++b) {
+          const uint32_t w = (uint32_t)__ldg(src + c * step + b) << (8 * (b & 3));
+          if (b < 4) v[c].x |= w;
+          else v[c].y |= w;
+        }
   }
 }
 
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   uint8_t* ring = sm + kProductSmem - 1024 - product_fixed_smem(p.E);
   uint8_t* slots = ring + kScaleWarps * kScaleStage;
-  uint8_t* turn = slots + kScaleWarps * kScaleSlots * kScaleSlot;
+  uint8_t* turn = slots + kScaleWarps * kScaleSlots * kSfbBytes;
   int* pre = reinterpret_cast<int*>(turn + 8 * kTurnWarp);
 
   if (threadIdx.x == 0) {
@@ -424,26 +435,28 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   // stage. Under a divergent branch every descriptor took the slow way into uniform
   // registers, and coming together again cost 120 clocks.
   if (warp == 0) {
-    const CUtensorMap* mw = width == 192 ? &maps.w192 : width == 128 ? &maps.w128 : &maps.w64;
     const uint32_t sm0 = smem_u32(sm);
+    const int w_boxes = width >> 6;
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
     bool ok = true;
     for (ProductCursor at(n_tiles); at.u < units && ok; at.next()) {
       const ProductUnit un = product_unit(p, pre, at, width);
       const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
-                row = __shfl_sync(0xffffffffu, (int)un.row0, 0);
+                row = __shfl_sync(0xffffffffu, (int)un.row0, 0), n0 = at.ni * width;
       const int a_boxes = (rows + kRowsBox - 1) / kRowsBox;
       const uint32_t bytes = (uint32_t)(width + a_boxes * kRowsBox) * 128u;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = __all_sync(0xffffffffu, product_wait(empty0 + stage * 8, phase, ab));
+        ok = product_wait_all(empty0 + stage * 8, phase, ab);
         if (!ok) break;
         const uint32_t st = sm0 + stage * stage_bytes, bar = full0 + stage * 8;
-        if (leader) {
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_3d(st + a_bytes, mw, kb * 128, un.n0, e, bar);
-          for (int b = 0; b < a_boxes; ++b) tma_load_2d(st + b * (kRowsBox * 128), &maps.x, kb * 128, row + b * kRowsBox, bar);
-        }
+        mbar_expect_tx_if(leader, bar, bytes);
+#pragma unroll
+        for (int b = 0; b < kMaxBoxes; ++b)
+          tma_load_3d_if(leader && b < w_boxes, st + a_bytes + b * (64 * 128), &maps.w, kb * 128, n0 + b * 64, e, bar);
+#pragma unroll
+        for (int b = 0; b < kRowsTile / kRowsBox; ++b)
+          tma_load_2d_if(leader && b < a_boxes, st + b * (kRowsBox * 128), &maps.x, kb * 128, row + b * kRowsBox, bar);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1;
@@ -459,9 +472,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int n0 = at.ni * width, cols = min(width, (p.N - n0 + 63) & ~63);
       const uint32_t shift = (n0 & 127) >> 5;  // columns before the unit's first weight row: 0 or 2
       const uint32_t idesc = idesc_mxf4(cols), buf = done & 1, acc = tmem + buf * width;
-      ok = product_wait(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
+      ok = product_wait_all(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
       for (int kb = 0; kb < KB && ok; ++kb) {
-        ok = product_wait(full0 + stage * 8, phase, ab);
+        ok = product_wait_all(full0 + stage * 8, phase, ab);
         if (!ok) break;
         tc_fence_after();
         const uint32_t step = stage * (stage_bytes >> 4), here = stage;
@@ -485,10 +498,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (warp < 2 + kScaleWarps) {
     // scales of the stages in this warp's places of the ring
     const uint32_t mine = warp - 2;
-    const uint8_t* my_slots = slots + mine * kScaleSlots * kScaleSlot;
+    const uint8_t* my_slots = slots + mine * kScaleSlots * kSfbBytes;
     const uint8_t* my_ring = ring + mine * kScaleStage;
     const uint32_t slot0 = smem_u32(my_slots), dst = smem_u32(my_ring) + lane * 16;
-    const uint64_t asf = sf_desc(my_ring), bsf0 = sf_desc(my_slots + kScaleStage);
+    const uint64_t asf = sf_desc(my_ring), bsf0 = sf_desc(my_slots);
     const int nt128 = (p.N + 127) / 128;
     const bool leader = elect_one();
     // from one of its places to the next one's stage; true where that is in the ring's next round
@@ -511,39 +524,27 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t load_slot = 0, load_stage = mine;
     bool fresh = true;
     ProductUnit ahead{};
+    uint2 v[4];  // the lane's own rows: word i of row c is 128-element group i
     first(load, load_kb);
     first(at, kb);
     const auto load_next = [&] {
       if (load.u < units) {
         if (fresh) ahead = product_unit(p, pre, load, width);
         fresh = false;
-        const uint32_t to = slot0 + load_slot * kScaleSlot, bar = smem_u32(&landed[mine][load_slot]);
-        load_row_scales(p, ahead, load_kb, to + lane * 8);
-        if (leader) {
-          mbar_arrive_expect_tx(&landed[mine][load_slot], kSfbBytes);
-          tma_load_2d(to + kScaleStage, &maps.wsf, load_kb * 256, ahead.e * nt128 + (ahead.n0 >> 7), bar);
-        }
-        __syncwarp();
+        const uint32_t bar = smem_u32(&landed[mine][load_slot]);
+        load_row_scales(p, ahead, load_kb, v);
+        mbar_expect_tx_if(leader, bar, kSfbBytes);
+        tma_load_2d_if(leader, slot0 + load_slot * kSfbBytes, &maps.wsf, load_kb * 256, ahead.e * nt128 + (ahead.n0 >> 7), bar);
         load_slot ^= 1;
         hop(load, load_kb, load_stage, fresh);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     load_next();
     uint32_t stage = mine, phase = 1, slot = 0, landed_phase = 0, taken_phase = 1;
     for (bool moved; at.u < units; phase ^= hop(at, kb, stage, moved)) {
       // tcgen05.cp has taken the stage before: its slot and the ordered scales are free
-      if (!__all_sync(0xffffffffu, product_wait(smem_u32(&taken[mine]), taken_phase, ab))) break;
+      if (!product_wait_all(smem_u32(&taken[mine]), taken_phase, ab)) break;
       taken_phase ^= 1;
-      load_next();
-      asm volatile("cp.async.wait_group %0;" ::"n"(kScaleSlots - 1) : "memory");
-      // the lane's own rows: word i of row c is 128-element group i
-      uint2 v[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(v[c].x), "=r"(v[c].y)
-                     : "r"(slot0 + slot * kScaleSlot + lane * 8 + c * 256));
       // the 4 bytes of row r and group i at i * 512 + (r % 32) * 16 + (r / 32) * 4
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0].x), "r"(v[1].x), "r"(v[2].x), "r"(v[3].x)
                    : "memory");
@@ -551,15 +552,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                    : "memory");
       fence_proxy_async_smem();
       __syncwarp();
+      load_next();
       // the weights' scales are there, and the MMAs of the round before are done with the TMEM columns
-      const bool ok = product_wait(smem_u32(&landed[mine][slot]), landed_phase, ab) && product_wait(empty0 + stage * 8, phase, ab);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!product_wait_all(smem_u32(&landed[mine][slot]), landed_phase, ab)) break;
+      if (!product_wait_all(empty0 + stage * 8, phase, ab)) break;
       tc_fence_after();
       const int n0 = at.ni * width;
       const bool two = (n0 & 127) + min(width, (p.N - n0 + 63) & ~63) > 128;
       const bool more = p.K - kb * kKStage > 128;  // than one 128-element group
       const uint32_t ta = tmem_sf + stage * sf_cols;
-      const uint64_t bsf = bsf0 + slot * (kScaleSlot >> 4);
+      const uint64_t bsf = bsf0 + slot * (kSfbBytes >> 4);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const bool go = leader && (j == 0 || more);
@@ -572,7 +574,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       slot ^= 1;
       landed_phase ^= slot == 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp >= kEpilogueWarp) {
     // quarter q: rows 32 q ..; four warps take the even units, four the odd ones (an
     // accumulator each): what a unit costs a warp besides its columns, some 650
@@ -728,12 +729,9 @@ extern "C" moe_status_t moe_expert_product(const moe_config_t* cfg, const void* 
 
   ProductMaps maps;
   const unsigned long long row_bytes = (unsigned long long)k / 2, rows = (unsigned long long)W * A;
-  const auto map_w = [&](CUtensorMap* m, unsigned box) {
-    return product_map(m, w, row_bytes, (unsigned long long)n, (unsigned long long)E, box);
-  };
   if (!product_map(&maps.x, x, row_bytes, rows, 0, kRowsBox) ||
       !scale_map(&maps.wsf, w_scales, (unsigned long long)(k + 127) / 128 * 512, (unsigned long long)E * ((n + 127) / 128)) ||
-      !map_w(&maps.w64, 64) || !map_w(&maps.w128, 128) || !map_w(&maps.w192, 192))
+      !product_map(&maps.w, w, row_bytes, (unsigned long long)n, (unsigned long long)E, 64))
     return MOE_ERR_CUDA;
   ProductParams p{};
   p.xs = x_scales;

@@ -88,6 +88,17 @@ def test_binding_refuses_cpu_tensors(lib):
         lib.mx_quantize(x, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))
 
 
+def test_binding_refuses_other_configurations(lib):
+    import torch
+    x, ids, w = torch.zeros(4, 64), torch.zeros(4, 8, dtype=torch.int32), torch.zeros(4, 8)
+    with pytest.raises(ValueError):
+        lib.route(lib.config(2, 4, 64, 2, 4, torch.bfloat16), x, None, ids, w)
+    with pytest.raises(TypeError):
+        lib.route(None, x, None, ids, w)
+    with pytest.raises(ValueError):
+        lib.expert_product(lib.router_config(4, 64, 8, torch.float32), x, x, ids, x, x, x, ws=x)
+
+
 def test_plain_quantiser_rounds_to_nearest_even():
     m = np.array([0.0, 0.25, 0.2501, 0.75, 0.7499, 1.25, 1.75, 2.5, 2.51, 3.5, 5.0, 5.01, 6.0, 7.9])
     assert P.nearest_code(m).tolist() == [0, 0, 1, 2, 1, 2, 4, 4, 5, 6, 6, 7, 7, 7]

@@ -610,6 +610,23 @@ def test_product_reports_bad_counts(bad):
     run_product(pr, "bf16", False, expect="BAD_ASSIST", ep=ep)
 
 
+def test_streams_by_object_and_by_handle():
+    rc = M.router_config(300, 64, 4, torch.float32)
+    x = torch.randn(300, 64, device="cuda")
+    got = []
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream, 0):
+        ids, w = torch.full((300, 4), -1, dtype=torch.int32, device="cuda"), torch.zeros(300, 4, device="cuda")
+        torch.cuda.synchronize()
+        M.route(rc, x, None, ids, w, stream=stream)
+        torch.cuda.synchronize()
+        got.append((ids, w))
+    assert all(torch.equal(a, got[0][0]) and torch.equal(b, got[0][1]) for a, b in got)
+    with pytest.raises((TypeError, AttributeError)):
+        M.route(rc, x, None, *got[0], stream="side")
+
+
 def test_product_passes_over_counts_that_overlap_many_times():
     """Counts that fall to zero and rise again at every other expert give some thousand row tiles, of a
     hundred that the units are numbered for."""
