@@ -7,10 +7,10 @@
 // reciprocal (within 2^-21 of the formula; equal logits and biases give equal keys),
 // and the lanes that end up with a pick compute its weight with expf and IEEE
 // division. Picking the K largest keys one by one costs a warp-wide argmax and a
-// rescan each (73 us where this takes 57, 65521 tokens x 256 experts); instead
-//   * the K-th largest of the 32 lanes' maxima, or a little less, bounds the K-th
-//     largest key from below, since at least K keys are not below it: found by
-//     halving an interval of keys, a ballot a step;
+// rescan each (73 us where this takes 56, 65521 tokens x 256 experts); instead
+//   * the K-th largest of the 32 lanes' maxima bounds the K-th largest key from below,
+//     since at least K keys are not below it: each lane counts the maxima ahead of
+//     its own;
 //   * the keys that reach it, mostly little more than K of them, are listed in shared
 //     memory by ballots, one a lane comes back, and each counts the keys ahead of it
 //     (larger, or equal with a lower index): its rank is its place in the output.
@@ -27,9 +27,14 @@
 namespace crs {
 
 constexpr int kRouterWarps = 4;
-// From here on two tokens a warp: 256 experts 6.3 us either way at 4096 tokens, 4.5
-// against 5.2 us at 2048, 57 against 44 us at 65521.
-constexpr int kPairTokens = 4096;
+// From here on two tokens a warp. One / two at 4096, 8192 and 65521 tokens: 256 experts in 8
+// groups 6.1 / 6.6, 10.1 / 9.2 and 56 / 44 us, 128 experts 4.5 / 4.4, 6.6 / 5.6 and 37 / 26 us, 256
+// experts without groups 4.6 / 6.6, 7.9 / 8.6 and 46 / 39 us.
+constexpr int kPairTokens = 8192;
+// The gradient's row is most of its work. One / two at 4096, 8192 and 65536 tokens: 128 experts 2.4 /
+// 2.2, 3.5 / 2.7 and 18.7 / 12.7 us, 256 experts (every gradient) 3.2 / 3.9, 4.9 / 5.4 and 32 / 28 us, the
+// two lines of which meet at some 16000.
+constexpr int kGradPairTokens = 4096, kGradPairTokensWide = 16384;
 constexpr int kBoundSteps = 12;    // halvings of the interval that a bound on the picks' keys is sought in
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -237,6 +242,7 @@ struct RouteScratch {
   float x[32 * EPL];
   unsigned long long order[32];
   int list[32];
+  uint32_t best[32];
 };
 
 template <int DT, int EPL>
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
     } else {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) top = fmaxf(top, x[j]);
-      top = warp_max(top);
+      top = key_value(__reduce_max_sync(kAll, ordered_number(top)));
       sum = 0.f;
       float v[EPL];
 #pragma unroll
@@ -334,16 +340,16 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
     }
     uint32_t bound = 1;  // fewer lanes than picks: every key that may be picked
     if (__popc(__ballot_sync(kAll, best != 0)) >= p.K) {
-      uint32_t high = __reduce_max_sync(kAll, best), low = __reduce_min_sync(kAll, best ? best : 0xffffffffu);
-      bound = low;  // reached by K lanes and more; high by fewer, or itself the bound
-      for (int i = 0; i < kBoundSteps && low < high; ++i) {
-        const uint32_t mid = low + (high - low) / 2 + 1;
-        const int reach = __popc(__ballot_sync(kAll, best >= mid));
-        if (reach >= p.K) low = mid;
-        else high = mid - 1;
-        if (reach == p.K) break;
+      // the least of the K largest lanes' maxima, each lane counting those ahead of its own
+      sc.best[lane] = best;
+      __syncwarp();
+      int ahead = 0;
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&sc.best[i]);
+        ahead += (o.x > best) + (o.y > best) + (o.z > best) + (o.w > best);
       }
-      bound = low;
+      bound = __reduce_min_sync(kAll, best && ahead < p.K ? best : 0xffffffffu);
     }
     uint32_t in = 0;
 #pragma unroll
@@ -422,8 +428,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
 // its experts' keys, rather more than half, is then spent once for two. The steps are
 // route_kernel's; where that asks the whole warp, the halves use shuffles within
 // themselves, and ranks by counting in place of repeated maxima. 65521 tokens: 256
-// experts in 8 groups 57 -> 44 us, 128 without groups 44 -> 26 us (64 registers; with
-// the 96 that the compiler would take, 56 us). Below some 4096 tokens there are warps
+// experts in 8 groups 56 -> 44 us, 128 without groups 37 -> 26 us (64 registers; with
+// the 96 that the compiler would take, 56 us). Below some 8192 tokens there are warps
 // enough for one token each, and those are done sooner.
 // A lane's experts lie kRow words from the next lane's (no bank conflicts).
 template <int EPL>
@@ -1004,7 +1010,7 @@ extern "C" moe_status_t moe_route_backward(const moe_router_config_t* rc, const 
   p.grad_logits = grad_logits;
   p.grad_stride = grad_stride;
   const int epl = lane_experts(p.E), pair_epl = 2 * epl;
-  if (p.T >= kPairTokens && p.K <= 16 && pair_epl >= 4 && pair_epl <= 16 &&
+  if (p.T >= (pair_epl > 8 ? kGradPairTokensWide : kGradPairTokens) && p.K <= 16 && pair_epl >= 4 && pair_epl <= 16 &&
       whole_lanes(logits, p.stride, p.E, pair_epl, (int)es, 16) &&
       whole_lanes(grad_logits, grad_stride, p.E, pair_epl, (int)es, 16)) {
     p.T_step = 2;

@@ -125,16 +125,16 @@ def test_route(case):
     check_route(x, bias, K, G, KG, sigmoid, top2, renorm, 2.5, DT[dt], pad)
 
 
-@pytest.mark.parametrize("case", [
-    # large batches take two tokens a warp: E, K, G, KG, sigmoid, top2, bias, renorm, dtype
+ROUTE_LARGE_CASES = [
+    # E, K, G, KG, sigmoid, top2, bias, renorm, dtype
     (256, 8, 8, 4, True, True, True, True, "f32"), (256, 16, 1, 1, False, False, False, True, "bf16"),
     (128, 8, 1, 1, False, False, False, True, "bf16"), (128, 6, 4, 2, False, False, True, False, "f16"),
     (64, 6, 1, 1, True, False, True, True, "f32"), (64, 4, 16, 4, True, True, False, False, "bf16"),
-    (256, 2, 2, 1, False, True, False, True, "f16"), (60, 4, 1, 1, False, False, False, True, "f32")],
-    ids=lambda c: "-".join(map(str, c)))
-def test_route_large_batches(case):
+    (256, 2, 2, 1, False, True, False, True, "f16"), (60, 4, 1, 1, False, False, False, True, "f32")]
+
+
+def check_large_batch(case, T):
     E, K, G, KG, sigmoid, top2, with_bias, renorm, dt = case
-    T = 4099  # an odd last token
     rng = np.random.default_rng(E + K)
     bias = np.round(rng.uniform(-0.1, 0.1, E), 3).astype(np.float32) if with_bias else None
     some = separated_logits(rng, 48, E, DT[dt], bias, sigmoid, K, G, KG, top2 and G > 1, masked=E // 16)
@@ -152,6 +152,16 @@ def test_route_large_batches(case):
         ri, rw = want[key]
         assert np.array_equal(ids[t], ri), (t, ids[t], ri)
         assert (np.abs(w[t] - rw) <= 128 * EPS * np.abs(rw) + 1e-37).all(), t  # spans of 20 and sums of 256 at most
+
+
+@pytest.mark.parametrize("case", ROUTE_LARGE_CASES, ids=lambda c: "-".join(map(str, c)))
+def test_route_large_batches(case):
+    check_large_batch(case, 4099)
+
+
+@pytest.mark.parametrize("case", ROUTE_LARGE_CASES, ids=lambda c: "-".join(map(str, c)))
+def test_route_batches_of_two_tokens_a_warp(case):
+    check_large_batch(case, 8195)  # an odd last token
 
 
 @pytest.mark.parametrize("E,K,G,KG", [(64, 8, 1, 1), (256, 8, 8, 4), (100, 10, 5, 2), (1024, 32, 4, 2)])
@@ -253,7 +263,16 @@ def test_route_backward(sigmoid, renorm, T, E, K, dt, pad):
 @pytest.mark.parametrize("sigmoid,renorm", list(itertools.product((False, True), (False, True))))
 @pytest.mark.parametrize("E,K,dt", [(256, 8, "f32"), (256, 16, "bf16"), (128, 8, "f16"), (64, 6, "f32"), (128, 4, "bf16")])
 def test_route_backward_large_batches(sigmoid, renorm, E, K, dt):
-    T = 4097
+    check_large_gradient(sigmoid, renorm, E, K, dt, 4097)
+
+
+@pytest.mark.parametrize("sigmoid,renorm", list(itertools.product((False, True), (False, True))))
+@pytest.mark.parametrize("E,K,dt", [(256, 8, "f32"), (256, 16, "bf16"), (256, 4, "f16"), (128, 8, "f32")])
+def test_route_backward_larger_batches(sigmoid, renorm, E, K, dt):
+    check_large_gradient(sigmoid, renorm, E, K, dt, 16387)
+
+
+def check_large_gradient(sigmoid, renorm, E, K, dt, T):
     rng = np.random.default_rng(E + K)
     x = rounded(rng.standard_normal((T, E)) * 2, DT[dt])
     x[7::50, : E // 4] = -np.inf
