@@ -607,10 +607,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           for (int j = 0; j < 32; ++j) {
             const float a = __uint_as_float(v[2 * j]), b = __uint_as_float(v[2 * j + 1]);
             // both within a few ulps (exp: plus |a| / 2^23 of its value), far below the rounding to 16 or 4
-            // bits that follows; the divisor stays within [1, 2], where the fast division holds (as a / (1 + exp(-a)),
+            // bits that follows; the divisor stays within [1, 2], where the fast reciprocal holds (as a / (1 + exp(-a)),
             // gates below -87 came out as 0, whatever they were to be multiplied by)
             const float t = __expf(-fabsf(a));
-            h[j] = __fdividef(a < 0.f ? a * t : a, 1.0f + t) * b;
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+            h[j] = (a < 0.f ? a * t : a) * r * b;
           }
           store_results<YT>(p, my_turn, un.row0 + 32 * q, rows, n / 2, h);
         } else {

@@ -7,7 +7,7 @@
 // reciprocal (within 2^-21 of the formula; equal logits and biases give equal keys),
 // and the lanes that end up with a pick compute its weight with expf and IEEE
 // division. Picking the K largest keys one by one costs a warp-wide argmax and a
-// rescan each (73 us where this takes 56, 65521 tokens x 256 experts); instead
+// rescan each (73 us where this took 57, 65521 tokens x 256 experts); instead
 //   * the K-th largest of the 32 lanes' maxima bounds the K-th largest key from below,
 //     since at least K keys are not below it: each lane counts the maxima ahead of
 //     its own;
@@ -28,8 +28,8 @@ namespace crs {
 
 constexpr int kRouterWarps = 4;
 // From here on two tokens a warp. One / two at 4096, 8192 and 65521 tokens: 256 experts in 8
-// groups 6.1 / 6.6, 10.1 / 9.2 and 56 / 44 us, 128 experts 4.5 / 4.4, 6.6 / 5.6 and 37 / 26 us, 256
-// experts without groups 4.6 / 6.6, 7.9 / 8.6 and 46 / 39 us.
+// groups 5.8 / 6.5, 9.6 / 8.1 and 52 / 39 us, 128 experts 4.6 / 4.2, 6.6 / 5.3 and 37 / 26 us, 256
+// experts without groups 4.6 / 6.5, 7.9 / 8.2 and 46 / 38 us.
 constexpr int kPairTokens = 8192;
 // The gradient's row is most of its work. One / two at 4096, 8192 and 65536 tokens: 128 experts 2.4 /
 // 2.2, 3.5 / 2.7 and 18.7 / 12.7 us, 256 experts (every gradient) 3.2 / 3.9, 4.9 / 5.4 and 32 / 28 us, the
@@ -95,6 +95,25 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // 1 / (1 + exp(-x)); the reciprocal rounded to nearest is the division's result.
 __device__ __forceinline__ float sigmoid_of(float x) { return __frcp_rn(__fadd_rn(1.f, expf(-x))); }
+
+// Scores for the keys: the special functions' exponential and reciprocal, subnormal numbers as
+// zeros (an exponential of those changes nothing next to 1, a score of those is far within
+// the keys' 2^-21). Their plain forms' care for subnormals cost a tenth of the time (44 -> 40 us).
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504088896f));  // 2^(-x / ln 2)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
+// A bias of NaN counts as -inf: then no sum with a score is NaN, or -0.
+__device__ __forceinline__ float load_bias(const float* bias, int e) {
+  const float b = __ldg(bias + e);
+  return b == b ? b : -INFINITY;
+}
+__device__ __forceinline__ uint32_t score_key(float x, float score, float bias) {
+  const uint32_t b = __float_as_uint(__fadd_rn(score, bias));
+  return x == -INFINITY ? kMaskedKey : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
 
 // The index of the largest key among a lane's best (key, index) pairs, the
 // lowest index among equal keys.
@@ -256,7 +275,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
   pdl_launch_dependents();
   float bias[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) bias[j] = p.bias && j < mine ? __ldg(p.bias + e0 + j) : 0.f;
+  for (int j = 0; j < EPL; ++j) bias[j] = p.bias && j < mine ? load_bias(p.bias, e0 + j) : 0.f;
   for (long long t = (long long)blockIdx.x * kRouterWarps + warp; t < p.T; t += (long long)gridDim.x * kRouterWarps) {
     float x[EPL];
     uint32_t key[EPL];
@@ -271,10 +290,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
     if (p.sigmoid) {
       if (by_score) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          const float s = __fdividef(1.f, 1.f + __expf(-x[j]));
-          key[j] = x[j] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(s, bias[j]));
-        }
+        for (int j = 0; j < EPL; ++j) key[j] = score_key(x[j], fast_sigmoid(x[j]), bias[j]);
       }
     } else {
 #pragma unroll
@@ -293,8 +309,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
       if (by_score) {
         const float share = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-          key[j] = x[j] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(__fmul_rn(v[j], share), bias[j]));
+        for (int j = 0; j < EPL; ++j) key[j] = score_key(x[j], __fmul_rn(v[j], share), bias[j]);
       }
     }
     if (!p.vec) {
@@ -428,8 +443,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_kernel(RouterParams p
 // its experts' keys, rather more than half, is then spent once for two. The steps are
 // route_kernel's; where that asks the whole warp, the halves use shuffles within
 // themselves, and ranks by counting in place of repeated maxima. 65521 tokens: 256
-// experts in 8 groups 56 -> 44 us, 128 without groups 37 -> 26 us (64 registers; with
-// the 96 that the compiler would take, 56 us). Below some 8192 tokens there are warps
+// experts in 8 groups 52 -> 39 us, 128 without groups 37 -> 26 us (seven CTAs an SM by
+// their registers; six take 41 us, eight 40, nine 43). Below some 8192 tokens there are warps
 // enough for one token each, and those are done sooner.
 // A lane's experts lie kRow words from the next lane's (no bank conflicts).
 template <int EPL>
@@ -454,7 +469,7 @@ __device__ __forceinline__ float half_sum(float v) {
 }
 
 template <int DT, int EPL>
-__global__ void __launch_bounds__(kRouterWarps * 32, 8) route_pair_kernel(RouterParams p) {
+__global__ void __launch_bounds__(kRouterWarps * 32, 7) route_pair_kernel(RouterParams p) {
   __shared__ alignas(16) PairScratch<EPL> scratch[kRouterWarps];
   using Scratch = PairScratch<EPL>;
   __shared__ alignas(16) float bias[16 * Scratch::kRow];
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, 8) route_pair_kernel(Router
   const bool by_score = p.bias || p.top2;
   pdl_wait();
   pdl_launch_dependents();
-  for (int e = threadIdx.x; e < 16 * EPL; e += kRouterWarps * 32) bias[Scratch::place(e)] = p.bias ? __ldg(p.bias + e) : 0.f;
+  for (int e = threadIdx.x; e < 16 * EPL; e += kRouterWarps * 32) bias[Scratch::place(e)] = p.bias ? load_bias(p.bias, e) : 0.f;
   __syncthreads();
   const bool plenty = 16 * p.KG / p.G >= 2 * p.K;  // open lanes for each pick
   const long long pairs = ((long long)p.T + 1) / 2;
@@ -510,10 +525,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, 8) route_pair_kernel(Router
           const float4 b = *reinterpret_cast<const float4*>(&bias[s0 + j]);
           const float bj[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float s = __fdividef(1.f, 1.f + __expf(-x[j + i]));
-            key[j + i] = x[j + i] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(s, bj[i]));
-          }
+          for (int i = 0; i < 4; ++i) key[j + i] = score_key(x[j + i], fast_sigmoid(x[j + i]), bj[i]);
         }
       }
     } else {
@@ -532,8 +544,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, 8) route_pair_kernel(Router
       if (by_score) {
         const float share = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-          key[j] = x[j] == -INFINITY ? kMaskedKey : ordered_key(__fadd_rn(__fmul_rn(v[j], share), bias[s0 + j]));
+        for (int j = 0; j < EPL; ++j) key[j] = score_key(x[j], __fmul_rn(v[j], share), bias[s0 + j]);
       }
     }
     uint32_t best = 0, next = 0;  // the lane's two largest
