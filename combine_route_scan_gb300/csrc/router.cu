@@ -681,40 +681,34 @@ __global__ void __launch_bounds__(kRouterWarps * 32, 7) route_pair_kernel(Router
   }
 }
 
-// A lane's EPL neighbouring gradients.
+// A lane's EPL neighbouring gradients, stored at once.
 template <int DT, int EPL>
-__device__ __forceinline__ void store_lane(void* row, int E, bool vec, int lane, const float (&x)[EPL]) {
-  const int e0 = lane * EPL;
+__device__ __forceinline__ void store_lane(void* row, int lane, const float (&x)[EPL]) {
   constexpr int kBytes = EPL * (DT == MOE_F32 ? 4 : 2);
-  if (vec) {
-    alignas(16) uint32_t w[(kBytes + 3) / 4] = {};
+  alignas(16) uint32_t w[(kBytes + 3) / 4] = {};
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      if (DT == MOE_F32) w[j] = __float_as_uint(x[j]);
-      else if (DT == MOE_BF16) w[j / 2] |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[j])) << (16 * (j & 1));
-      else w[j / 2] |= (uint32_t)__half_as_ushort(__float2half_rn(x[j])) << (16 * (j & 1));
-    }
-    uint8_t* q = static_cast<uint8_t*>(row) + (size_t)e0 * (DT == MOE_F32 ? 4 : 2);
-    if (kBytes >= 16) {
+  for (int j = 0; j < EPL; ++j) {
+    if (DT == MOE_F32) w[j] = __float_as_uint(x[j]);
+    else if (DT == MOE_BF16) w[j / 2] |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[j])) << (16 * (j & 1));
+    else w[j / 2] |= (uint32_t)__half_as_ushort(__float2half_rn(x[j])) << (16 * (j & 1));
+  }
+  uint8_t* q = static_cast<uint8_t*>(row) + (size_t)lane * kBytes;
+  if (kBytes >= 16) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) st_v4(q + i * 16, *reinterpret_cast<int4*>(&w[i * 4]));
-    } else if (kBytes == 8) {
-      *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[kBytes == 8 ? 1 : 0]);
-    } else if (kBytes == 4) {
-      *reinterpret_cast<uint32_t*>(q) = w[0];
-    } else {
-      *reinterpret_cast<uint16_t*>(q) = (uint16_t)w[0];
-    }
+    for (int i = 0; i < kBytes / 16; ++i) st_v4(q + i * 16, *reinterpret_cast<int4*>(&w[i * 4]));
+  } else if (kBytes == 8) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[kBytes == 8 ? 1 : 0]);
+  } else if (kBytes == 4) {
+    *reinterpret_cast<uint32_t*>(q) = w[0];
   } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (e0 + j < E) store_logit<DT>(row, e0 + j, x[j]);
+    *reinterpret_cast<uint16_t*>(q) = (uint16_t)w[0];
   }
 }
 
 // A row over LANES lanes, where it does not matter which of its elements a lane has: 16
 // bytes a lane in turn (neighbouring lanes' 32 bytes apart would fetch and write each
-// sector twice), or a lane's neighbouring ones where they are fewer, or not aligned.
+// sector twice), or a lane's neighbouring ones where they are fewer, or an element a lane in
+// turn where rows are not aligned (34056 rows of 425 gradients, bf16 78 -> 44 us, fp32 67 -> 28).
 template <int DT, int EPL, int LANES>
 __device__ __forceinline__ void load_row(const void* row, int E, bool vec, int lane, float (&x)[EPL]) {
   constexpr int kVec = DT == MOE_F32 ? 4 : 8;
@@ -730,7 +724,12 @@ __device__ __forceinline__ void load_row(const void* row, int E, bool vec, int l
       return;
     }
   }
-  load_lane<DT, EPL>(row, E, vec, lane, x);
+  if (vec) {
+    load_lane<DT, EPL>(row, E, true, lane, x);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) x[j] = j * LANES + lane < E ? load_logit<DT>(row, j * LANES + lane) : -INFINITY;
 }
 template <int DT, int EPL, int LANES>
 __device__ __forceinline__ void store_row(void* row, int E, bool vec, int lane, const float (&x)[EPL]) {
@@ -742,12 +741,18 @@ __device__ __forceinline__ void store_row(void* row, int E, bool vec, int lane, 
         float part[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) part[j] = x[i * kVec + j];
-        store_lane<DT, kVec>(static_cast<uint8_t*>(row) + i * LANES * 16, E, true, lane, part);
+        store_lane<DT, kVec>(static_cast<uint8_t*>(row) + i * LANES * 16, lane, part);
       }
       return;
     }
   }
-  store_lane<DT, EPL>(row, E, vec, lane, x);
+  if (vec) {
+    store_lane<DT, EPL>(row, lane, x);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j)
+    if (j * LANES + lane < E) store_logit<DT>(row, j * LANES + lane, x[j]);
 }
 
 template <int LANES>
