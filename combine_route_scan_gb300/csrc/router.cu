@@ -49,7 +49,7 @@ struct RouterParams {
   long long stride, grad_stride;
   int T, E, K, G, KG, top2, sigmoid, renorm;
   int T_step;        // tokens a warp takes at once
-  int vec, vec_out;  // whole lanes at once: E = 32 * EPL and rows aligned for it
+  int vec;           // whole lanes at once: E = 32 * EPL and the rows that are held by lanes aligned for it
   float scaling;
 };
 
@@ -709,6 +709,7 @@ __device__ __forceinline__ void store_lane(void* row, int lane, const float (&x)
 // bytes a lane in turn (neighbouring lanes' 32 bytes apart would fetch and write each
 // sector twice), or a lane's neighbouring ones where they are fewer, or an element a lane in
 // turn where rows are not aligned (34056 rows of 425 gradients, bf16 78 -> 44 us, fp32 67 -> 28).
+// `vec` says which, so a row that is loaded and stored has the same for both.
 template <int DT, int EPL, int LANES>
 __device__ __forceinline__ void load_row(const void* row, int E, bool vec, int lane, float (&x)[EPL]) {
   constexpr int kVec = DT == MOE_F32 ? 4 : 8;
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, LANES == 16 ? 6 : 1) route_
 #pragma unroll
       for (int j = 0; j < EPL; ++j) v[j] = 0.f;
     }
-    if (there) store_row<DT, EPL, LANES>(out, p.E, p.vec_out, lane, v);
+    if (there) store_row<DT, EPL, LANES>(out, p.E, p.vec, lane, v);
     __syncwarp();
     if (id >= 0) store_logit<DT>(out, id, d);
     load_chosen(t + step);
@@ -1025,19 +1026,23 @@ extern "C" moe_status_t moe_route_backward(const moe_router_config_t* rc, const 
   p.grad = grad_scales;
   p.grad_logits = grad_logits;
   p.grad_stride = grad_stride;
+  // the softmax's gradient loads the row that it stores: both in whole lanes, or neither
+  const bool dense = !p.sigmoid && !p.renorm;
+  const auto whole = [&](int epl, int lanes) {
+    return whole_lanes(grad_logits, grad_stride, p.E, epl, (int)es, lanes) &&
+           (!dense || whole_lanes(logits, p.stride, p.E, epl, (int)es, lanes));
+  };
   const int epl = lane_experts(p.E), pair_epl = 2 * epl;
   if (p.T >= (pair_epl > 8 ? kGradPairTokensWide : kGradPairTokens) && p.K <= 16 && pair_epl >= 4 && pair_epl <= 16 &&
-      whole_lanes(logits, p.stride, p.E, pair_epl, (int)es, 16) &&
-      whole_lanes(grad_logits, grad_stride, p.E, pair_epl, (int)es, 16)) {
+      whole(pair_epl, 16)) {
     p.T_step = 2;
-    p.vec = p.vec_out = 1;
+    p.vec = 1;
     return launch(rc->logits_dtype == MOE_F32   ? route_grad_pair_of<MOE_F32>(pair_epl)
                   : rc->logits_dtype == MOE_F16 ? route_grad_pair_of<MOE_F16>(pair_epl)
                                                 : route_grad_pair_of<MOE_BF16>(pair_epl),
                   p, 0, stream);
   }
-  p.vec = whole_lanes(logits, p.stride, p.E, epl, (int)es);
-  p.vec_out = whole_lanes(grad_logits, grad_stride, p.E, epl, (int)es);
+  p.vec = whole(epl, 32);
   return launch(rc->logits_dtype == MOE_F32   ? route_grad_of<MOE_F32>(epl)
                 : rc->logits_dtype == MOE_F16 ? route_grad_of<MOE_F16>(epl)
                                               : route_grad_of<MOE_BF16>(epl),

@@ -1,0 +1,81 @@
+"""Operators around the experts (include/moe_experts.h) at layouts and counts
+beside the usual ones: rows of logits and gradients aligned differently, batches
+of many experts, receive counts that are wrong in one place."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import experts_plain as P
+from test_experts_gpu import DT, EPS, HALF_ULP, rounded
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from combine_route_scan_gb300 import build as B
+    from combine_route_scan_gb300 import moe as M
+    B.build()
+
+
+# ------------------------------------------------------------------ the router's gradient
+
+def laid_out(T, E, dtype, pad, offset, fill):
+    """A [T, E] view whose rows are E + pad elements apart and begin `offset` elements behind an
+    allocation's start, and the whole of what it lies in."""
+    whole = torch.full((T * (E + pad) + offset,), fill, dtype=dtype, device="cuda")
+    return whole[offset:].view(T, E + pad)[:, :E], whole
+
+
+def gradient(x, ids, grad, sigmoid, renorm, scaling, dtype, logits_at, grad_at):
+    T, E = x.shape
+    logits, _ = laid_out(T, E, dtype, *logits_at, float("nan"))
+    logits.copy_(torch.from_numpy(x))
+    out, whole = laid_out(T, E, dtype, *grad_at, 7.0)
+    rc = M.router_config(T, E, ids.shape[1], dtype, score_func=int(sigmoid), renormalize=renorm, scaling=scaling,
+                         logits_stride=E + logits_at[0])
+    M.route_backward(rc, logits, torch.from_numpy(ids).cuda(), torch.from_numpy(grad).cuda(), out)
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    out.fill_(7.0)
+    assert bool((whole == 7.0).all())  # nothing was written beside the rows
+    return got
+
+
+def check_gradient(T, E, K, dt, sigmoid, renorm, logits_at, grad_at, tokens):
+    rng = np.random.default_rng(T + E + K)
+    x = rounded(rng.standard_normal((T, E)) * 2, DT[dt])
+    x[T // 2, rng.permutation(E)[: E // 4]] = -np.inf
+    ids = np.argsort(-x, axis=1, kind="stable")[:, :K].astype(np.int32)
+    grad = rng.standard_normal((T, K)).astype(np.float32)
+    got = gradient(x, ids, grad, sigmoid, renorm, 2.5, DT[dt], logits_at, grad_at)
+    for t in tokens:
+        want = P.route_gradient(x[t], ids[t], grad[t], sigmoid, renorm, 2.5)
+        # as in test_route_backward: terms of size share * (|g| + |mean|), exponentials of rounded
+        # differences, sums of E / 32 (E / 16 of two tokens a warp) and five numbers; the type's own rounding
+        s = P.scores(x[t], sigmoid)[0]
+        share = s / (s[ids[t]].sum() if renorm else 1.0)
+        fin = x[t][np.isfinite(x[t])]
+        tol = (2 * (fin.max() - fin.min()) + E / 16 + 48) * EPS * 2.5 * np.abs(grad[t]).max() * 2
+        assert (np.abs(got[t] - want) <= tol * share + HALF_ULP[dt] * np.abs(want) + 1e-7 * (dt == "f16") + 1e-30).all(), t
+
+
+# (pad, offset) of the logits and of the gradient, in elements
+LAYOUTS = [((0, 0), (1, 0)), ((1, 0), (0, 0)), ((0, 1), (0, 0)), ((0, 0), (0, 1)), ((32, 0), (0, 0)), ((1, 0), (3, 1))]
+
+
+@pytest.mark.parametrize("sigmoid,renorm", list(itertools.product((False, True), (False, True))))
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E", [32, 64, 128, 256, 512, 1024])
+@pytest.mark.parametrize("logits_at,grad_at", LAYOUTS)
+def test_gradient_rows_aligned_unlike_the_logits(logits_at, grad_at, E, dt, sigmoid, renorm):
+    check_gradient(5, E, 6, dt, sigmoid, renorm, logits_at, grad_at, range(5))
+
+
+@pytest.mark.parametrize("sigmoid,renorm", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("E,dt", [(256, "f32"), (128, "bf16")])
+@pytest.mark.parametrize("logits_at,grad_at", LAYOUTS[:4])
+def test_gradient_of_large_batches_aligned_unlike_the_logits(logits_at, grad_at, E, dt, sigmoid, renorm):
+    """Beyond the batches from which two tokens share a warp where both sides are aligned."""
+    T = 16387
+    check_gradient(T, E, 8, dt, sigmoid, renorm, logits_at, grad_at, [*range(20), *range(T // 2 - 5, T // 2 + 5), *range(T - 20, T)])
