@@ -583,7 +583,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * width;
     const uint32_t my_turn = smem_u32(turn) + (warp - kEpilogueWarp) * kTurnWarp;
     uint32_t done = 0;
-    for (ProductCursor at(n_tiles); at.u < units && !s_abort; at.next(), ++done) {
+    // ended by an abort at the wait alone, which answers for the whole warp: lanes that read the flag by themselves
+    // could part before the next ballot
+    for (ProductCursor at(n_tiles); at.u < units; at.next(), ++done) {
       if ((done & 1) != buf) continue;
       const ProductUnit un = product_unit(p, pre, at, width);
       if (!product_wait_warp(smem_u32(&acc_full[buf]), (done >> 1) & 1, ab)) break;
