@@ -3,7 +3,8 @@
 Each .cu file compiles to its own object in parallel with nvcc, then nvcc links
 them into combine_route_scan_gb300/_build/libcrs_moe.so. The CUDA runtime is
 linked statically. No cmake. Beside it _build/_bind.so, the native part of the
-binding (csrc/bind.cpp, g++), is built.
+binding (csrc/bind.cpp, g++), is built; where that cannot be, build() warns and the
+library serves every call but those of include/moe_experts.h, which raise.
 
 ``build(observer=True)`` builds the flag-observer test variant
 (_build/observer/libcrs_moe.so, ``-DMOE_FLAG_OBSERVER``): the dispatch payload
@@ -32,6 +33,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -89,6 +91,13 @@ def build_bind() -> str:
     return BIND
 
 
+def _try_bind() -> None:
+    try:
+        build_bind()
+    except Exception as e:  # no compiler, no headers: the library does without
+        warnings.warn(f"the calls of include/moe_experts.h are left without their binding: {e}", RuntimeWarning)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None, checked: bool = False,
           observer: bool = False, phase: bool = False) -> str:
     out_dir, lib = ((CHECKED_DIR, CHECKED_LIB) if checked else (OBSERVER_DIR, OBSERVER_LIB) if observer else
@@ -97,7 +106,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, checked:
     bind = force or _bind_stale()
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _inputs_mtime():
         if bind:
-            build_bind()
+            _try_bind()
         return lib
     cc = nvcc()
     flags = (NVCC_FLAGS + list(extra_flags or []) + (["-DMOE_BOUNDS_CHECK"] if checked else []) +
@@ -116,7 +125,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, checked:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        other = ex.submit(build_bind) if bind else None
+        other = ex.submit(_try_bind) if bind else None
         objs = list(ex.map(compile_one, sources()))
         if other:
             other.result()

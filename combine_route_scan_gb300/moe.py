@@ -118,13 +118,10 @@ _bind = None
 
 
 def _calls():
-    """The native module (csrc/bind.cpp) through which the calls of include/moe_experts.h go."""
-    lib()
-    return _bind
-
-
-def _load_bind(L):
+    """The native module (csrc/bind.cpp) through which the calls of include/moe_experts.h go; loaded
+    by the first of them (the calls of include/moe.h need the library alone)."""
     global _bind
+    L = lib()
     path = os.path.join(_HERE, "_build", "_bind.so")
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with combine_route_scan_gb300.build.build()")
@@ -133,6 +130,7 @@ def _load_bind(L):
     module.entries(*(ctypes.cast(f, ctypes.c_void_p).value
                      for f in (L.moe_route, L.moe_route_backward, L.moe_mx_quantize, L.moe_expert_product)))
     _bind = module
+    return module
 
 
 def lib() -> ctypes.CDLL:
@@ -165,7 +163,6 @@ def lib() -> ctypes.CDLL:
                   "moe_dispatch_ffn_combine", "moe_combine_noalloc", "moe_get_device_status", "moe_route",
                   "moe_route_backward", "moe_mx_quantize", "moe_expert_product"):
             getattr(L, f).restype = ctypes.c_int32
-        _load_bind(L)
         _lib = L
     return _lib
 

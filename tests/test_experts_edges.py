@@ -1,7 +1,12 @@
 """What of the operators around the experts can be looked over without a GPU,
-beside test_experts_abi.py: how their kernels leave a loop after an abort."""
+beside test_experts_abi.py: how their kernels leave a loop after an abort, and
+where their binding is needed."""
 import os
 import re
+import subprocess
+import sys
+
+import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "combine_route_scan_gb300", "csrc")
@@ -35,3 +40,44 @@ def test_product_waits_end_with_one_answer_for_the_warp():
         body = text[text.index(f"bool {name}(") :]
         body = body[: body.index("\n}")]
         assert re.search(r"return __all_sync\(0xffffffffu, \w+(\([^()]*\))?\);$", body.strip()), name
+
+
+# ------------------------------------------------------------------ the native binding
+
+def child(program):
+    r = subprocess.run([sys.executable, "-c", program], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+@pytest.fixture(scope="module")
+def build():
+    from combine_route_scan_gb300 import build
+    build.build()
+    return build
+
+
+def test_dispatch_and_combine_do_without_the_native_binding(build):
+    """The calls of include/moe.h need the library alone; those of include/moe_experts.h say what is missing."""
+    out = child("""
+import os.path, torch
+there = os.path.exists
+os.path.exists = lambda p: "_bind" not in str(p) and there(p)
+from combine_route_scan_gb300 import moe
+print(moe.workspace_size(moe.config(2, 4, 64, 2, 4, torch.bfloat16))[1])
+try:
+    moe.route(moe.router_config(4, 64, 8, torch.float32), torch.zeros(4, 64), None, None, None)
+except RuntimeError as e:
+    print("missing" in str(e))
+""")
+    assert out.split() == ["16", "True"]
+
+
+def test_library_is_built_where_the_binding_cannot_be(build, monkeypatch):
+    def fail():
+        raise RuntimeError("no Python.h")
+
+    monkeypatch.setattr(build, "_bind_stale", lambda: True)
+    monkeypatch.setattr(build, "build_bind", fail)
+    with pytest.warns(RuntimeWarning, match="no Python.h"):
+        assert build.build() == build.LIB
