@@ -2,8 +2,9 @@
 
 Each .cu file compiles to its own object in parallel with nvcc, then nvcc links
 them into combine_route_scan_gb300/_build/libcrs_moe.so. The CUDA runtime is
-linked statically. No cmake. Beside it _build/_bind.so, the native part of the
-binding (csrc/bind.cpp, g++), is built; where that cannot be, build() warns and the
+linked statically. No cmake. Beside it the native part of the binding
+(csrc/bind.cpp, g++) is built, under a name that holds the versions of Python and
+torch that it is linked to (bind_path); where that cannot be, build() warns and the
 library serves every call but those of include/moe_experts.h, which raise.
 
 ``build(observer=True)`` builds the flag-observer test variant
@@ -44,7 +45,6 @@ CHECKED_LIB = os.path.join(CHECKED_DIR, "libcrs_moe.so")
 OBSERVER_DIR = os.path.join(OUT_DIR, "observer")
 OBSERVER_LIB = os.path.join(OBSERVER_DIR, "libcrs_moe.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
-BIND = os.path.join(OUT_DIR, "_bind.so")
 PHASE_DIR = os.path.join(OUT_DIR, "phase")
 PHASE_LIB = os.path.join(PHASE_DIR, "libcrs_moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -70,15 +70,24 @@ def _inputs_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def bind_path() -> str:
+    """Where the native part of the binding is for this Python and this torch, whose C++ symbols it
+    uses: another version has a file of its own, and none until build() makes it."""
+    import torch
+    return os.path.join(OUT_DIR, f"_bind.{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}.so")
+
+
 def _bind_stale() -> bool:
+    path = bind_path()
     files = [BIND_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h"))]
-    return not os.path.exists(BIND) or os.path.getmtime(BIND) < max(os.path.getmtime(f) for f in files)
+    return not os.path.exists(path) or os.path.getmtime(path) < max(os.path.getmtime(f) for f in files)
 
 
 def build_bind() -> str:
-    """The CPython module _build/_bind.so, against the headers of Python, CUDA and torch."""
+    """The CPython module _bind at bind_path(), against the headers of Python, CUDA and torch."""
+    path = bind_path()
     torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
-    tmp = BIND + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     os.makedirs(OUT_DIR, exist_ok=True)
     cmd = [os.environ.get("CXX") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-I{torch_dir}/include",
            f"-I{torch_dir}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
@@ -87,8 +96,8 @@ def build_bind() -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, path)
+    return path
 
 
 def _try_bind() -> None:

@@ -19,6 +19,8 @@ from typing import Optional
 
 import torch
 
+from .build import bind_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # CRS_MOE_CHECKED=1 selects the bounds-checked build (build.build(checked=True)),
 # CRS_MOE_OBSERVER=1 the flag-observer test build (build.build(observer=True)),
@@ -122,7 +124,7 @@ def _calls():
     by the first of them (the calls of include/moe.h need the library alone)."""
     global _bind
     L = lib()
-    path = os.path.join(_HERE, "_build", "_bind.so")
+    path = bind_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with combine_route_scan_gb300.build.build()")
     spec = importlib.util.spec_from_file_location("_bind", path)

@@ -81,3 +81,16 @@ def test_library_is_built_where_the_binding_cannot_be(build, monkeypatch):
     monkeypatch.setattr(build, "build_bind", fail)
     with pytest.warns(RuntimeWarning, match="no Python.h"):
         assert build.build() == build.LIB
+
+
+def test_binding_of_another_torch_is_not_taken_for_this_one(build, monkeypatch):
+    import torch
+    assert not build._bind_stale()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert build._bind_stale()
+
+
+def test_binding_of_another_python_is_not_taken_for_this_one(build, monkeypatch):
+    there = build.sysconfig.get_config_var
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else there(name))
+    assert build._bind_stale()
