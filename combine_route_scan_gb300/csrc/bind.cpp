@@ -171,13 +171,14 @@ PyObject* mx_quantize(PyObject* const* a) {
   const int64_t rows = x.size(-2), cols = x.size(-1), experts = x.dim() == 3 ? x.size(0) : 1;
   if (cols > 1 && x.stride(-1) != 1) refuse("x", "expected contiguous rows");
   if (cols != (int32_t)cols || experts != (int32_t)experts) refuse("x", "sizes beyond 32 bits");
-  const int64_t layout = integer(a[3]), blocks = (cols + 31) / 32;
+  const int32_t layout = integer32(a[3], "layout");
+  const int64_t blocks = (cols + 31) / 32;
   void* codes = typed(a[1], at::kByte, experts * rows * (cols / 2), "codes");
   void* scales = typed(a[2], at::kByte,
                        layout == MOE_SF_ROWS ? experts * rows * blocks : experts * ((rows + 127) / 128) * ((blocks + 3) / 4) * 512,
                        "scales");
   return enqueue(mx_quantize_entry, static_cast<const void*>(x.data_ptr()), dtype, (int32_t)experts, rows, (int32_t)cols,
-                 rows > 1 ? x.stride(-2) : cols, x.dim() == 3 ? x.stride(0) : 0, (int32_t)layout,
+                 rows > 1 ? x.stride(-2) : cols, x.dim() == 3 ? x.stride(0) : 0, layout,
                  static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), stream_of(a[4]));
 }
 

@@ -79,3 +79,17 @@ def test_gradient_of_large_batches_aligned_unlike_the_logits(logits_at, grad_at,
     """Beyond the batches from which two tokens share a warp where both sides are aligned."""
     T = 16387
     check_gradient(T, E, 8, dt, sigmoid, renorm, logits_at, grad_at, [*range(20), *range(T // 2 - 5, T // 2 + 5), *range(T - 20, T)])
+
+
+# ------------------------------------------------------------------ the quantiser's layouts
+
+def test_quantiser_refuses_layouts_that_there_are_not():
+    """One beyond 32 bits is not cut to one that there is."""
+    x = torch.randn(4, 64, device="cuda")
+    codes, scales = M.alloc_mx(x, M.SF_TILED)
+    for layout in (1 << 32, (1 << 32) + 1, -(1 << 32)):
+        with pytest.raises(ValueError, match="layout"):
+            M.mx_quantize(x, codes, scales, layout)
+    for layout in (2, -1):
+        with pytest.raises(M.MoeError, match="INVALID_ARG"):
+            M.mx_quantize(x, codes, scales, layout)
