@@ -140,7 +140,8 @@ enum {
  *                 the intermediate size for rows of this function's MOE_MXFP4 output)
  *   x             [W][A][k / 2] codes (A from moe_get_workspace_size), 16-byte aligned
  *   x_scales      [W][A][k / 32] E8M0 bytes, 4-byte aligned
- *   ep_recv_count [W][L*W] as moe_dispatch wrote it
+ *   ep_recv_count [W][L*W] as moe_dispatch wrote it; of an expert's W running counts only the last, at
+ *                 its rows' end, is read
  *   w             [E][n][k / 2] codes, 16-byte aligned
  *   w_scales      MOE_SF_TILED scales of w (moe_mx_quantize with experts = E, rows = n,
  *                 cols = k), 16-byte aligned
@@ -149,11 +150,11 @@ enum {
  *                 and codes are taken from the fp32 results); 16-byte aligned
  *   y_scales      [W][A][ceil(c / 32)] E8M0 bytes for MOE_MXFP4, else NULL
  *   ws            the workspace that the dispatch used (it holds the status word)
- * Rows at or beyond ep_recv_count[d][L*W-1] are left untouched. A count that is
- * negative, decreasing or above A is reported as MOE_ERR_BAD_ASSIST, and that
- * expert's rows are passed over (all rows, where the counts left overlap to more
- * 128-row tiles than counts of dispatch can have); a wait that ran out as
- * MOE_ERR_TIMEOUT. */
+ * Rows at or beyond ep_recv_count[d][L*W-1] are left untouched. An expert whose
+ * count at its rows' begin or end is negative, decreasing or above A is reported
+ * as MOE_ERR_BAD_ASSIST, and its rows are passed over (all rows, where the counts
+ * left overlap to more 128-row tiles than counts of dispatch can have); a wait that
+ * ran out as MOE_ERR_TIMEOUT. */
 moe_status_t moe_expert_product(const moe_config_t* cfg, const void* x, const uint8_t* x_scales,
                                 const int32_t* ep_recv_count, const void* w, const uint8_t* w_scales, int32_t n,
                                 int32_t k, int32_t epilogue, int32_t y_dtype, void* y, uint8_t* y_scales, void* ws,

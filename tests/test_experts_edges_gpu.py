@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import experts_plain as P
-from test_experts_gpu import DT, EPS, HALF_ULP, rounded
+from test_experts_gpu import DT, EPS, HALF_ULP, Product, product_want, rounded, run_product
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,53 @@ def test_quantiser_refuses_layouts_that_there_are_not():
     for layout in (2, -1):
         with pytest.raises(M.MoeError, match="INVALID_ARG"):
             M.mx_quantize(x, codes, scales, layout)
+
+
+# ------------------------------------------------------------------ the product's receive counts
+
+def check_experts(pr, y, swiglu, dt, refused=()):
+    """The refused experts' rows, and those beyond the counts, hold what they held; the others the product."""
+    fill = torch.ones(pr.W, pr.A, dtype=torch.bool)
+    for e, (d, lo, hi) in enumerate(pr.ranges):
+        if e in refused or hi == lo:
+            continue
+        fill[d, lo:hi] = False
+        want, tol = product_want(pr, e, swiglu)
+        got = y[d, lo:hi].double().cpu().numpy()
+        assert (np.abs(got - want) <= tol + HALF_ULP[dt] * (np.abs(want) + tol) + 1e-40).all(), e
+    assert bool((y.cpu()[fill] == 777.0).all())
+
+
+@pytest.mark.parametrize("bad,refused", [("above", (3,)), ("above inside", (0, 1)), ("negative", (0, 1)), ("decreasing", (1,))])
+def test_product_leaves_out_the_experts_of_bad_counts_alone(bad, refused):
+    pr = Product(2, 8, 2, [3, 4, 5, 6], 64, 64, seed=2)
+    ep = pr.ep.copy()  # [rank][expert, source]: an expert's end is its second entry
+    if bad == "above":
+        ep[1, 3] = pr.A + 1
+    elif bad == "above inside":
+        ep[0, 1] = pr.A + 1
+    elif bad == "negative":
+        ep[0, 1] = -1
+    else:
+        ep[0, 3] = ep[0, 1] - 1
+    y, _ = run_product(pr, "bf16", False, expect="BAD_ASSIST", ep=ep)
+    check_experts(pr, y, False, "bf16", refused)
+
+
+def test_product_reads_the_counts_at_the_experts_ends_alone():
+    pr = Product(4, 8, 2, [3, 4, 5, 6, 0, 16, 1, 2], 64, 64, seed=6)
+    ep = pr.ep.copy()
+    ep.reshape(4, 2, 4)[..., :3] = np.array([-5, 1 << 30, 7])
+    y, _ = run_product(pr, "bf16", False, ep=ep)
+    check_experts(pr, y, False, "bf16")
+
+
+@pytest.mark.parametrize("E,swiglu", [(450, False), (512, True), (1024, False)])
+def test_product_of_more_experts_than_threads(E, swiglu):
+    """Their running row tiles take more than one pass of a CTA's 448 threads; rows on either side of its end."""
+    rng = np.random.default_rng(E)
+    counts = rng.integers(0, 4, E)
+    counts[[0, 446, 447, 448, E - 1]] = 131, 5, 130, 3, 129
+    pr = Product(2, 300, 2, counts.tolist(), 66, 96, seed=E)
+    y, _ = run_product(pr, "bf16", swiglu)
+    check_experts(pr, y, swiglu, "bf16")
