@@ -574,6 +574,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       slot ^= 1;
       landed_phase ^= slot == 0;
     }
+    // the last stage's arrival: the MMAs' end, which the kernel waits for, does not say that it has come
+    product_wait_all(smem_u32(&taken[mine]), taken_phase, ab);
   } else if (warp >= kEpilogueWarp) {
     // quarter q: rows 32 q ..; four warps take the even units, four the odd ones (an
     // accumulator each): what a unit costs a warp besides its columns, some 650

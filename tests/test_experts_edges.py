@@ -42,6 +42,14 @@ def test_product_waits_end_with_one_answer_for_the_warp():
         assert re.search(r"return __all_sync\(0xffffffffu, \w+(\([^()]*\))?\);$", body.strip()), name
 
 
+def test_product_waits_for_every_arrival_of_its_scale_warps():
+    """Each of their commits arrives on a barrier in shared memory: the last one before the block ends, too."""
+    text = code("expert_product.cu")
+    body = text[text.index("} else if (warp < 2 + kScaleWarps) {") : text.index("} else if (warp >= kEpilogueWarp) {")]
+    behind = body[body.rindex("tc_commit_if(leader, smem_u32(&taken[mine]));") :]
+    assert "product_wait_all(smem_u32(&taken[mine]), taken_phase, ab)" in behind
+
+
 # ------------------------------------------------------------------ the native binding
 
 def child(program):
