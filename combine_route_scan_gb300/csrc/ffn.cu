@@ -247,12 +247,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     const int q = warp & 3;
     const int feat = 32 * q + lane;
     uint32_t acc = 0;
-    for (int u = blockIdx.x; u < n_units && !s_abort; u += gridDim.x) {
+    // an abort ends the loops for the whole warp at once: the loads from tensor memory want all lanes
+    bool cut = false;
+    for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
       const Unit un = unit_of(p, u);
       const int passes = (un.n_e + kNP - 1) / kNP;
-      for (int ps = 0; ps < passes && !s_abort; ++ps, ++acc) {
+      for (int ps = 0; ps < passes; ++ps, ++acc) {
         const uint32_t buf = acc & 1u;
-        if (!wait_or_abort(&acc_full[buf], (acc >> 1) & 1u, p, &s_abort)) break;
+        cut = !__all_sync(0xffffffffu, wait_or_abort(&acc_full[buf], (acc >> 1) & 1u, p, &s_abort));
+        if (cut) break;
         tc_fence_after();
         const int n_rem = min(kNP, un.n_e - ps * kNP);
         const int chunks = (n_rem + 15) >> 4;
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         tc_fence_before();
         mbar_arrive(&acc_empty[buf]);
       }
+      if (cut) break;
       if (un.mode == FFN_GATE_UP && passes > 0) {
         // this warp's h1 columns of the unit are stored: make them visible (to
         // the async proxy too: down units read them by TMA), then count them

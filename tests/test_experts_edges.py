@@ -34,6 +34,18 @@ def test_product_epilogue_leaves_its_loop_as_a_whole_warp():
     assert unvoted(loop) == []
 
 
+def test_ffn_epilogue_leaves_its_loops_as_a_whole_warp():
+    """Its tensor-memory loads want all lanes, as the product's votes do; and a unit that an abort cut off
+    is not counted as stored."""
+    text = code("ffn.cu")
+    body = text[text.index("const int feat = 32 * q + lane;") :]
+    loop = body[: body.index("tmem_dealloc(")]
+    loop = loop[: loop.rindex("__syncthreads();")]
+    assert "tc_ld16(" in loop and "wait_or_abort(" in loop
+    assert unvoted(loop) == []
+    assert loop.index("if (cut) break;") < loop.index("red.release")
+
+
 def test_product_waits_end_with_one_answer_for_the_warp():
     text = code("expert_product.cu")
     for name in ("product_wait_warp", "product_wait_all"):
