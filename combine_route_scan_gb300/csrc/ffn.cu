@@ -310,6 +310,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (s_abort) {
+    // copies and MMAs under way, which nobody waits for then, end before their memory is given back
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {}
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

@@ -46,6 +46,15 @@ def test_ffn_epilogue_leaves_its_loops_as_a_whole_warp():
     assert loop.index("if (cut) break;") < loop.index("red.release")
 
 
+def test_ffn_lets_its_copies_end_after_an_abort():
+    """Nobody waits for the copies and MMAs under way then: the block does, for a bounded time, before its
+    shared and tensor memory are given back."""
+    text = code("ffn.cu")
+    end = text[text.index("const int feat = 32 * q + lane;") : text.index("tmem_dealloc(tmem, kTmemCols);")]
+    behind = end[end.rindex("__syncthreads();") :]
+    assert re.search(r"if \(s_abort\) \{[^}]*globaltimer_ns\(\) - t0 < \d+ull", behind)
+
+
 def test_product_waits_end_with_one_answer_for_the_warp():
     text = code("expert_product.cu")
     for name in ("product_wait_warp", "product_wait_all"):
