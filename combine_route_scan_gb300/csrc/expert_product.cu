@@ -35,6 +35,7 @@
 #include <mutex>
 
 #include "../../include/moe_experts.h"
+#include "experts_host.h"
 #include "quant_common.cuh"
 #include "tcgen05.cuh"
 

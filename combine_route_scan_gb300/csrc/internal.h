@@ -188,11 +188,6 @@ struct FfnLaunch {
 // microseconds; the answer is cached per (device, kernel, threads, smem).
 cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* per_sm);
 
-// SMs of the current device (0 when the query fails); cached per device.
-int num_sms_of_current_device();
-// n more kernels were enqueued (moe_launch_count).
-void note_launches(int n);
-
 // True when the TMA scatter's shared-memory ring fits for this shape.
 bool scatter_tma_fits(const Shape& sh);
 // The quantising scatter (every quant_mode but 0) and its fit test.

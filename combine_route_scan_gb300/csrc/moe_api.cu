@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "experts_host.h"
 #include "internal.h"
 
 namespace crs {

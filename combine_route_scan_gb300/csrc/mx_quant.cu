@@ -12,6 +12,7 @@
 // of a row, two at a time, a pair of elements a lane. (64 x 1024 rows of 2048 bf16
 // 55 us, 6.2 TB/s; of 2046 114 us; as pairs all would take the latter.)
 #include "../../include/moe_experts.h"
+#include "experts_host.h"
 #include "quant_common.cuh"
 
 namespace crs {

@@ -23,6 +23,7 @@
 
 #include "../../include/moe_experts.h"
 #include "common.cuh"
+#include "experts_host.h"
 
 namespace crs {
 
