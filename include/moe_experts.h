@@ -58,15 +58,20 @@ typedef struct {
  *          keys and equal groups go to the lower index, so masked experts are
  *          picked last, and the ids of a token are always distinct and valid.
  *   weight w_k = scaling * s_k / (renormalize ? sum_j s_j : 1), zeros where
- *          that sum is 0 (a token whose picks are all masked).
+ *          that sum is 0 (a token whose picks are all masked, or all have sigmoid
+ *          scores below those of fp32's exponential: logits under -88).
  *
  *   logits        [T] rows of E elements, logits_stride apart, aligned to the element
  *   bias          NULL or [E] fp32; it moves the choice, not the weights
  *   expert_ids    [T][K] int32 (moe_dispatch's expert_ids, with T = W * bs)
  *   expert_scales [T][K] fp32  (moe_dispatch's and moe_combine's expert_scales)
- * Weights are computed in fp32 with expf and IEEE division. Keys that hold scores
- * are within 2^-21 of the formula's (experts of equal logit and bias have equal
- * keys): experts whose keys are nearer than that may be chosen either way. */
+ * Weights are computed in fp32 with expf and IEEE division. Scores in keys come from
+ * faster functions: within 2^-21 of the formula's, and within 2^-16 of their own size
+ * down to 2^-126 (smaller ones may count as 0); experts of equal logit and bias have
+ * equal keys. Experts whose keys are nearer than that may be chosen either way.
+ * A token's sums run in an order that depends on the batch's size and alignment (in
+ * large batches two tokens share a warp): the last bits of its softmax weights, and
+ * choices as near as that, may differ from those of another batch. */
 moe_status_t moe_route(const moe_router_config_t* rc, const void* logits, const float* bias, int32_t* expert_ids,
                        float* expert_scales, void* stream);
 
@@ -79,6 +84,7 @@ moe_status_t moe_route(const moe_router_config_t* rc, const void* logits, const 
  * at the chosen experts, zero elsewhere, and
  *   softmax, not renormalised  d_e = s_e * (g_e - sum_j g_j s_j), g_e = 0 where e
  *                              was not chosen, at every expert.
+ * It is taken in fp32 (zeros where a renormalised token's scores sum to 0).
  * Masked experts get zero, and what grad_scales holds at masked picks (infinities
  * and NaN included) is not used. expert_ids as moe_route gave them; an id outside
  * [0, E) is passed over, ids repeated in a token give unspecified values.
@@ -132,7 +138,8 @@ enum {
  * ep_recv_count gives to local expert le (expert e = d * L + le),
  *   z[r][j] = sum over i of x[r][i] * w[e][j][i]
  * with x and w the MX FP4 values, on the tensor cores' block-scaled path with
- * fp32 accumulation, then the epilogue in fp32, rounded once to y_dtype.
+ * fp32 accumulation, then the epilogue in fp32, rounded once to y_dtype. silu takes
+ * the fast exponential and reciprocal: within 2^-16 of its size for gates above -87.
  *
  *   cfg           the dispatch's configuration: W, bs, topk, E, wait_timeout_us and
  *                 the workspace size are taken from it; h, types and modes are not

@@ -143,3 +143,55 @@ def test_product_of_more_experts_than_threads(E, swiglu):
     pr = Product(2, 300, 2, counts.tolist(), 66, 96, seed=E)
     y, _ = run_product(pr, "bf16", swiglu)
     check_experts(pr, y, swiglu, "bf16")
+
+
+# ------------------------------------------------------------------ scores of small size
+
+def far_below(rng, T, E, K, G, KG):
+    """fp32 logits whose sigmoid scores are all below 2^-28, those that the choice hangs on 2^-15 of their
+    size apart: twice what two keys are off."""
+    out = np.empty((T, E))
+    for t in range(T):
+        while True:
+            x = rounded(np.clip(rng.standard_normal(E) * 6 - 50, -80, -20), torch.float32)
+            _, key = P.keys(x, None, True, True)
+            v = P.group_values(key, G, True)
+            opened = sorted(range(G), key=lambda g: (-v[g], g))[:KG]
+            left = np.sort(key[np.isin(np.arange(E) // (E // G), opened)])[::-1][: K + 1]
+            ordered = np.sort(v)[::-1]
+            if all(((a[:-1] - a[1:]) > 2.0 ** -15 * a[:-1]).all() for a in (left, ordered)):
+                break
+        out[t] = x
+    return out
+
+
+@pytest.mark.parametrize("T,E,K,G,KG", [(40, 64, 6, 4, 2), (40, 256, 8, 8, 4), (40, 60, 5, 6, 3), (8195, 256, 8, 8, 4), (8195, 128, 4, 2, 1)])
+def test_route_by_scores_far_below_one(T, E, K, G, KG):
+    """Keys of scores alone order by their own size, not by how near to one another they are."""
+    rng = np.random.default_rng(E + T)
+    some = far_below(rng, min(T, 64), E, K, G, KG)
+    x = some[np.arange(T) % len(some)]
+    logits = torch.from_numpy(x).float().cuda()
+    rc = M.router_config(T, E, K, torch.float32, G, KG, M.GROUP_TOP2_SUM, M.SCORE_SIGMOID, True, 1.0)
+    ids = torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, K), float("nan"), device="cuda")
+    M.route(rc, logits, None, ids, w)
+    want = [P.route_token(r, None, K, G, KG, True, True, True, 1.0) for r in some]
+    ids, w = ids.cpu().numpy(), w.double().cpu().numpy()
+    for t in range(T):
+        ri, rw = want[t % len(some)]
+        assert np.array_equal(ids[t], ri), t
+        assert (np.abs(w[t] - rw) <= 64 * EPS * rw).all(), t  # exponentials, a sum and a division of some ulps each
+
+
+@pytest.mark.parametrize("T", [3, 8193])
+def test_renormalised_weights_and_gradient_of_scores_below_fp32(T):
+    """Sigmoid scores of logits under -88 are 0 in fp32: the picks go by the logits, their weights and gradients are 0."""
+    x = -95.0 - torch.arange(128, device="cuda").flip(0).float()[None] / 8 + torch.zeros(T, 1, device="cuda")
+    rc = M.router_config(T, 128, 4, torch.float32, score_func=M.SCORE_SIGMOID)
+    ids, w = torch.zeros(T, 4, dtype=torch.int32, device="cuda"), torch.full((T, 4), float("nan"), device="cuda")
+    M.route(rc, x, None, ids, w)
+    assert bool((ids == torch.tensor([127, 126, 125, 124], device="cuda")).all()) and bool((w == 0).all())
+    g = torch.full_like(x, 7.0)
+    M.route_backward(rc, x, ids, torch.ones_like(w), g)
+    assert bool((g == 0).all())
