@@ -106,3 +106,31 @@ def test_logits_gradient_of_a_step():
     for t in range(len(ids)):
         want = P.route_gradient(lg[t], ids[t], g[t], False, False, 1.0)
         assert np.allclose(got[t], want, rtol=0, atol=2.0 ** -18 * np.abs(g[t]).max())
+
+
+def test_layer_with_groups_and_a_bias():
+    """The router's groups and balancing bias reach the layer's choice, its weights the output."""
+    from test_experts_gpu import separated_logits
+    rng = np.random.default_rng(12)
+    W, bs, h, E, K, I = 4, 12, 256, 16, 3, 64
+    bias = np.round(rng.uniform(-0.1, 0.1, E), 3).astype(np.float32)
+    router = dict(score_func=M.SCORE_SIGMOID, group_num=4, topk_group=2, group_score=M.GROUP_TOP2_SUM, scaling=2.5)
+    layer, x, _, (wg, wu, wd) = make(W, bs, h, E, K, I, seed=12, bias=torch.from_numpy(bias).cuda(), router=router)
+    lg = separated_logits(rng, W * bs, E, torch.float32, bias, True, K, 4, 2, True)
+    out = layer(x, torch.from_numpy(lg).float().cuda())
+    assert M.get_device_status(layer.ws) == 0
+    ids, weights = layer.ids.cpu().numpy().reshape(-1, K), layer.weights.double().cpu().numpy().reshape(-1, K)
+    for t in range(W * bs):
+        ri, rw = P.route_token(lg[t], bias, K, 4, 2, True, True, True, 2.5)
+        assert np.array_equal(ids[t], ri)
+        assert np.allclose(weights[t], rw, rtol=2.0 ** -18)
+    cfg = M.config(W, bs, h, K, E, torch.bfloat16, ffn_intermediate=128)
+    # the bf16 layer wants 128 features: the others' weights are zeros
+    pad = lambda w: torch.nn.functional.pad(w, (0, 0, 0, 128 - I))  # noqa: E731
+    ws = M.alloc_workspace(cfg)
+    want = torch.empty_like(x)
+    M.dispatch_ffn_combine(cfg, x, layer.ids, None, layer.weights, pad(wg).contiguous(), pad(wu).contiguous(),
+                           torch.nn.functional.pad(wd, (0, 128 - I)).contiguous(), want, ws)
+    assert M.get_device_status(ws) == 0
+    # as in test_layer_near_the_bf16_layer
+    assert float((out.float() - want.float()).norm() / want.float().norm()) < 1 / 3
