@@ -52,7 +52,6 @@ NOALLOC_MAX_PICKS = 262144
 
 MOE_F32, MOE_MXFP4 = 3, 4
 FLOAT_CODE = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
-FLOAT_TYPE = {code: dtype for dtype, code in FLOAT_CODE.items()}
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2_SUM = 0, 1
 SF_ROWS, SF_TILED = 0, 1
