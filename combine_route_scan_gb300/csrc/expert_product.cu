@@ -109,7 +109,8 @@ __device__ __forceinline__ ProductShape product_shape(int N, int E, int m_tiles,
   // many, its rows and weights come from L2 and a wider unit saves rows. Measured
   // with 64 / 128 / 192 weight rows: 8 rows of 8 experts 5.9 / 6.2 / 6.9 us, 32 rows an
   // expert 30.9 / 27.6 / 28.7 us, 128 rows (k 7168) 239 / 182 / 188 us, 1024 rows 224 /
-  // 137 / 124 us.
+  // 137 / 124 us (short runs; at the power limit the last takes 137 us). Between one tile an expert and eight
+  // nothing was measured, nor batches whose rows are with a few of the experts.
   const bool streams = m_tiles < 3 * E;
   for (int b = kMaxBoxes; b >= 1; --b) {
     const uint32_t units = (uint32_t)m_tiles * (uint32_t)((N + 64 * b - 1) / (64 * b));

@@ -10,7 +10,7 @@
 // on them: 223 us for 128 x 1024 x 2048 bf16.) Rows that 16-byte loads do not fit, or
 // that end inside a block, go through mx_quantize_pairs_kernel: a warp takes 16 blocks
 // of a row, two at a time, a pair of elements a lane. (64 x 1024 rows of 2048 bf16
-// 55 us, 6.2 TB/s; of 2046 114 us; as pairs all would take the latter.)
+// 52 us, 6.5 TB/s; of 2046 104 us; as pairs all would take the latter.)
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "quant_common.cuh"

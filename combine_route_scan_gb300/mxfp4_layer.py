@@ -5,7 +5,8 @@
 
 Every step is one call of the library (``combine_route_scan_gb300.moe``); the
 rows stay in 4 bits from the dispatch to the down projection. The weights are
-quantised once, when the layer is made.
+quantised once, when the layer is made. Every token is active and every expert one
+of the E: the dispatch's token masks and its zero and copy experts are not passed on.
 
 ``python -m combine_route_scan_gb300.mxfp4_layer`` builds one on random weights
 (8 ranks x 64 tokens, hidden 2048, 128 experts, top-8, intermediate 512), runs
@@ -67,7 +68,8 @@ class Mxfp4Layer:
         return out
 
     def logits_gradient(self, logits, grad_weights, out=None):
-        """The gradient of the last step's routing weights with respect to its logits."""
+        """The gradient of the last step's routing weights with respect to its logits. grad_weights, the
+        loss's gradient by those weights, is the caller's: the library has no backward of the combine."""
         out = torch.empty_like(logits) if out is None else out
         M.route_backward(self.router, logits, self.ids, grad_weights, out)
         return out
