@@ -40,6 +40,8 @@ __global__ void __launch_bounds__(kInvThreads) combine_inverse_kernel(CombinePar
   if (h && h->inv_valid && h->inv_assist == (unsigned long long)(uintptr_t)p.assist &&
       h->inv_ep == (unsigned long long)(uintptr_t)p.ep_recv_count)
     return;
+  // from here on the map is this call's, whose buffers may change before the next one
+  if (h && threadIdx.x == 0 && blockIdx.x == 0 && d == 0) p.hdr->inv_valid = 0;
   long long count = p.ep_recv_count[(size_t)d * LW + LW - 1];
   if (count < 0 || count > sh.A) {
     if (threadIdx.x == 0 && blockIdx.x == 0) set_error(p.status, MOE_ERR_BAD_ASSIST);

@@ -279,6 +279,17 @@ void set_map_owner(const void* ws, const void* assist, const void* ep, cudaStrea
   if (cap != 0) o->graphed = true;
 }
 
+// A call on `s` enqueues the inverse-map pass: the workspace's map is no dispatch's any more, and where
+// the pass is captured, a replay may replace the map of a later dispatch unseen.
+void drop_map_owner(const void* ws, cudaStream_t s) {
+  const unsigned long long cap = capture_id(s);
+  std::lock_guard<std::mutex> lock(g_owner_mu);
+  MapOwner* o = owner_slot(ws);
+  o->assist = o->ep = nullptr;
+  o->capture = 0ull;
+  if (cap != 0) o->graphed = true;
+}
+
 void reset_map_owner(const void* ws) {
   std::lock_guard<std::mutex> lock(g_owner_mu);
   *owner_slot(ws) = MapOwner{ws, nullptr, nullptr, 0ull, false};
@@ -517,6 +528,7 @@ moe_status_t moe_combine(const moe_config_t* cfg, const void* expert_out, const 
     // the map of the dispatch that wrote these buffers on this workspace is
     // used as it is; otherwise it is rebuilt from assist_info first
     if (!map_owned_by(ws, assist_info, ep_recv_count, s)) {
+      drop_map_owner(ws, s);
       if (launch_combine_inverse(cp, s) != cudaSuccess) return MOE_ERR_CUDA;
       note_launches(1);
     }
