@@ -13,10 +13,13 @@
 // ascending, one fused multiply-add per pick, and rounds once to the output
 // type. The reduce checks every pick it reads against assist_info, so a row
 // map that does not match the routing is reported, not silently used.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+//
+// The same reduce is dispatch's gradient (moe_dispatch_backward): with every
+// weight 1, the routed picks alone and a residual to start from, grad_x[token] =
+// residual[token] + sum_k grad_expand_x[row of (token, k)].
+#include <type_traits>
 
-#include "common.cuh"
+#include "rows.cuh"
 
 namespace crs {
 
@@ -62,50 +65,6 @@ __global__ void __launch_bounds__(kInvThreads) combine_inverse_kernel(CombinePar
   }
 }
 
-// Element traits: 16-byte vectors of T, fp32 (or wrapping int32) accumulators.
-template <int DT>
-struct Vec;
-template <>
-struct Vec<MOE_F16> {
-  static constexpr int N = 8;
-  __device__ static void fma(float* acc, float w, int4 v) {
-    const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(h[i]);
-      acc[2 * i] = __fmaf_rn(w, f.x, acc[2 * i]);
-      acc[2 * i + 1] = __fmaf_rn(w, f.y, acc[2 * i + 1]);
-    }
-  }
-  __device__ static int4 pack(const float* acc) {
-    int4 o;
-    __half2* h = reinterpret_cast<__half2*>(&o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(acc[2 * i], acc[2 * i + 1]);
-    return o;
-  }
-};
-template <>
-struct Vec<MOE_BF16> {
-  static constexpr int N = 8;
-  __device__ static void fma(float* acc, float w, int4 v) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(h[i]);
-      acc[2 * i] = __fmaf_rn(w, f.x, acc[2 * i]);
-      acc[2 * i + 1] = __fmaf_rn(w, f.y, acc[2 * i + 1]);
-    }
-  }
-  __device__ static int4 pack(const float* acc) {
-    int4 o;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
-    return o;
-  }
-};
-
 // Builds the contributing-pick list of token `tau` (warp 0): source row
 // pointers and weights in ascending k. Records errors for ids out of range and
 // for a row map that does not name this pick.
@@ -115,7 +74,9 @@ struct ReduceTable {
   int n;
 };
 
-__device__ __forceinline__ void build_reduce_table(const CombineParams& p, size_t tau, ReduceTable& tab) {
+template <class P>
+__device__ __forceinline__ void build_reduce_table(const P& p, size_t tau, ReduceTable& tab) {
+  constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
   const Shape& sh = p.sh;
   const int lane = threadIdx.x & 31;
   const uint8_t* src = nullptr;
@@ -140,10 +101,17 @@ __device__ __forceinline__ void build_reduce_table(const CombineParams& p, size_
       } else {
         set_error(p.status, MOE_ERR_BAD_ASSIST);
       }
-    } else if (c == kPickCopy) {
+    } else if (!kGrad && c == kPickCopy) {
       src = static_cast<const uint8_t*>(p.x) + tau * (size_t)sh.row_in;
     }
-    if (src) w = reinterpret_cast<const uint32_t*>(p.scales)[tau * sh.K + lane];
+    if constexpr (kGrad) {
+      w = __float_as_uint(1.f);
+      if (p.pick_weights)
+        p.pick_weights[tau * sh.K + lane] =
+            src ? p.row_weights[(src - static_cast<const uint8_t*>(p.expert_out)) / sh.row_in] : 0.f;
+    } else {
+      if (src) w = reinterpret_cast<const uint32_t*>(p.scales)[tau * sh.K + lane];
+    }
   }
   const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
   if (src) {
@@ -163,7 +131,7 @@ __device__ __forceinline__ void build_reduce_table(const CombineParams& p, size_
 // read), so the check costs no round trip on the critical path.
 template <int DT>
 __device__ __forceinline__ void reduce_vector(const uint8_t* const* src, const uint32_t* w, int n, size_t off,
-                                              uint8_t* out) {
+                                              uint8_t* out, const uint8_t* residual = nullptr) {
   if constexpr (DT == MOE_I32) {
     uint32_t acc[4] = {0u, 0u, 0u, 0u};
     for (int j = 0; j < n; j += kReduceBatch) {
@@ -187,6 +155,8 @@ __device__ __forceinline__ void reduce_vector(const uint8_t* const* src, const u
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    // an ordinary load: the residual may be what this thread then writes
+    if (residual) Vec<DT>::fma(acc, 1.f, ld_v4(residual + off));
     for (int j = 0; j < n; j += kReduceBatch) {
       int4 y[kReduceBatch];
 #pragma unroll
@@ -202,8 +172,9 @@ __device__ __forceinline__ void reduce_vector(const uint8_t* const* src, const u
 
 // At most 64 registers a thread: four CTAs (32 warps) per SM keep enough
 // loads in flight to cover HBM latency.
-template <int DT>
-__global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(CombineParams p, int chunks, int vpl) {
+template <int DT, class P>
+__global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(P p, int chunks, int vpl) {
+  constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
   MOE_PHASE_BEGIN(p, kPhaseReduce);
   __shared__ const uint8_t* s_src[kReduceThreads / 32][32];
   __shared__ uint32_t s_w[kReduceThreads / 32][32];
@@ -230,7 +201,7 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(Combi
   if (lane < sh.K) {
     const size_t pk = tau * sh.K + lane;
     r = p.inv[pk];
-    w = reinterpret_cast<const uint32_t*>(p.scales)[pk];
+    w = kGrad ? __float_as_uint(1.f) : reinterpret_cast<const uint32_t*>(p.scales)[pk];
     const int cls = classify_pick(p.ids, p.mask, sh, tau, lane);
     if (cls >= 0) {
       d = cls / sh.L;
@@ -240,10 +211,13 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(Combi
       } else {
         set_error(p.status, MOE_ERR_BAD_ASSIST);
       }
-    } else if (cls == kPickCopy) {
+    } else if (!kGrad && cls == kPickCopy) {
       src = static_cast<const uint8_t*>(p.x) + tau * (size_t)sh.row_in;
     } else if (cls == kPickBad) {
       set_error(p.status, MOE_ERR_BAD_EXPERT_ID);
+    }
+    if constexpr (kGrad) {
+      if (p.pick_weights && c == 0) p.pick_weights[pk] = src ? p.row_weights[r] : 0.f;
     }
   }
   const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
@@ -269,11 +243,15 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(Combi
 
   const int nvec = sh.row_in / 16;
   uint8_t* out = static_cast<uint8_t*>(p.x_out) + tau * (size_t)sh.row_in;
+  const uint8_t* residual = nullptr;
+  if constexpr (kGrad) {
+    if (p.residual) residual = static_cast<const uint8_t*>(p.residual) + tau * (size_t)sh.row_in;
+  }
   const int v0 = c * 32 * vpl;
   for (int i = 0; i < vpl; ++i) {
     const int v = v0 + i * 32 + lane;
     if (v >= nvec) break;
-    reduce_vector<DT>(s_src[warp], s_w[warp], n, (size_t)v * 16, out);
+    reduce_vector<DT>(s_src[warp], s_w[warp], n, (size_t)v * 16, out, residual);
   }
 
   if (check) {
@@ -284,8 +262,8 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(Combi
 }
 
 // Element-wise fallback for rows that are not 16-byte multiples.
-template <int DT>
-__global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(CombineParams p) {
+template <int DT, class P>
+__global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(P p) {
   __shared__ ReduceTable tab;
   const Shape sh = p.sh;
   pdl_wait();
@@ -301,15 +279,12 @@ __global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(Co
         reinterpret_cast<uint32_t*>(p.x_out)[tau * sh.h + j] = acc;
       } else {
         float acc = 0.f;
-        for (int q = 0; q < n; ++q) {
-          const uint16_t b = reinterpret_cast<const uint16_t*>(tab.src[q])[j];
-          const float y = DT == MOE_F16 ? __half2float(__ushort_as_half(b))
-                                        : __bfloat162float(__ushort_as_bfloat16(b));
-          acc = __fmaf_rn(__uint_as_float(tab.w[q]), y, acc);
+        if constexpr (std::is_same<P, DispatchGradParams>::value) {
+          if (p.residual) acc = elem_to_float<DT>(static_cast<const uint16_t*>(p.residual)[tau * sh.h + j]);
         }
-        uint16_t o = DT == MOE_F16 ? __half_as_ushort(__float2half_rn(acc))
-                                   : __bfloat16_as_ushort(__float2bfloat16_rn(acc));
-        reinterpret_cast<uint16_t*>(p.x_out)[tau * sh.h + j] = o;
+        for (int q = 0; q < n; ++q)
+          acc = __fmaf_rn(__uint_as_float(tab.w[q]), elem_to_float<DT>(reinterpret_cast<const uint16_t*>(tab.src[q])[j]), acc);
+        reinterpret_cast<uint16_t*>(p.x_out)[tau * sh.h + j] = float_to_elem<DT>(acc);
       }
     }
     __syncthreads();
@@ -324,16 +299,20 @@ cudaError_t launch_combine_inverse(const CombineParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&L.cfg, combine_inverse_kernel, p);
 }
 
-cudaError_t launch_combine_reduce(const CombineParams& p, cudaStream_t st, int num_sms) {
+template <class P>
+static cudaError_t launch_reduce(const P& p, cudaStream_t st, int num_sms) {
+  constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
   const Shape& sh = p.sh;
   const long long n_tok = (long long)sh.W * sh.bs;
   if (n_tok == 0) return cudaSuccess;
   if (sh.row_in % 16 != 0) {
     const int grid = (int)(n_tok < num_sms * 8LL ? n_tok : num_sms * 8LL);
     PdlLaunch L(dim3(grid), dim3(kReduceThreads), 0, st);
-    if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_I32>, p);
-    if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_F16>, p);
-    return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_BF16>, p);
+    if constexpr (!kGrad) {
+      if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_I32, P>, p);
+    }
+    if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_F16, P>, p);
+    return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_BF16, P>, p);
   }
   const int nvec = sh.row_in / 16;
   // smaller work items when the batch is too small to give every SM ~16 warps
@@ -344,9 +323,18 @@ cudaError_t launch_combine_reduce(const CombineParams& p, cudaStream_t st, int n
   const long long grid = (items + kReduceThreads / 32 - 1) / (kReduceThreads / 32);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   PdlLaunch L(dim3((unsigned)grid), dim3(kReduceThreads), 0, st);
-  if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_I32>, p, chunks, vpl);
-  if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_F16>, p, chunks, vpl);
-  return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_BF16>, p, chunks, vpl);
+  if constexpr (!kGrad) {
+    if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_I32, P>, p, chunks, vpl);
+  }
+  if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_F16, P>, p, chunks, vpl);
+  return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_BF16, P>, p, chunks, vpl);
+}
+
+cudaError_t launch_combine_reduce(const CombineParams& p, cudaStream_t st, int num_sms) {
+  return launch_reduce(p, st, num_sms);
+}
+cudaError_t launch_dispatch_grad(const DispatchGradParams& p, cudaStream_t st, int num_sms) {
+  return launch_reduce(p, st, num_sms);
 }
 
 }  // namespace crs

@@ -1,0 +1,251 @@
+// Rows quantised to 8-bit integers with a scale each (moe_int8_quantize;
+// include/moe_experts.h), with the arithmetic of dispatch's quant_mode 2
+// (quant_common.cuh): scale = amax / 127, code = round(x / scale).
+//
+// One pass over the data, bound by HBM: a row stays in registers between its maximum
+// and its codes, in a warp's where it has up to 2048 elements, in a block's up to
+// 16384. Rows that 16-byte loads do not fit, and longer ones, are read twice, an
+// element at a time, the second time from cache.
+#include "../../include/moe_experts.h"
+#include "experts_host.h"
+#include "quant_common.cuh"
+
+namespace crs {
+
+constexpr int kInt8Threads = 256;
+constexpr int kInt8CountedMats = 1024;  // matrices with row counts: one for each rank
+
+struct Int8QuantParams {
+  const void* x;
+  const int32_t* counts;  // [mats][counts_len], or null
+  int8_t* codes;
+  float* scales;
+  long long rows, row_stride, mat_stride;
+  int mats, cols, counts_len;
+};
+
+// The rows to work on, numbered through: matrix and row of number i, found in ascending order.
+struct Int8Rows {
+  const Int8QuantParams& p;
+  const int* pre;  // running row counts [mats + 1], with counts
+  long long total;
+  int m = 0;
+  __device__ Int8Rows(const Int8QuantParams& p_, int* s_pre) : p(p_), pre(s_pre) {
+    total = (long long)p.mats * p.rows;
+    if (!p.counts) return;
+    if (threadIdx.x < 32) {
+      int carry = 0;
+      for (int m0 = 0; m0 < p.mats; m0 += 32) {
+        const int mine = m0 + (int)threadIdx.x;
+        int n = mine < p.mats ? p.counts[(size_t)mine * p.counts_len + p.counts_len - 1] : 0;
+        n = n < 0 ? 0 : n > p.rows ? (int)p.rows : n;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int below = __shfl_up_sync(0xffffffffu, sum, o);
+          if ((int)threadIdx.x >= o) sum += below;
+        }
+        if (mine < p.mats) s_pre[mine] = carry + sum - n;
+        carry += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      if (threadIdx.x == 0) s_pre[p.mats] = carry;
+    }
+    __syncthreads();
+    total = s_pre[p.mats];
+  }
+  // where row i begins in x (elements) and its place among all rows of codes and scales
+  __device__ size_t find(long long i, size_t& place) {
+    long long r;
+    if (p.counts) {
+      while (i >= pre[m + 1]) ++m;
+      r = i - pre[m];
+    } else {
+      m = (int)(i / p.rows);
+      r = i - (long long)m * p.rows;
+    }
+    place = (size_t)m * p.rows + r;
+    return (size_t)(m * p.mat_stride + r * p.row_stride);
+  }
+};
+
+// 8 elements as loaded, and as fp32 pairs.
+template <int DT>
+struct Int8Unit {
+  static constexpr int kLoads = DT == MOE_F32 ? 2 : 1;
+  int4 v[kLoads];
+  __device__ void load(const void* x, size_t at) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      v[i] = ld_nc_v4(static_cast<const uint8_t*>(x) + at * (DT == MOE_F32 ? 4 : 2) + i * 16);
+  }
+  __device__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = make_int4(0, 0, 0, 0);
+  }
+  __device__ void pairs(f32x2 (&o)[4]) const {
+    if constexpr (DT == MOE_F32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o[2 * i] = f2_pack(__int_as_float(v[i].x), __int_as_float(v[i].y));
+        o[2 * i + 1] = f2_pack(__int_as_float(v[i].z), __int_as_float(v[i].w));
+      }
+    } else {
+      unpack8x2<DT>(v[0], o);
+    }
+  }
+};
+
+// The largest magnitude among the threads of a warp, or (BLOCK) of the block.
+template <bool BLOCK>
+__device__ __forceinline__ float int8_amax(float m, float (&s_max)[kInt8Threads / 32]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!BLOCK) return m;
+  __syncthreads();  // the row before is done with s_max
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = s_max[threadIdx.x & (kInt8Threads / 32 - 1)];
+#pragma unroll
+  for (int o = kInt8Threads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// cols a multiple of 8 that a warp's (BLOCK: the block's) threads hold as NV units each,
+// rows of x 16-byte aligned, codes 8-byte aligned.
+template <int DT, int NV, bool BLOCK>
+__global__ void __launch_bounds__(kInt8Threads) int8_quantize_vec_kernel(Int8QuantParams p) {
+  __shared__ int s_pre[kInt8CountedMats + 1];
+  __shared__ float s_max[kInt8Threads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kThreads = BLOCK ? kInt8Threads : 32;
+  const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  const int units = p.cols >> 3;
+  Int8Rows rows(p, s_pre);
+  const long long first = BLOCK ? blockIdx.x : blockIdx.x * (kInt8Threads / 32ll) + (threadIdx.x >> 5);
+  const long long step = BLOCK ? gridDim.x : gridDim.x * (kInt8Threads / 32ll);
+  for (long long i = first; i < rows.total; i += step) {
+    size_t place;
+    const size_t from = rows.find(i, place);
+    Int8Unit<DT> u[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (t + j * kThreads < units) u[j].load(p.x, from + (size_t)(t + j * kThreads) * 8);
+      else u[j].zero();
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      f32x2 v[4];
+      u[j].pairs(v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        f2_split(v[k], lo, hi);
+        m = fmax_abs3(m, lo, hi);
+      }
+    }
+    m = int8_amax<BLOCK>(m, s_max);
+    const float scale = __fdiv_rn(m, 127.0f);
+    const bool fast = token_rcp_ok(scale);
+    const float rcp = fast ? __frcp_rn(scale) : 0.f;
+    const f32x2 rcp2 = f2_pack(rcp, rcp);
+    int8_t* out = p.codes + place * p.cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (t + j * kThreads >= units) break;
+      f32x2 v[4];
+      u[j].pairs(v);
+      *reinterpret_cast<uint2*>(out + (size_t)(t + j * kThreads) * 8) = token_codes8(v, scale, m, fast, rcp2);
+    }
+    if (t == 0) p.scales[place] = scale;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ float int8_load(const void* x, size_t i) {
+  if constexpr (DT == MOE_F32) return static_cast<const float*>(x)[i];
+  else return load_elem(x, i, DT);
+}
+
+// Any columns and alignment: a warp or (BLOCK) a block a row, read twice.
+template <int DT, bool BLOCK>
+__global__ void __launch_bounds__(kInt8Threads) int8_quantize_plain_kernel(Int8QuantParams p) {
+  __shared__ int s_pre[kInt8CountedMats + 1];
+  __shared__ float s_max[kInt8Threads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kThreads = BLOCK ? kInt8Threads : 32;
+  const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  Int8Rows rows(p, s_pre);
+  const long long first = BLOCK ? blockIdx.x : blockIdx.x * (kInt8Threads / 32ll) + (threadIdx.x >> 5);
+  const long long step = BLOCK ? gridDim.x : gridDim.x * (kInt8Threads / 32ll);
+  for (long long i = first; i < rows.total; i += step) {
+    size_t place;
+    const size_t from = rows.find(i, place);
+    float m = 0.f;
+#pragma unroll 8
+    for (int c = t; c < p.cols; c += kThreads) m = fmaxf(m, fabsf(int8_load<DT>(p.x, from + c)));
+    m = int8_amax<BLOCK>(m, s_max);
+    const float scale = __fdiv_rn(m, 127.0f);
+    const bool fast = token_rcp_ok(scale);
+    const float rcp = fast ? __frcp_rn(scale) : 0.f;
+    int8_t* out = p.codes + place * p.cols;
+#pragma unroll 8
+    for (int c = t; c < p.cols; c += kThreads) {
+      const float v = int8_load<DT>(p.x, from + c);
+      out[c] = (int8_t)(fast ? token_code(v, scale, rcp) : m == 0.f ? 0u : (uint32_t)token_q(v, scale));
+    }
+    if (t == 0) p.scales[place] = scale;
+  }
+}
+
+struct Int8QuantKernel {
+  void (*kernel)(Int8QuantParams);
+  bool block;
+};
+
+// Where rows align for 16-byte loads, the narrowest group of threads that holds one.
+template <int DT>
+Int8QuantKernel int8_quant_kernel(int cols, bool vec) {
+  if (vec && cols <= 256) return {int8_quantize_vec_kernel<DT, 1, false>, false};
+  if (vec && cols <= 512) return {int8_quantize_vec_kernel<DT, 2, false>, false};
+  if (vec && cols <= 1024) return {int8_quantize_vec_kernel<DT, 4, false>, false};
+  if (vec && cols <= 2048) return {int8_quantize_vec_kernel<DT, 8, false>, false};
+  if (vec && cols <= 8192) return {int8_quantize_vec_kernel<DT, 4, true>, true};
+  if (vec && cols <= 16384) return {int8_quantize_vec_kernel<DT, 8, true>, true};
+  if (cols <= 1024) return {int8_quantize_plain_kernel<DT, false>, false};
+  return {int8_quantize_plain_kernel<DT, true>, true};
+}
+
+}  // namespace crs
+
+extern "C" moe_status_t moe_int8_quantize(const void* x, int32_t x_dtype, int32_t mats, int64_t rows, int32_t cols,
+                                          int64_t row_stride, int64_t mat_stride, const int32_t* counts,
+                                          int32_t counts_len, int8_t* codes, float* scales, void* stream) {
+  using namespace crs;
+  if (x_dtype != MOE_F32 && x_dtype != MOE_F16 && x_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (mats < 0 || rows < 0 || cols < 1 || cols > (1 << 30)) return MOE_ERR_INVALID_ARG;
+  if (rows >= 2147483648LL || mats * rows >= 2147483648LL) return MOE_ERR_INVALID_ARG;
+  if (row_stride < cols || mat_stride < 0) return MOE_ERR_INVALID_ARG;
+  if (counts && (counts_len < 1 || mats > kInt8CountedMats || (uintptr_t)counts % 4)) return MOE_ERR_INVALID_ARG;
+  if (mats == 0 || rows == 0) return MOE_OK;
+  const int es = x_dtype == MOE_F32 ? 4 : 2;
+  if (!x || !codes || !scales || (uintptr_t)x % es || (uintptr_t)scales % 4) return MOE_ERR_INVALID_ARG;
+  const int nsm = num_sms_of_current_device();
+  if (nsm <= 0) return MOE_ERR_CUDA;
+  const Int8QuantParams p{x, counts, codes, scales, rows, row_stride, mat_stride, mats, cols, counts_len};
+  const bool vec = cols % 8 == 0 && (uintptr_t)x % 16 == 0 && (mats * rows == 1 || row_stride * es % 16 == 0) &&
+                   (mats == 1 || mat_stride * es % 16 == 0) && (uintptr_t)codes % 8 == 0;
+  const Int8QuantKernel k = x_dtype == MOE_F32   ? int8_quant_kernel<MOE_F32>(cols, vec)
+                            : x_dtype == MOE_F16 ? int8_quant_kernel<MOE_F16>(cols, vec)
+                                                 : int8_quant_kernel<MOE_BF16>(cols, vec);
+  int per_sm = 0;
+  if (resident_blocks((const void*)k.kernel, kInt8Threads, 0, &per_sm) != cudaSuccess || per_sm < 1) return MOE_ERR_CUDA;
+  const long long need = k.block ? mats * rows : (mats * rows + kInt8Threads / 32 - 1) / (kInt8Threads / 32);
+  const long long most = (long long)nsm * per_sm;
+  PdlLaunch L(dim3((unsigned)(need < most ? need : most)), dim3(kInt8Threads), 0, static_cast<cudaStream_t>(stream));
+  if (cudaLaunchKernelEx(&L.cfg, k.kernel, p) != cudaSuccess) return MOE_ERR_CUDA;
+  note_launches(1);
+  return MOE_OK;
+}

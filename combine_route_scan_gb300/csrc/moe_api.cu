@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "internal.h"
 
@@ -665,6 +666,104 @@ moe_status_t moe_dispatch_ffn_combine(const moe_config_t* cfg, const void* x, co
   if (launch_combine_reduce(cp, s, nsm) != cudaSuccess) return MOE_ERR_CUDA;
   note_launches(1);
   return MOE_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What both gradients check and fill in of a call; *empty: nothing to launch.
+moe_status_t grad_params(const moe_config_t* cfg, const int32_t* assist_info, const int32_t* ep_recv_count,
+                         const int32_t* expert_ids, const uint8_t* active_mask, void* ws, size_t ws_bytes,
+                         CombineParams* p, bool* empty) {
+  Shape sh;
+  moe_status_t st = make_shape(cfg, &sh);
+  if (st != MOE_OK) return st;
+  if (cfg->quant_mode != 0 || cfg->x_dtype == MOE_I32) return MOE_ERR_UNSUPPORTED;
+  *empty = sh.W * (long long)sh.bs == 0;
+  if (!ep_recv_count) return MOE_ERR_INVALID_ARG;
+  if (!*empty && (!assist_info || !expert_ids || (sh.mask_kind != 0 && !active_mask))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(assist_info, 4) || !aligned(ep_recv_count, 4) || !aligned(expert_ids, 4)) return MOE_ERR_INVALID_ARG;
+  WsLayout L;
+  st = check_ws(cfg, sh, ws, ws_bytes, &L);
+  if (st != MOE_OK) return st;
+  p->assist = assist_info;
+  p->ep_recv_count = ep_recv_count;
+  p->ids = expert_ids;
+  p->mask = sh.mask_kind ? active_mask : nullptr;
+  p->inv = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + L.inv);
+  p->sh = sh;
+  p->hdr = static_cast<WsHeader*>(ws);
+  p->status = &p->hdr->status;
+  return MOE_OK;
+}
+
+// The pick -> row map, as moe_combine takes it, then `launch`.
+template <class P, class F>
+moe_status_t run_grad(const moe_config_t* cfg, const P& p, void* ws, cudaStream_t s, F launch) {
+  const int nsm = num_sms_of_current_device();
+  if (nsm <= 0) return MOE_ERR_CUDA;
+  if (!map_owned_by(ws, p.assist, p.ep_recv_count, s)) {
+    drop_map_owner(ws, s);
+    if (launch_combine_inverse(p, s) != cudaSuccess) return MOE_ERR_CUDA;
+    note_launches(1);
+  }
+  if (record(cfg->prof_events, 0, s) != MOE_OK) return MOE_ERR_CUDA;
+  if (launch(p, s, nsm) != cudaSuccess) return MOE_ERR_CUDA;
+  note_launches(1);
+  return record(cfg->prof_events, 1, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out, const void* expert_out,
+                                  const int32_t* assist_info, const int32_t* ep_recv_count, const int32_t* expert_ids,
+                                  const float* expert_scales, const uint8_t* active_mask, const void* x,
+                                  void* grad_expert_out, float* grad_scales, void* grad_x, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  CombineGradParams p{};
+  bool empty;
+  const moe_status_t st = grad_params(cfg, assist_info, ep_recv_count, expert_ids, active_mask, ws, ws_bytes, &p, &empty);
+  if (st != MOE_OK) return st;
+  if (!grad_expert_out && !grad_scales && !grad_x) return MOE_ERR_INVALID_ARG;
+  if (!empty && (!grad_out || !expert_scales || (grad_scales && !expert_out) || (grad_scales && p.sh.C > 0 && !x)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(grad_out, 16) || !aligned(expert_out, 16) || !aligned(expert_scales, 4) || !aligned(x, 16) ||
+      !aligned(grad_expert_out, 16) || !aligned(grad_scales, 4) || !aligned(grad_x, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (empty) return MOE_OK;
+  p.expert_out = expert_out;
+  p.scales = expert_scales;
+  p.x = x;
+  p.grad_out = grad_out;
+  p.grad_rows = grad_expert_out;
+  p.grad_scales = grad_scales;
+  p.grad_x = grad_x;
+  return run_grad(cfg, p, ws, static_cast<cudaStream_t>(stream), launch_combine_grad);
+}
+
+moe_status_t moe_dispatch_backward(const moe_config_t* cfg, const void* grad_expand_x, const int32_t* assist_info,
+                                   const int32_t* ep_recv_count, const int32_t* expert_ids, const uint8_t* active_mask,
+                                   const void* residual, const float* grad_expand_scales, void* grad_x,
+                                   float* grad_scales, void* ws, size_t ws_bytes, void* stream) {
+  DispatchGradParams p{};
+  bool empty;
+  const moe_status_t st = grad_params(cfg, assist_info, ep_recv_count, expert_ids, active_mask, ws, ws_bytes, &p, &empty);
+  if (st != MOE_OK) return st;
+  if ((grad_expand_scales != nullptr) != (grad_scales != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!empty && (!grad_expand_x || !grad_x)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(grad_expand_x, 16) || !aligned(residual, 16) || !aligned(grad_expand_scales, 4) || !aligned(grad_x, 16) ||
+      !aligned(grad_scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (empty) return MOE_OK;
+  p.expert_out = grad_expand_x;
+  p.x_out = grad_x;
+  p.residual = residual;
+  p.row_weights = grad_expand_scales;
+  p.pick_weights = grad_scales;
+  return run_grad(cfg, p, ws, static_cast<cudaStream_t>(stream), launch_dispatch_grad);
 }
 
 moe_status_t moe_get_device_status(void* ws, void* stream, int32_t* status) {

@@ -1,0 +1,88 @@
+// Rows of fp16 / bf16 as fp32 numbers and back, for combine and the gradients of
+// combine and dispatch.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace crs {
+
+// Element traits: 16-byte vectors of T, fp32 accumulators.
+template <int DT>
+struct Vec;
+template <>
+struct Vec<MOE_F16> {
+  __device__ static void unpack(float (&f)[8], int4 v) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = __half22float2(h[i]);
+      f[2 * i] = a.x;
+      f[2 * i + 1] = a.y;
+    }
+  }
+  __device__ static void fma(float* acc, float w, int4 v) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      acc[2 * i] = __fmaf_rn(w, f.x, acc[2 * i]);
+      acc[2 * i + 1] = __fmaf_rn(w, f.y, acc[2 * i + 1]);
+    }
+  }
+  __device__ static int4 pack(const float* acc) {
+    int4 o;
+    __half2* h = reinterpret_cast<__half2*>(&o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(acc[2 * i], acc[2 * i + 1]);
+    return o;
+  }
+};
+template <>
+struct Vec<MOE_BF16> {
+  __device__ static void unpack(float (&f)[8], int4 v) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = __bfloat1622float2(h[i]);
+      f[2 * i] = a.x;
+      f[2 * i + 1] = a.y;
+    }
+  }
+  __device__ static void fma(float* acc, float w, int4 v) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(h[i]);
+      acc[2 * i] = __fmaf_rn(w, f.x, acc[2 * i]);
+      acc[2 * i + 1] = __fmaf_rn(w, f.y, acc[2 * i + 1]);
+    }
+  }
+  __device__ static int4 pack(const float* acc) {
+    int4 o;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+    return o;
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ float elem_to_float(uint16_t b) {
+  return DT == MOE_F16 ? __half2float(__ushort_as_half(b)) : __bfloat162float(__ushort_as_bfloat16(b));
+}
+template <int DT>
+__device__ __forceinline__ uint16_t float_to_elem(float f) {
+  return DT == MOE_F16 ? __half_as_ushort(__float2half_rn(f)) : __bfloat16_as_ushort(__float2bfloat16_rn(f));
+}
+
+// 16 bytes that the kernel may write to as well.
+__device__ __forceinline__ int4 ld_v4(const void* p) {
+  int4 v;
+  asm volatile("ld.global.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+}  // namespace crs

@@ -47,7 +47,8 @@ BULK_MIN_BYTES = 2 * 1024 * 1024
 EXPORTS = ("moe_get_workspace_size", "moe_workspace_init", "moe_dispatch", "moe_combine",
            "moe_dispatch_ffn_combine", "moe_combine_noalloc", "moe_get_device_status", "moe_status_string")
 # ... and include/moe_experts.h.
-EXPERTS_EXPORTS = ("moe_route", "moe_route_backward", "moe_mx_scale_bytes", "moe_mx_quantize", "moe_expert_product")
+EXPERTS_EXPORTS = ("moe_route", "moe_route_backward", "moe_mx_scale_bytes", "moe_mx_quantize", "moe_expert_product",
+                   "moe_int8_quantize", "moe_expert_product_int8", "moe_combine_backward", "moe_dispatch_backward")
 NOALLOC_MAX_PICKS = 262144
 
 MOE_F32, MOE_MXFP4 = 3, 4
@@ -129,7 +130,8 @@ def _calls():
     spec = importlib.util.spec_from_file_location("_bind", path)
     module = importlib.util.module_from_spec(spec)
     module.entries(*(ctypes.cast(f, ctypes.c_void_p).value
-                     for f in (L.moe_route, L.moe_route_backward, L.moe_mx_quantize, L.moe_expert_product)))
+                     for f in (L.moe_route, L.moe_route_backward, L.moe_mx_quantize, L.moe_expert_product, L.moe_int8_quantize,
+                               L.moe_expert_product_int8, L.moe_combine_backward, L.moe_dispatch_backward)))
     _bind = module
     return module
 
@@ -160,9 +162,14 @@ def lib() -> ctypes.CDLL:
         L.moe_mx_scale_bytes.restype = ctypes.c_uint64
         L.moe_mx_quantize.argtypes = [P, I32, I32, I64, I32, I64, I64, I32, P, P, P]
         L.moe_expert_product.argtypes = [C, P, P, P, P, P, I32, I32, I32, I32, P, P, P, ctypes.c_size_t, P]
+        L.moe_int8_quantize.argtypes = [P, I32, I32, I64, I32, I64, I64, P, I32, P, P, P]
+        L.moe_expert_product_int8.argtypes = [C, P, P, P, P, P, I32, I32, I32, I32, P, P, ctypes.c_size_t, P]
+        L.moe_combine_backward.argtypes = [C, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_dispatch_backward.argtypes = [C, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         for f in ("moe_get_workspace_size", "moe_workspace_init", "moe_dispatch", "moe_combine",
                   "moe_dispatch_ffn_combine", "moe_combine_noalloc", "moe_get_device_status", "moe_route",
-                  "moe_route_backward", "moe_mx_quantize", "moe_expert_product"):
+                  "moe_route_backward", "moe_mx_quantize", "moe_expert_product", "moe_int8_quantize",
+                  "moe_expert_product_int8", "moe_combine_backward", "moe_dispatch_backward"):
             getattr(L, f).restype = ctypes.c_int32
         _lib = L
     return _lib
@@ -323,6 +330,41 @@ def expert_product(cfg: MoeConfig, x, x_scales, ep_recv_count, w, w_scales, y, y
                                               stream), "moe_expert_product")
 
 
+def int8_quantize(x, codes, scales, ep_recv_count=None, stream=None):
+    """moe_int8_quantize: x [rows, cols] or [matrices, rows, cols] (contiguous rows, any
+    strides between them) -> codes int8 of x's shape and scales fp32 [..., rows]
+    (alloc_int8 makes both). With dispatch's ep_recv_count, x is [W, A, cols] and only
+    the received rows are read and written."""
+    _check((_bind or _calls()).int8_quantize(x, codes, scales, ep_recv_count, stream), "moe_int8_quantize")
+
+
+def expert_product_int8(cfg: MoeConfig, x, x_scales, ep_recv_count, w, w_scales, y, epilogue: int = EPI_NONE, ws=None,
+                        stream=None):
+    """moe_expert_product_int8: dispatched int8 rows x [W, A, k] with x_scales [W, A] (or None)
+    times w int8 [E, n, k] with w_scales [E, n] -> y [W, A, c] float16 / bfloat16; c = n, or
+    n/2 with EPI_SWIGLU. ws is the dispatch's workspace."""
+    _check((_bind or _calls()).expert_product_int8(cfg, x, x_scales, ep_recv_count, w, w_scales, y, epilogue, ws, stream),
+           "moe_expert_product_int8")
+
+
+def combine_backward(cfg: MoeConfig, grad_out, expert_out, assist_info, ep_recv_count, expert_ids, expert_scales,
+                     active_mask, x, grad_expert_out, grad_scales=None, grad_x=None, ws=None, stream=None):
+    """moe_combine_backward: from grad_out [W, bs, h] the gradients of combine's expert_out, expert_scales and x, written
+    to those of grad_expert_out [W, A, h], grad_scales fp32 [W, bs, K] and grad_x [W, bs, h] that are not None."""
+    _check((_bind or _calls()).combine_backward(cfg, grad_out, expert_out, assist_info, ep_recv_count, expert_ids,
+                                                expert_scales, active_mask, x, grad_expert_out, grad_scales, grad_x, ws,
+                                                stream), "moe_combine_backward")
+
+
+def dispatch_backward(cfg: MoeConfig, grad_expand_x, assist_info, ep_recv_count, expert_ids, active_mask, grad_x,
+                      residual=None, grad_expand_scales=None, grad_scales=None, ws=None, stream=None):
+    """moe_dispatch_backward: each token's rows of grad_expand_x [W, A, h] summed onto residual (which may be grad_x)
+    into grad_x [W, bs, h], and grad_expand_scales fp32 [W, A] taken back to grad_scales [W, bs, K]."""
+    _check((_bind or _calls()).dispatch_backward(cfg, grad_expand_x, assist_info, ep_recv_count, expert_ids, active_mask,
+                                                 grad_x, residual, grad_expand_scales, grad_scales, ws, stream),
+           "moe_dispatch_backward")
+
+
 def get_device_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream; returns and clears the first device-side error."""
     v = ctypes.c_int32(0)
@@ -391,3 +433,9 @@ def alloc_mx(x: torch.Tensor, layout: int = SF_ROWS) -> tuple:
     codes = torch.empty((*x.shape[:-1], cols // 2), dtype=torch.uint8, device=x.device)
     shape = (*lead, rows, blocks) if layout == SF_ROWS else (*(lead or [1]), -(-rows // 128), -(-blocks // 4), 512)
     return codes, torch.empty(shape, dtype=torch.uint8, device=x.device)
+
+
+def alloc_int8(x: torch.Tensor) -> tuple:
+    """(codes, scales) that int8_quantize fills for x."""
+    return (torch.empty(x.shape, dtype=torch.int8, device=x.device),
+            torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device))

@@ -1,11 +1,14 @@
 /*
  * moe_experts.h - C ABI of the operators around the experts (libcrs_moe.so):
- * routing scores to expert ids and weights, with its gradient, and the experts'
- * product on microscaled 4-bit (MX FP4) operands, with the quantiser that makes
- * them. They join onto include/moe.h: moe_route writes the expert_ids and
- * expert_scales that moe_dispatch and moe_combine take, and moe_expert_product
- * reads the rows, scales and counts that moe_dispatch leaves in quant_mode 4
- * with MOE_Y_FP4_E2M1.
+ * routing scores to expert ids and weights, with its gradient; the experts'
+ * product on microscaled 4-bit (MX FP4) and on 8-bit integer operands, with the
+ * quantisers that make them; and the gradients of combine and dispatch. They join
+ * onto include/moe.h: moe_route writes the expert_ids and expert_scales that
+ * moe_dispatch and moe_combine take, moe_expert_product reads the rows, scales and
+ * counts that moe_dispatch leaves in quant_mode 4 with MOE_Y_FP4_E2M1,
+ * moe_expert_product_int8 those of quant_mode 2, and a training step goes
+ * moe_combine_backward, the experts' own gradient, moe_dispatch_backward and
+ * moe_route_backward.
  *
  * The conventions of include/moe.h hold: array pointers are device pointers of
  * the caller, nothing is allocated or kept, `stream` is a cudaStream_t, calls
@@ -166,6 +169,103 @@ moe_status_t moe_expert_product(const moe_config_t* cfg, const void* x, const ui
                                 const int32_t* ep_recv_count, const void* w, const uint8_t* w_scales, int32_t n,
                                 int32_t k, int32_t epilogue, int32_t y_dtype, void* y, uint8_t* y_scales, void* ws,
                                 size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------- int8 quantisation and product */
+
+/* Quantises rows to 8-bit integers with a scale each, with moe_dispatch's
+ * quant_mode 2 arithmetic: scale = amax|x| / 127 and code = clamp(rne(x / scale),
+ * -127, 127), both IEEE divisions in fp32; a row of zeros gets scale 0 and zero
+ * codes. An infinity gives its row an infinite scale and zero codes; a NaN is passed
+ * over in amax and its code is unspecified (the format has no NaN).
+ * For weights [E][n][k] that is a scale for each output channel, as
+ * moe_expert_product_int8 takes them; with `counts`, the rows that the ranks
+ * received, such as the SwiGLU output of one product on its way to the next.
+ *
+ *   x       x_dtype MOE_F32, MOE_F16 or MOE_BF16, aligned to the element; row r of
+ *           matrix m begins at m * mat_stride + r * row_stride elements (row_stride >=
+ *           cols, mat_stride >= 0)
+ *   cols    [1, 2^30]; mats >= 0, rows >= 0, mats * rows < 2^31
+ *   counts  NULL, or [mats][counts_len] int32 with mats <= 1024: of matrix m only the
+ *           rows below counts[m][counts_len - 1] (taken into [0, rows]) are read and
+ *           written: moe_dispatch's ep_recv_count with mats = W and counts_len = L*W
+ *   codes   [mats][rows][cols] int8
+ *   scales  [mats][rows] fp32 */
+moe_status_t moe_int8_quantize(const void* x, int32_t x_dtype, int32_t mats, int64_t rows, int32_t cols,
+                               int64_t row_stride, int64_t mat_stride, const int32_t* counts, int32_t counts_len,
+                               int8_t* codes, float* scales, void* stream);
+
+/* The experts' product on dispatched int8 rows, with a scale for each row and each
+ * output channel: for every row r of rank d that ep_recv_count gives to local
+ * expert le (expert e = d * L + le),
+ *   z[r][j] = x_scales[r] * w_scales[e][j] * (sum over i of x[r][i] * w[e][j][i])
+ * then the epilogue (MOE_EPI_*) in fp32, rounded once to y_dtype; silu as in
+ * moe_expert_product. The integers' sum is exact where no partial sum is beyond 2^24
+ * (any with k <= 1024); past that it is rounded as fp32 sums are.
+ *
+ *   cfg           the dispatch's configuration: W, bs, topk, E, wait_timeout_us and
+ *                 the workspace size are taken from it; h, types and modes are not
+ *   k             elements of a row, [1, 131071]
+ *   x             [W][A][k] int8 (A from moe_get_workspace_size), 16-byte aligned
+ *   x_scales      [W][A] fp32 as moe_dispatch (quant_mode 2) or moe_int8_quantize wrote
+ *                 them, or NULL for 1 everywhere (static scales, folded into w_scales)
+ *   ep_recv_count [W][L*W] as moe_dispatch wrote it; of an expert's W running counts only the last, at
+ *                 its rows' end, is read
+ *   w             [E][n][k] int8, 16-byte aligned; w_scales [E][n] fp32
+ *   y             [W][A][c], c = n, or n / 2 with MOE_EPI_SWIGLU: MOE_F16 or MOE_BF16
+ *                 elements, 16-byte aligned
+ *   ws            the workspace that the dispatch used (it holds the status word)
+ * Rows at or beyond ep_recv_count[d][L*W-1] are left untouched; counts that dispatch
+ * cannot have written are treated as in moe_expert_product. */
+moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const int8_t* x, const float* x_scales,
+                                     const int32_t* ep_recv_count, const int8_t* w, const float* w_scales, int32_t n,
+                                     int32_t k, int32_t epilogue, int32_t y_dtype, void* y, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* ------------------------------------------------- gradients of combine and dispatch */
+
+/* The gradient of moe_combine, from grad_out, the gradient of x_out. With g =
+ * grad_out[s][t] and w_k = expert_scales[s][t][k]:
+ *   routed pick  grad_expert_out[its row] = w_k * g        grad_scales = <g, its row of expert_out>
+ *   copy expert  adds w_k to the factor of grad_x[s][t]    grad_scales = <g, x[s][t]>
+ *   zero expert or inactive pick                           grad_scales = 0
+ *   grad_x[s][t] = (sum of its copies' w_k, k ascending) * g, zeros without a copy
+ * in fp32, each rounded once to x_dtype (grad_scales stays fp32). Rows that belong
+ * to no pick are left untouched, what tensors hold at picks and tokens that have no
+ * part (infinities and NaN included) is not read, and the sums' order is fixed.
+ *
+ *   cfg         the combine's configuration: quant_mode 0, x_dtype MOE_F16 or MOE_BF16, else
+ *               MOE_ERR_UNSUPPORTED; combine_mode plays no part
+ *   grad_out    [W][bs][h]
+ *   expert_out, x (with copy experts): as given to moe_combine; needed iff grad_scales is wanted
+ *   assist_info, ep_recv_count, expert_ids, expert_scales, active_mask: as given to moe_combine
+ *   grad_expert_out [W][A][h], grad_scales [W][bs][K] fp32, grad_x [W][bs][h]: any of them, but not all,
+ *               may be NULL; none may overlap an input
+ *   ws          a workspace of cfg, best the dispatch's: the pick -> row map is taken
+ *               from it or rebuilt in it as moe_combine does, and checked as there
+ * Row arrays are 16-byte aligned. grad_scales is what moe_route_backward takes. */
+moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out, const void* expert_out,
+                                  const int32_t* assist_info, const int32_t* ep_recv_count, const int32_t* expert_ids,
+                                  const float* expert_scales, const uint8_t* active_mask, const void* x,
+                                  void* grad_expert_out, float* grad_scales, void* grad_x, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* The gradient of moe_dispatch without quantisation (with it: straight through, by a
+ * configuration of quant_mode 0), from grad_expand_x, the gradient of expand_x:
+ *   grad_x[s][t] = residual[s][t] + sum over its routed picks, k ascending, of the pick's row of grad_expand_x
+ * in fp32, rounded once to x_dtype; a token with no row keeps its residual, or gets
+ * zeros. And of expand_scales:
+ *   grad_scales[s][t][k] = grad_expand_scales[the pick's row], 0 for picks that have none.
+ *
+ *   cfg, ws, assist_info, ep_recv_count, expert_ids, active_mask: as in moe_combine_backward
+ *   grad_expand_x [W][A][h]
+ *   residual      NULL or [W][bs][h]: the gradient that x has from elsewhere (moe_combine_backward's
+ *                 grad_x, the way past the layer); it may be grad_x itself
+ *   grad_expand_scales NULL or [W][A] fp32; NULL iff grad_scales is
+ *   grad_x        [W][bs][h]; grad_scales [W][bs][K] fp32 */
+moe_status_t moe_dispatch_backward(const moe_config_t* cfg, const void* grad_expand_x, const int32_t* assist_info,
+                                   const int32_t* ep_recv_count, const int32_t* expert_ids, const uint8_t* active_mask,
+                                   const void* residual, const float* grad_expand_scales, void* grad_x,
+                                   float* grad_scales, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
