@@ -1,12 +1,32 @@
 // The experts' product on dispatched int8 rows (moe_expert_product_int8;
 // include/moe_experts.h): z[r][j] = xs[r] * ws[e(r)][j] * sum_i x[r][i] * w[e(r)][j][i] over
 // the rows that ep_recv_count gives to each expert, then the epilogue.
+//
+// sm_103a's integer tensor rate is a small part of its fp16 rate, and fp16 holds every
+// int8 exactly, products below 2^14 and sums to 2^24 in fp32 too: the codes are
+// widened to fp16 on the way from shared memory to the tensor cores.
+//   * a unit is 128 weight rows of an expert (the MMA's A operand) against up to 192 of
+//     its rows (B), K in stages of 128 elements. Weights are A because A may come from
+//     TMEM: a weight goes TMA -> shared memory -> registers -> TMEM, 2 bytes of shared-memory
+//     traffic for each; a row's element, written back as fp16 and read by the
+//     MMA, takes 6. Shared memory (128 bytes a clock) and not the MMA bounds a unit of many rows;
+//     with few rows the weights' stream from HBM does;
+//   * four bytes become two fp16 pairs by (w & 0x00ff00ff) ^ 0x64806480 = 1152 + value, less
+//     1152: bytes 0 and 2, and shifted by 8 bytes 1 and 3. The order of K that this gives is
+//     the same for both operands;
+//   * warps: 0 TMA, 1 MMA, 4..11 widen (each thread half a weight row a stage, each warp
+//     16 elements of all rows), 12..15 epilogue. Two accumulators, so that the
+//     next unit's MMAs run while this one is read.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <mutex>
+
 #include "../../include/moe_experts.h"
-#include "common.cuh"
 #include "experts_host.h"
+#include "tcgen05.cuh"
 
 namespace crs {
 
@@ -20,6 +40,7 @@ struct Int8ProductParams {
   int W, L, E, N, K, C;
   long long A;
   int* status;
+  uint64_t timeout_ns;
 };
 
 // SwiGLU of a gate and what it gates. exp and the reciprocal are the fast ones, within a
@@ -32,32 +53,36 @@ __device__ __forceinline__ float int8_swiglu(float gate, float up) {
   return (gate < 0.f ? gate * t : gate) * r * up;
 }
 
-// The experts' rows: running tiles of `tile` rows pre[E + 1], first flat row [E], row
-// count [E] behind one another; false (for every thread) where counts overlap to more tiles
-// than dispatch's can make. All threads of the block take part.
+// The experts' rows: first flat row [E] and row count [E] behind the tiles pre[E + 1]. The
+// calling thread's largest count is returned; no barrier.
 template <int THREADS>
-__device__ __forceinline__ bool int8_expert_rows(const Int8ProductParams& p, int tile, int* pre, long long* scratch) {
+__device__ __forceinline__ int int8_expert_rows(const Int8ProductParams& p, int* pre) {
   int* first = pre + p.E + 1;
   int* count = first + p.E;
+  int most = 0;
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    const int le = e % p.L;
+    const int32_t* ep = p.ep + (size_t)(e / p.L) * p.L * p.W;
+    const int hi = ep[le * p.W + p.W - 1], lo = le ? ep[le * p.W - 1] : 0;
+    const bool good = lo >= 0 && hi >= lo && hi <= p.A;
+    if (!good && blockIdx.x == 0) set_error(p.status, MOE_ERR_BAD_ASSIST);
+    first[e] = (int)(e / p.L * p.A) + (good ? lo : 0);  // flat rows fit 32 bits
+    count[e] = good ? hi - lo : 0;
+    most = max(most, count[e]);
+  }
+  return most;
+}
+
+// Running tiles of `tile` rows, pre[E + 1], of counts that the same threads have written; false
+// (for every thread) where counts overlap to more tiles than dispatch's can make. All
+// threads of the block take part.
+template <int THREADS>
+__device__ __forceinline__ bool int8_row_tiles(const Int8ProductParams& p, int tile, int* pre, long long* scratch) {
+  const int* count = pre + 2 * p.E + 1;
   long long carry = 0;
   for (int e0 = 0; e0 < p.E; e0 += THREADS) {
     const int e = e0 + (int)threadIdx.x;
-    int lo = 0, n = 0;
-    if (e < p.E) {
-      const int le = e % p.L;
-      const int32_t* ep = p.ep + (size_t)(e / p.L) * p.L * p.W;
-      const int hi = ep[le * p.W + p.W - 1];
-      lo = le ? ep[le * p.W - 1] : 0;
-      n = hi - lo;
-      if (lo < 0 || hi < lo || hi > p.A) {
-        if (blockIdx.x == 0) set_error(p.status, MOE_ERR_BAD_ASSIST);
-        n = 0;
-        lo = 0;
-      }
-      first[e] = (int)(e / p.L * p.A) + lo;  // flat rows fit 32 bits
-      count[e] = n;
-    }
-    const long long tiles = (n + tile - 1) / tile;
+    const long long tiles = e < p.E ? (count[e] + tile - 1) / tile : 0;
     const long long before = carry + block_exclusive_scan(tiles, scratch);
     if (e < p.E) {
       pre[e] = (int)min(before, 1ll << 30);
@@ -68,6 +93,438 @@ __device__ __forceinline__ bool int8_expert_rows(const Int8ProductParams& p, int
     carry = pre[last] + (count[last] + tile - 1) / tile;
   }
   return pre[p.E] <= (long long)p.W * p.A / tile + p.E;
+}
+
+// The expert whose tiles hold mt: the last one whose tiles begin at or before it.
+__device__ __forceinline__ int int8_expert_of(const int* pre, int E, int mt) {
+  int e = 0;
+  for (int half = 512; half; half >>= 1)
+    if (e + half < E && pre[e + half] <= mt) e += half;
+  return e;
+}
+
+template <int YT>
+__device__ __forceinline__ uint16_t int8_round(float v) {
+  return YT == MOE_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// ------------------------------------------------------------- the tensor cores
+
+// Boxes of 32 rows of x and of 64 rows of w, 128 elements of K.
+struct Int8Maps {
+  CUtensorMap x, w;
+};
+
+constexpr int kInt8ProductThreads = 512;
+constexpr int kWidenWarp = 4, kWidenWarps = 8, kInt8EpilogueWarp = 12;
+constexpr int kInt8Stage = 128;    // elements of K a stage
+constexpr int kInt8MostRows = 192; // MMA N
+constexpr int kInt8RawStages = 8;  // at most
+constexpr int kInt8WideStages = 4; // at most
+// An epilogue warp turns 32 rows x 32 results of 2 bytes around in shared memory, rows 80 bytes apart.
+constexpr uint32_t kInt8TurnRow = 80, kInt8TurnWarp = 32 * kInt8TurnRow;
+constexpr size_t kInt8ProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
+
+__host__ __device__ constexpr uint32_t int8_fixed_smem(int E) { return 4 * kInt8TurnWarp + ((3u * E + 1) * 4 + 127) / 128 * 128; }
+
+struct Int8Wait {
+  volatile int* flag;
+  int* status;
+  uint64_t limit;
+};
+
+// A wait of the pipeline, bounded by `limit` once it has lasted a while.
+__device__ __forceinline__ bool int8_wait(uint32_t bar, uint32_t parity, const Int8Wait& a) {
+#pragma unroll 1
+  for (int it = 0; it < 64; ++it)
+    if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*a.flag) return false;
+      if (globaltimer_ns() - t0 > a.limit) {
+        set_error(a.status, MOE_ERR_TIMEOUT);
+        *a.flag = 1;
+        return false;
+      }
+    }
+  }
+}
+// The same for a whole warp, one lane asking, with one answer for all.
+__device__ __forceinline__ bool int8_wait_warp(uint32_t bar, uint32_t parity, const Int8Wait& a) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = int8_wait(bar, parity, a);
+  return __all_sync(0xffffffffu, ok);
+}
+// The same, all lanes asking: nothing of it diverges when the phase is there at once.
+__device__ __forceinline__ bool int8_wait_all(uint32_t bar, uint32_t parity, const Int8Wait& a) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, int8_wait(bar, parity, a));
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ int4 lds_v4(uint32_t at) {
+  int4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
+// Four int8 as two fp16 pairs, elements (0, 2) and (1, 3), exactly.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const uint32_t bias = 0x64806480u;  // 1024 + (value + 128) in fp16
+  const uint32_t a = (w & 0x00ff00ffu) ^ bias, b = ((w >> 8) & 0x00ff00ffu) ^ bias;
+  const __half2 less = __half2half2(__ushort_as_half(0xe480));  // -1152
+  const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), less), y = __hadd2(*reinterpret_cast<const __half2*>(&b), less);
+  even = *reinterpret_cast<const uint32_t*>(&x);
+  odd = *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ void widen16(int4 v, uint32_t* o) {
+  widen4((uint32_t)v.x, o[0], o[1]);
+  widen4((uint32_t)v.y, o[2], o[3]);
+  widen4((uint32_t)v.z, o[4], o[5]);
+  widen4((uint32_t)v.w, o[6], o[7]);
+}
+
+struct Int8Unit {
+  int e, n0, rows, row0;
+};
+
+// A CTA's units in turn: row tile mt and n-tile ni of unit u, u + gridDim.x, ..
+struct Int8Cursor {
+  int u, mt, ni, m_step, n_step, n_tiles;
+  __device__ Int8Cursor(int n_tiles_) : u(blockIdx.x), n_tiles(n_tiles_) {
+    mt = u / n_tiles;
+    ni = u - mt * n_tiles;
+    m_step = (int)gridDim.x / n_tiles;
+    n_step = (int)gridDim.x - m_step * n_tiles;
+  }
+  __device__ void next() {
+    u += gridDim.x;
+    mt += m_step;
+    ni += n_step;
+    if (ni >= n_tiles) {
+      ni -= n_tiles;
+      ++mt;
+    }
+  }
+};
+
+__device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int width, int tile) {
+  // found by a whole warp: among every (E/32)th expert, then among those between
+  const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
+  const int far = lane * step;
+  const int block = (31 - __clz(__ballot_sync(0xffffffffu, far < p.E && pre[far] <= at.mt))) * step;
+  const int near = block + lane;
+  const int e = block + 31 - __clz(__ballot_sync(0xffffffffu, lane < step && near < p.E && pre[near] <= at.mt));
+  const int* first = pre + p.E + 1;
+  const int* count = first + p.E;
+  const int before = (at.mt - pre[e]) * tile;
+  return {e, at.ni * width, min(tile, count[e] - before), first[e] + before};
+}
+
+// How a launch cuts its work: rows a tile, weight rows a unit, stages.
+struct Int8Shape {
+  int tile, width, n_tiles;
+  uint32_t raw_stages, wide_stages, raw_bytes;
+};
+
+__device__ __forceinline__ Int8Shape int8_shape(int N, int E, int tile, int m_tiles) {
+  Int8Shape s;
+  s.tile = tile;
+  // 64 weight rows a unit where 128 would leave CTAs without one
+  int best = 0x7fffffff;
+  s.width = 128;
+  for (int b = 2; b >= 1; --b) {
+    const int units = m_tiles * ((N + 64 * b - 1) / (64 * b));
+    const int cost = (units + (int)gridDim.x - 1) / (int)gridDim.x * (max(356 * b, 128 * b + 6 * tile) + 64);
+    if (cost < best) {
+      best = cost;
+      s.width = 64 * b;
+    }
+  }
+  s.n_tiles = (N + s.width - 1) / s.width;
+  s.wide_stages = tile > 128 ? 2 : tile > 64 ? 3 : 4;
+  s.raw_bytes = (uint32_t)(s.width + tile) * 128;
+  s.raw_stages = min((uint32_t)kInt8RawStages,
+                     ((uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - s.wide_stages * tile * 256) / s.raw_bytes);
+  return s;
+}
+static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - 2 * kInt8MostRows * 256) / ((128 + kInt8MostRows) * 128) >= 2,
+              "two stages at least");
+
+// 32 neighbouring columns (rows c0 .. of the tile) of the accumulator by 32 weight rows (a lane each): scaled,
+// through the epilogue, turned around and stored. xs: the lane's row scale (of row c0 + lane).
+template <int YT, bool SWIGLU>
+__device__ __forceinline__ void int8_store(const Int8ProductParams& p, uint32_t turn, const uint32_t (&v)[32], float wscale, float xs,
+                                           int row0, int rows, int col) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    const float z0 = __uint_as_float(v[c]) * __shfl_sync(0xffffffffu, xs, c) * wscale;
+    const float z1 = __uint_as_float(v[c + 1]) * __shfl_sync(0xffffffffu, xs, c + 1) * wscale;
+    if (SWIGLU) {
+      // gates lie in the even lanes, what they gate in the odd ones: the even lane takes row c, the odd one row c + 1
+      const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? z0 : z1, 1);
+      const float h = lane & 1 ? int8_swiglu(got, z1) : int8_swiglu(z0, got);
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (c + (lane & 1)) * kInt8TurnRow + (lane >> 1) * 2), "h"(int8_round<YT>(h))
+                   : "memory");
+    } else {
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + c * kInt8TurnRow + lane * 2), "h"(int8_round<YT>(z0)) : "memory");
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (c + 1) * kInt8TurnRow + lane * 2), "h"(int8_round<YT>(z1)) : "memory");
+    }
+  }
+  __syncwarp();
+  constexpr int kCols = SWIGLU ? 16 : 32;  // results of a row
+  uint16_t* out = static_cast<uint16_t*>(p.y) + (size_t)row0 * p.C + col;
+  if ((p.C & 7) == 0) {
+    constexpr int kParts = kCols / 8;  // of 16 bytes
+    const int part = lane % kParts, r0 = lane / kParts;
+    const int last = col + part * 8 < p.C ? rows : 0;
+#pragma unroll
+    for (int r = r0; r < 32; r += 32 / kParts) {
+      const int4 w = lds_v4(turn + r * kInt8TurnRow + part * 16);
+      if (r < last) st_v4(out + (size_t)r * p.C + part * 8, w);
+    }
+  } else {
+    const int c = lane % kCols, last = col + c < p.C ? rows : 0;
+#pragma unroll 4
+    for (int r = lane / kCols; r < last; r += 32 / kCols) {
+      uint16_t w;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(turn + r * kInt8TurnRow + c * 2));
+      out[(size_t)r * p.C + c] = w;
+    }
+  }
+  __syncwarp();
+}
+
+template <int YT, bool SWIGLU>
+__global__ void __launch_bounds__(kInt8ProductThreads, 1)
+    int8_product_kernel(const __grid_constant__ Int8Maps maps, Int8ProductParams p) {
+  extern __shared__ __align__(1024) uint8_t psm_raw[];
+  __shared__ __align__(8) uint64_t raw_full[kInt8RawStages], raw_empty[kInt8RawStages];
+  __shared__ __align__(8) uint64_t wide_full[kInt8WideStages], wide_empty[kInt8WideStages];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ long long scan_scratch[32];
+  __shared__ int s_most[kInt8ProductThreads / 32];
+  __shared__ volatile int s_abort;
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
+  uint8_t* turn = sm + kInt8ProductSmem - 1024 - int8_fixed_smem(p.E);
+  int* pre = reinterpret_cast<int*>(turn + 4 * kInt8TurnWarp);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kInt8RawStages; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kWidenWarps);
+    }
+    for (int i = 0; i < kInt8WideStages; ++i) {
+      mbar_init(&wide_full[i], kWidenWarps);
+      mbar_init(&wide_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(&drained, 1);
+    mbar_fence_init();
+    s_abort = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  int most = __reduce_max_sync(0xffffffffu, int8_expert_rows<kInt8ProductThreads>(p, pre));
+  if (lane == 0) s_most[warp] = most;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  most = __reduce_max_sync(0xffffffffu, lane < kInt8ProductThreads / 32 ? s_most[lane] : 0);
+  const int tile = min(kInt8MostRows, max(32, (most + 31) / 32 * 32));
+  const bool countable = int8_row_tiles<kInt8ProductThreads>(p, tile, pre, scan_scratch);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  // overlapping experts can have more row tiles than the units' numbers hold: then none is worked on
+  const int m_tiles = countable ? __shfl_sync(0xffffffffu, pre[p.E], 0) : 0, KB = (p.K + kInt8Stage - 1) / kInt8Stage;
+  const Int8Shape shape = int8_shape(p.N, p.E, tile, m_tiles);
+  const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
+  const uint32_t raw_stages = __shfl_sync(0xffffffffu, shape.raw_stages, 0), raw_bytes = __shfl_sync(0xffffffffu, shape.raw_bytes, 0);
+  const uint32_t wide_stages = __shfl_sync(0xffffffffu, shape.wide_stages, 0), wide_bytes = tile * 256;
+  const int units = m_tiles * n_tiles;
+  // shared memory: the widened rows, then the copies' ring; tensor memory: two accumulators, then the widened weights
+  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + wide_stages * wide_bytes, tmem_a = tmem + 2 * tile;
+  const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty);
+  const uint32_t wide_full0 = smem_u32(wide_full), wide_empty0 = smem_u32(wide_empty);
+  const Int8Wait ab{&s_abort, p.status, p.timeout_ns};
+
+  if (warp == 0) {
+    const int w_boxes = width >> 6;
+    const bool leader = elect_one();
+    uint32_t stage = 0, phase = 1;
+    bool ok = true;
+    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
+      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
+                row = __shfl_sync(0xffffffffu, un.row0, 0), n0 = at.ni * width;
+      const int x_boxes = (rows + 31) / 32;
+      const uint32_t bytes = (uint32_t)(width + x_boxes * 32) * 128u;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = int8_wait_all(raw_empty0 + stage * 8, phase, ab);
+        if (!ok) break;
+        const uint32_t st = raw0 + stage * raw_bytes, bar = raw_full0 + stage * 8;
+        mbar_expect_tx_if(leader, bar, bytes);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          tma_load_3d_if(leader && b < w_boxes, st + b * 8192, &maps.w, kb * kInt8Stage, n0 + b * 64, e, bar);
+#pragma unroll
+        for (int b = 0; b < kInt8MostRows / 32; ++b)
+          tma_load_2d_if(leader && b < x_boxes, st + width * 128 + b * 4096, &maps.x, kb * kInt8Stage, row + b * 32, bar);
+        if (++stage == raw_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    const uint64_t bdesc0 = sw128_desc(sm);
+    const bool leader = elect_one();
+    uint32_t stage = 0, phase = 0, done = 0;
+    bool ok = true;
+    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
+      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const int rows = __shfl_sync(0xffffffffu, un.rows, 0);
+      const uint32_t idesc = idesc_f16((rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
+      ok = int8_wait_all(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
+      for (int kb = 0; kb < KB && ok; ++kb) {
+        ok = int8_wait_all(wide_full0 + stage * 8, phase, ab);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bdesc = bdesc0 + stage * (wide_bytes >> 4);
+        const uint32_t a = tmem_a + stage * 64, here = stage;
+        if (++stage == wide_stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        const int steps = min(8, (p.K - kb * kInt8Stage + 15) / 16);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // two panels of 64 elements, 128 bytes a row
+          tc_mma_f16_ts_if(leader && kk < steps, acc, a + kk * 8, bdesc + (kk >> 2) * (tile * 8) + (kk & 3) * 2, idesc,
+                           kk > 0 || kb > 0);
+        tc_commit_if(leader, wide_empty0 + here * 8);
+        tc_commit_if(leader && kb + 1 == KB, smem_u32(&acc_full[buf]));
+      }
+    }
+    if (leader) tc_commit(&drained);
+  } else if (warp >= kWidenWarp && warp < kWidenWarp + kWidenWarps) {
+    const uint32_t q = warp & 3, mine = warp - kWidenWarp, half = mine >> 2;
+    const uint32_t swz = lane & 7;  // rows are 8-row groups of 1 KB apart: a row's place in its group
+    const bool has_weights = (int)(q * 32) < width;
+    const uint32_t w_row = (q * 32 + lane) * 128;
+    const uint32_t x_from = width * 128 + lane * 128 + ((mine ^ swz) << 4);
+    const uint32_t x_to = sm0 + (mine >> 2) * (tile * 128) + lane * 128, chunk = (mine & 3) * 2;
+    const uint32_t to0 = x_to + ((chunk ^ swz) << 4), to1 = x_to + (((chunk + 1) ^ swz) << 4);
+    const uint32_t ta0 = tmem_a + ((q * 32) << 16) + half * 32;
+    uint32_t raw = 0, raw_phase = 0, wide = 0, wide_phase = 1;
+    bool ok = true;
+    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
+      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const int groups = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = int8_wait_warp(raw_full0 + raw * 8, raw_phase, ab) && int8_wait_warp(wide_empty0 + wide * 8, wide_phase, ab);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = raw0 + raw * raw_bytes;
+        if (has_weights) {
+          uint32_t v[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) widen16(lds_v4(st + w_row + (((half * 4 + j) ^ swz) << 4)), v + 8 * j);
+          tc_st32(ta0 + wide * 64, v);
+        }
+        const uint32_t off = wide * wide_bytes;
+#pragma unroll 2
+        for (int g = 0; g < groups; ++g) {
+          uint32_t v[8];
+          widen16(lds_v4(st + x_from + g * 4096), v);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to0 + off + g * 4096), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to1 + off + g * 4096), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                       : "memory");
+        }
+        tc_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_at(raw_empty0 + raw * 8);
+          mbar_arrive_at(wide_full0 + wide * 8);
+        }
+        if (++raw == raw_stages) {
+          raw = 0;
+          raw_phase ^= 1;
+        }
+        if (++wide == wide_stages) {
+          wide = 0;
+          wide_phase ^= 1;
+        }
+      }
+    }
+  } else if (warp >= kInt8EpilogueWarp) {
+    const uint32_t q = warp & 3;
+    const uint32_t my_turn = smem_u32(turn) + q * kInt8TurnWarp;
+    uint32_t done = 0;
+    for (Int8Cursor at(n_tiles); at.u < units; at.next(), ++done) {
+      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const uint32_t buf = done & 1;
+      const int n = un.n0 + 32 * (int)q;  // the warp's first weight row
+      const int groups = 32 * (int)q < width && n < p.N ? (un.rows + 31) / 32 : 0;
+      const float wscale = n + lane < p.N && groups ? p.ws[(size_t)un.e * p.N + n + lane] : 0.f;
+      if (!int8_wait_warp(smem_u32(&acc_full[buf]), (done >> 1) & 1, ab)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((32 * q) << 16) + buf * tile;
+#pragma unroll 1
+      for (int g = 0; g < groups; ++g) {
+        const int left = un.rows - 32 * g;
+        const float xs = p.xs && lane < left ? p.xs[un.row0 + 32 * g + lane] : 1.f;
+        uint32_t v[32];
+        tc_ld32(acc + 32 * g, v);
+        tc_wait_ld();
+        if (g + 1 == groups) {
+          // the last columns are in registers: the accumulator goes back before they are stored
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        }
+        int8_store<YT, SWIGLU>(p, my_turn, v, wscale, xs, un.row0 + 32 * g, min(32, left), SWIGLU ? n / 2 : n);
+      }
+      if (groups == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // the MMAs, and after an abort the copies in flight, end before their memory is given back
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(&drained, 0) && globaltimer_ns() - t0 < 1000000ull) {}
+    if (s_abort)
+      while (globaltimer_ns() - t0 < 1000000ull) {}
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // ------------------------------------------------------------- any k and alignment
@@ -84,7 +541,8 @@ __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8P
   extern __shared__ int pre[];
   pdl_wait();
   pdl_launch_dependents();
-  if (!int8_expert_rows<kPlainThreads>(p, kPlainRows, pre, scratch)) return;
+  int8_expert_rows<kPlainThreads>(p, pre);
+  if (!int8_row_tiles<kPlainThreads>(p, kPlainRows, pre, scratch)) return;
   const int* first = pre + p.E + 1;
   const int* count = first + p.E;
   const int n_tiles = (p.N + kPlainCols - 1) / kPlainCols;
@@ -92,9 +550,7 @@ __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8P
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int mt = (int)(u / n_tiles), n0 = (int)(u % n_tiles) * kPlainCols;
-    int e = 0;  // the last expert whose tiles begin at or before mt
-    for (int half = 512; half; half >>= 1)
-      if (e + half < p.E && pre[e + half] <= mt) e += half;
+    const int e = int8_expert_of(pre, p.E, mt);
     const int before = (mt - pre[e]) * kPlainRows, rows = min(kPlainRows, count[e] - before);
     const long long row0 = first[e] + before;
     int acc[2][4] = {};
@@ -136,8 +592,7 @@ __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8P
         const int c = (SWIGLU ? n0 / 2 + tx * 2 : n0 + tx * 4) + b;
         if (c >= p.C) continue;
         const float v = SWIGLU ? int8_swiglu(z[(2 * b) & 3], z[(2 * b + 1) & 3]) : z[b];
-        static_cast<uint16_t*>(p.y)[(size_t)(row0 + r) * p.C + c] =
-            YT == MOE_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        static_cast<uint16_t*>(p.y)[(size_t)(row0 + r) * p.C + c] = int8_round<YT>(v);
       }
     }
   }
@@ -145,7 +600,35 @@ __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8P
 
 // ------------------------------------------------------------- host side
 
+static PFN_cuTensorMapEncodeTiled_v12000 int8_encode_fn() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Matrices [depth][rows][cols] of int8, boxes of 128 columns x box_rows rows; zeros beyond the ends.
+static bool int8_map(CUtensorMap* m, const void* base, unsigned long long cols, unsigned long long rows, unsigned long long depth,
+                     unsigned box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = int8_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cols, rows, depth};
+  cuuint64_t strides[2] = {cols, cols * rows};
+  cuuint32_t box[3] = {(cuuint32_t)kInt8Stage, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 typedef void (*Int8PlainKernel)(Int8ProductParams);
+typedef void (*Int8Kernel)(Int8Maps, Int8ProductParams);
 
 }  // namespace crs
 
@@ -162,7 +645,9 @@ extern "C" moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const i
   const int E = cfg->moe_expert_num, W = cfg->ep_world_size;
   if (epilogue == MOE_EPI_SWIGLU && n % 2) return MOE_ERR_INVALID_ARG;
   if (y_dtype != MOE_F16 && y_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  if ((long long)E * n >= 2147483647LL) return MOE_ERR_INVALID_ARG;
+  // units of a row tile x 64 weight rows are counted in 32 bits, and a CTA looks some of its units ahead
+  const long long most_units = ((long long)W * A / 32 + E) * ((n + 63LL) / 64);
+  if ((long long)E * n >= 2147483647LL || most_units >= 2147483647LL - 65536) return MOE_ERR_INVALID_ARG;
   if (!ep_recv_count || (A > 0 && (!x || !w || !w_scales || !y))) return MOE_ERR_INVALID_ARG;
   auto aligned = [](const void* p, size_t a) { return ((uintptr_t)p % a) == 0; };
   if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(ep_recv_count, 4) || !aligned(w, 16) || !aligned(w_scales, 4) ||
@@ -187,12 +672,28 @@ extern "C" moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const i
   p.C = epilogue == MOE_EPI_SWIGLU ? n / 2 : n;
   p.A = A;
   p.status = &static_cast<WsHeader*>(ws)->status;
+  p.timeout_ns = (uint64_t)cfg->wait_timeout_us * 1000ull;
   const bool sw = epilogue == MOE_EPI_SWIGLU;
+  int per_sm = 0;
+  if (k % 16 == 0) {
+    Int8Maps maps;
+    if (!int8_map(&maps.x, x, (unsigned long long)k, (unsigned long long)W * A, 0, 32) ||
+        !int8_map(&maps.w, w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, 64))
+      return MOE_ERR_CUDA;
+    const Int8Kernel kernel = y_dtype == MOE_F16 ? (sw ? int8_product_kernel<MOE_F16, true> : int8_product_kernel<MOE_F16, false>)
+                                                 : (sw ? int8_product_kernel<MOE_BF16, true> : int8_product_kernel<MOE_BF16, false>);
+    if (resident_blocks((const void*)kernel, kInt8ProductThreads, kInt8ProductSmem, &per_sm) != cudaSuccess || per_sm < 1)
+      return MOE_ERR_CUDA;
+    PdlLaunch L(dim3((unsigned)(most_units < nsm ? most_units : nsm)), dim3(kInt8ProductThreads), kInt8ProductSmem,
+                static_cast<cudaStream_t>(stream));
+    if (cudaLaunchKernelEx(&L.cfg, kernel, maps, p) != cudaSuccess) return MOE_ERR_CUDA;
+    note_launches(1);
+    return MOE_OK;
+  }
   const Int8PlainKernel plain =
       y_dtype == MOE_F16 ? (sw ? int8_product_plain_kernel<MOE_F16, true> : int8_product_plain_kernel<MOE_F16, false>)
                          : (sw ? int8_product_plain_kernel<MOE_BF16, true> : int8_product_plain_kernel<MOE_BF16, false>);
   const size_t smem = (3 * (size_t)E + 1) * 4;
-  int per_sm = 0;
   if (resident_blocks((const void*)plain, kPlainThreads, smem, &per_sm) != cudaSuccess || per_sm < 1) return MOE_ERR_CUDA;
   PdlLaunch L(dim3((unsigned)(nsm * per_sm)), dim3(kPlainThreads), smem, static_cast<cudaStream_t>(stream));
   if (cudaLaunchKernelEx(&L.cfg, plain, p) != cudaSuccess) return MOE_ERR_CUDA;
