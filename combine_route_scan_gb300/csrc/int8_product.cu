@@ -5,18 +5,19 @@
 // sm_103a's integer tensor rate is a small part of its fp16 rate, and fp16 holds every
 // int8 exactly, products below 2^14 and sums to 2^24 in fp32 too: the codes are
 // widened to fp16 on the way from shared memory to the tensor cores.
-//   * a unit is 128 weight rows of an expert (the MMA's A operand) against up to 192 of
-//     its rows (B), K in stages of 128 elements. Weights are A because A may come from
-//     TMEM: a weight goes TMA -> shared memory -> registers -> TMEM, 2 bytes of shared-memory
-//     traffic for each; a row's element, written back as fp16 and read by the
-//     MMA, takes 6. Shared memory (128 bytes a clock) and not the MMA bounds a unit of many rows;
-//     with few rows the weights' stream from HBM does;
+//   * two CTAs share a unit (cta_group::2): 256 weight rows of an expert, 128 each (the MMA's A
+//     operand), against up to 192 of its rows (B, half of them widened in each). Weights are A
+//     because A may come from TMEM: a weight goes TMA -> shared memory -> registers -> TMEM, 2
+//     bytes of shared-memory traffic for each; a row's element, written back as fp16 and
+//     read by the MMA, takes 6. Shared memory's 128 bytes a clock bound a unit of many rows: in one CTA
+//     128 x 192 took 235 bytes for each clock of the MMA, in a pair 139;
 //   * four bytes become two fp16 pairs by (w & 0x00ff00ff) ^ 0x64806480 = 1152 + value, less
 //     1152: bytes 0 and 2, and shifted by 8 bytes 1 and 3. The order of K that this gives is
 //     the same for both operands;
-//   * warps: 0 TMA, 1 MMA, 4..11 widen (each thread half a weight row a stage, each warp
-//     16 elements of all rows), 12..15 epilogue. Two accumulators, so that the
-//     next unit's MMAs run while this one is read.
+//   * copies bring 128 elements of K a stage; two sets of eight warps widen 64 of them each, into
+//     two slots a set in turn (four in all: 32 columns of TMEM for the weights);
+//   * warps: 0 TMA, 1 MMA (of the pair's first CTA), 2..17 widen, 18..21 epilogue. Two accumulators, so
+//     that the next unit's MMAs run while this one is read.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -110,17 +111,17 @@ __device__ __forceinline__ uint16_t int8_round(float v) {
 
 // ------------------------------------------------------------- the tensor cores
 
-// Boxes of 32 rows of x and of 64 rows of w, 128 elements of K.
+// Boxes of 16 rows of x and of 64 rows of w, 128 elements of K.
 struct Int8Maps {
   CUtensorMap x, w;
 };
 
-constexpr int kInt8ProductThreads = 512;
-constexpr int kWidenWarp = 4, kWidenWarps = 8, kInt8EpilogueWarp = 12;
+constexpr int kWidenWarp = 2, kWidenWarps = 16;
+constexpr int kInt8ProductThreads = 22 * 32;
 constexpr int kInt8Stage = 128;    // elements of K a stage
 constexpr int kInt8MostRows = 192; // MMA N
 constexpr int kInt8RawStages = 8;  // at most
-constexpr int kInt8WideStages = 4; // at most
+constexpr int kInt8Slots = 4;      // of 64 elements of K, widened
 // An epilogue warp turns 32 rows x 32 results of 2 bytes around in shared memory, rows 80 bytes apart.
 constexpr uint32_t kInt8TurnRow = 80, kInt8TurnWarp = 32 * kInt8TurnRow;
 constexpr size_t kInt8ProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
@@ -134,34 +135,28 @@ struct Int8Wait {
 };
 
 // A wait of the pipeline, bounded by `limit` once it has lasted a while.
-__device__ __forceinline__ bool int8_wait(uint32_t bar, uint32_t parity, const Int8Wait& a) {
-#pragma unroll 1
-  for (int it = 0; it < 64; ++it)
-    if (mbar_try_wait(bar, parity)) return true;
+static __device__ __noinline__ bool int8_wait_long(uint32_t bar, uint32_t parity, volatile int* flag, int* status, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
   for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 63u) {
-      if (*a.flag) return false;
-      if (globaltimer_ns() - t0 > a.limit) {
-        set_error(a.status, MOE_ERR_TIMEOUT);
-        *a.flag = 1;
+      if (*flag) return false;
+      if (globaltimer_ns() - t0 > limit) {
+        set_error(status, MOE_ERR_TIMEOUT);
+        *flag = 1;
         return false;
       }
     }
   }
 }
-// The same for a whole warp, one lane asking, with one answer for all.
-__device__ __forceinline__ bool int8_wait_warp(uint32_t bar, uint32_t parity, const Int8Wait& a) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = int8_wait(bar, parity, a);
-  return __all_sync(0xffffffffu, ok);
-}
-// The same, all lanes asking: nothing of it diverges when the phase is there at once.
-__device__ __forceinline__ bool int8_wait_all(uint32_t bar, uint32_t parity, const Int8Wait& a) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, int8_wait(bar, parity, a));
+// All lanes of a warp ask, with one answer for all: nothing of it diverges when the phase is there. (One lane asking for
+// the others cost 330 clocks for a phase that was there.)
+__device__ __forceinline__ bool int8_wait(uint32_t bar, uint32_t parity, const Int8Wait& a) {
+#pragma unroll 1
+  for (int it = 0; it < 64; ++it)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, int8_wait_long(bar, parity, a.flag, a.status, a.limit));
 }
 
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
@@ -193,17 +188,18 @@ struct Int8Unit {
   int e, n0, rows, row0;
 };
 
-// A CTA's units in turn: row tile mt and n-tile ni of unit u, u + gridDim.x, ..
+// A pair's units in turn: row tile mt and n-tile ni of unit u, u + pairs, ..
 struct Int8Cursor {
   int u, mt, ni, m_step, n_step, n_tiles;
-  __device__ Int8Cursor(int n_tiles_) : u(blockIdx.x), n_tiles(n_tiles_) {
+  __device__ Int8Cursor(int n_tiles_) : u(blockIdx.x >> 1), n_tiles(n_tiles_) {
+    const int pairs = gridDim.x >> 1;
     mt = u / n_tiles;
     ni = u - mt * n_tiles;
-    m_step = (int)gridDim.x / n_tiles;
-    n_step = (int)gridDim.x - m_step * n_tiles;
+    m_step = pairs / n_tiles;
+    n_step = pairs - m_step * n_tiles;
   }
   __device__ void next() {
-    u += gridDim.x;
+    u += gridDim.x >> 1;
     mt += m_step;
     ni += n_step;
     if (ni >= n_tiles) {
@@ -226,35 +222,34 @@ __device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const 
   return {e, at.ni * width, min(tile, count[e] - before), first[e] + before};
 }
 
-// How a launch cuts its work: rows a tile, weight rows a unit, stages.
+// How a launch cuts its work: weight rows a unit (half of them for each CTA), and as many stages as shared memory holds.
 struct Int8Shape {
-  int tile, width, n_tiles;
-  uint32_t raw_stages, wide_stages, raw_bytes;
+  int width, n_tiles;
+  uint32_t raw_stages, raw_bytes;
 };
 
 __device__ __forceinline__ Int8Shape int8_shape(int N, int E, int tile, int m_tiles) {
   Int8Shape s;
-  s.tile = tile;
-  // 64 weight rows a unit where 128 would leave CTAs without one
+  const int pairs = gridDim.x >> 1;
+  // 2 x 64 weight rows a unit where 2 x 128 would leave pairs without one
   int best = 0x7fffffff;
-  s.width = 128;
+  s.width = 256;
   for (int b = 2; b >= 1; --b) {
-    const int units = m_tiles * ((N + 64 * b - 1) / (64 * b));
-    const int cost = (units + (int)gridDim.x - 1) / (int)gridDim.x * (max(356 * b, 128 * b + 6 * tile) + 64);
+    const int units = m_tiles * ((N + 128 * b - 1) / (128 * b));
+    const int cost = (units + pairs - 1) / pairs * (max(356 * b, 128 * b + 3 * tile) + 64);
     if (cost < best) {
       best = cost;
-      s.width = 64 * b;
+      s.width = 128 * b;
     }
   }
   s.n_tiles = (N + s.width - 1) / s.width;
-  s.wide_stages = tile > 128 ? 2 : tile > 64 ? 3 : 4;
-  s.raw_bytes = (uint32_t)(s.width + tile) * 128;
-  s.raw_stages = min((uint32_t)kInt8RawStages,
-                     ((uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - s.wide_stages * tile * 256) / s.raw_bytes);
+  s.raw_bytes = (uint32_t)(s.width + tile) * 64;
+  s.raw_stages =
+      min((uint32_t)kInt8RawStages, ((uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - kInt8Slots * tile * 64) / s.raw_bytes);
   return s;
 }
-static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - 2 * kInt8MostRows * 256) / ((128 + kInt8MostRows) * 128) >= 2,
-              "two stages at least");
+static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - kInt8Slots * kInt8MostRows * 64) / ((256 + kInt8MostRows) * 64) >= 4,
+              "four stages at least");
 
 // 32 neighbouring columns (rows c0 .. of the tile) of the accumulator by 32 weight rows (a lane each): scaled,
 // through the epilogue, turned around and stored. xs: the lane's row scale (of row c0 + lane).
@@ -302,18 +297,19 @@ __device__ __forceinline__ void int8_store(const Int8ProductParams& p, uint32_t 
 }
 
 template <int YT, bool SWIGLU>
-__global__ void __launch_bounds__(kInt8ProductThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads, 1)
     int8_product_kernel(const __grid_constant__ Int8Maps maps, Int8ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
   __shared__ __align__(8) uint64_t raw_full[kInt8RawStages], raw_empty[kInt8RawStages];
-  __shared__ __align__(8) uint64_t wide_full[kInt8WideStages], wide_empty[kInt8WideStages];
-  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(8) uint64_t wide_full[kInt8Slots], wide_empty[kInt8Slots];  // full: of the first CTA, for both
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drained;              // empty: of the first CTA, for both
   __shared__ uint32_t tmem_slot;
   __shared__ long long scan_scratch[32];
   __shared__ int s_most[kInt8ProductThreads / 32];
   __shared__ volatile int s_abort;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   uint8_t* turn = sm + kInt8ProductSmem - 1024 - int8_fixed_smem(p.E);
   int* pre = reinterpret_cast<int*>(turn + 4 * kInt8TurnWarp);
@@ -323,21 +319,22 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kWidenWarps);
     }
-    for (int i = 0; i < kInt8WideStages; ++i) {
-      mbar_init(&wide_full[i], kWidenWarps);
+    for (int i = 0; i < kInt8Slots; ++i) {
+      mbar_init(&wide_full[i], kWidenWarps);  // a set's eight warps in each CTA
       mbar_init(&wide_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 8);
     }
     mbar_init(&drained, 1);
     mbar_fence_init();
     s_abort = 0;
   }
+  cluster_sync();  // the other CTA's barriers are there before anything arrives on them
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(&tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -355,28 +352,29 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
   const int m_tiles = countable ? __shfl_sync(0xffffffffu, pre[p.E], 0) : 0, KB = (p.K + kInt8Stage - 1) / kInt8Stage;
   const Int8Shape shape = int8_shape(p.N, p.E, tile, m_tiles);
   const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
+  const int half = width >> 1;  // this CTA's weight rows of a unit
   const uint32_t raw_stages = __shfl_sync(0xffffffffu, shape.raw_stages, 0), raw_bytes = __shfl_sync(0xffffffffu, shape.raw_bytes, 0);
-  const uint32_t wide_stages = __shfl_sync(0xffffffffu, shape.wide_stages, 0), wide_bytes = tile * 256;
+  const uint32_t slot_bytes = tile * 64;
   const int units = m_tiles * n_tiles;
   // shared memory: the widened rows, then the copies' ring; tensor memory: two accumulators, then the widened weights
-  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + wide_stages * wide_bytes, tmem_a = tmem + 2 * tile;
+  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + kInt8Slots * slot_bytes, tmem_a = tmem + 2 * tile;
   const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty);
   const uint32_t wide_full0 = smem_u32(wide_full), wide_empty0 = smem_u32(wide_empty);
   const Int8Wait ab{&s_abort, p.status, p.timeout_ns};
 
   if (warp == 0) {
-    const int w_boxes = width >> 6;
+    const int w_boxes = half >> 6;
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
     bool ok = true;
     for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
       const Int8Unit un = int8_unit(p, pre, at, width, tile);
-      const int rows = __shfl_sync(0xffffffffu, un.rows, 0), e = __shfl_sync(0xffffffffu, un.e, 0),
-                row = __shfl_sync(0xffffffffu, un.row0, 0), n0 = at.ni * width;
-      const int x_boxes = (rows + 31) / 32;
-      const uint32_t bytes = (uint32_t)(width + x_boxes * 32) * 128u;
+      const int x_boxes = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32;  // of 16 rows, in each CTA
+      const int e = __shfl_sync(0xffffffffu, un.e, 0), n0 = at.ni * width + (int)rank * half;
+      const int row = __shfl_sync(0xffffffffu, un.row0, 0) + (int)rank * x_boxes * 16;
+      const uint32_t bytes = (uint32_t)(half + x_boxes * 16) * 128u;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = int8_wait_all(raw_empty0 + stage * 8, phase, ab);
+        ok = int8_wait(raw_empty0 + stage * 8, phase, ab);
         if (!ok) break;
         const uint32_t st = raw0 + stage * raw_bytes, bar = raw_full0 + stage * 8;
         mbar_expect_tx_if(leader, bar, bytes);
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
           tma_load_3d_if(leader && b < w_boxes, st + b * 8192, &maps.w, kb * kInt8Stage, n0 + b * 64, e, bar);
 #pragma unroll
         for (int b = 0; b < kInt8MostRows / 32; ++b)
-          tma_load_2d_if(leader && b < x_boxes, st + width * 128 + b * 4096, &maps.x, kb * kInt8Stage, row + b * 32, bar);
+          tma_load_2d_if(leader && b < x_boxes, st + half * 128 + b * 2048, &maps.x, kb * kInt8Stage, row + b * 16, bar);
         if (++stage == raw_stages) {
           stage = 0;
           phase ^= 1;
@@ -393,68 +391,73 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
       }
     }
   } else if (warp == 1) {
-    const uint64_t bdesc0 = sw128_desc(sm);
-    const bool leader = elect_one();
-    uint32_t stage = 0, phase = 0, done = 0;
-    bool ok = true;
-    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
-      const Int8Unit un = int8_unit(p, pre, at, width, tile);
-      const int rows = __shfl_sync(0xffffffffu, un.rows, 0);
-      const uint32_t idesc = idesc_f16((rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
-      ok = int8_wait_all(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
-      for (int kb = 0; kb < KB && ok; ++kb) {
-        ok = int8_wait_all(wide_full0 + stage * 8, phase, ab);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t bdesc = bdesc0 + stage * (wide_bytes >> 4);
-        const uint32_t a = tmem_a + stage * 64, here = stage;
-        if (++stage == wide_stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-        const int steps = min(8, (p.K - kb * kInt8Stage + 15) / 16);
+    if (rank == 0) {
+      const uint64_t bdesc0 = sw128_desc(sm);
+      const bool leader = elect_one();
+      uint32_t slot = 0, phase = 0, done = 0;
+      bool ok = true;
+      for (Int8Cursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
+        const Int8Unit un = int8_unit(p, pre, at, width, tile);
+        const int rows = __shfl_sync(0xffffffffu, un.rows, 0);
+        const uint32_t idesc = idesc_f16_pair((rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
+        ok = int8_wait(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
+        for (int kb = 0; kb < 2 * KB && ok; ++kb) {
+          ok = int8_wait(wide_full0 + slot * 8, phase, ab);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bdesc = bdesc0 + slot * (slot_bytes >> 4);
+          const uint32_t a = tmem_a + slot * 32, here = slot;
+          if (++slot == kInt8Slots) {
+            slot = 0;
+            phase ^= 1;
+          }
+          const int steps = (p.K - kb * (kInt8Stage / 2) + 15) / 16;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)  // two panels of 64 elements, 128 bytes a row
-          tc_mma_f16_ts_if(leader && kk < steps, acc, a + kk * 8, bdesc + (kk >> 2) * (tile * 8) + (kk & 3) * 2, idesc,
-                           kk > 0 || kb > 0);
-        tc_commit_if(leader, wide_empty0 + here * 8);
-        tc_commit_if(leader && kb + 1 == KB, smem_u32(&acc_full[buf]));
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_pair_if(leader && kk < steps, acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
+          tc_commit_pair_if(leader, wide_empty0 + here * 8);
+          tc_commit_pair_if(leader && kb + 1 == 2 * KB, smem_u32(&acc_full[buf]));
+        }
       }
+      tc_commit_pair_if(leader, smem_u32(&drained));
     }
-    if (leader) tc_commit(&drained);
-  } else if (warp >= kWidenWarp && warp < kWidenWarp + kWidenWarps) {
-    const uint32_t q = warp & 3, mine = warp - kWidenWarp, half = mine >> 2;
-    const uint32_t swz = lane & 7;  // rows are 8-row groups of 1 KB apart: a row's place in its group
-    const bool has_weights = (int)(q * 32) < width;
-    const uint32_t w_row = (q * 32 + lane) * 128;
-    const uint32_t x_from = width * 128 + lane * 128 + ((mine ^ swz) << 4);
-    const uint32_t x_to = sm0 + (mine >> 2) * (tile * 128) + lane * 128, chunk = (mine & 3) * 2;
-    const uint32_t to0 = x_to + ((chunk ^ swz) << 4), to1 = x_to + (((chunk + 1) ^ swz) << 4);
-    const uint32_t ta0 = tmem_a + ((q * 32) << 16) + half * 32;
-    uint32_t raw = 0, raw_phase = 0, wide = 0, wide_phase = 1;
+  } else if (warp < kWidenWarp + kWidenWarps) {
+    // the set's half of each stage: a thread has 32 elements of a weight row, a warp 16 rows x 32 elements of x at a time
+    const uint32_t mine = warp - kWidenWarp, set = mine >> 3, w = mine & 7, q = warp & 3, part = w >> 2;
+    const uint32_t swz = lane & 7;  // a row's place in its group of 8, which the copies' and the MMA's swizzle go by
+    const bool has_weights = (int)(q * 32) < half;
+    const uint32_t w_row = (q * 32 + lane) * 128, w0 = w_row + (((set * 4 + part * 2) ^ swz) << 4),
+                   w1 = w_row + (((set * 4 + part * 2 + 1) ^ swz) << 4);
+    const uint32_t ta0 = tmem_a + ((q * 32) << 16) + part * 16;
+    // x: block of 16 rows t >> 1, chunks (t & 1) * 2 and the next, of task t = w, w + 8, ..
+    const uint32_t chunk = (w & 1) * 2 + (lane >> 4), x_row = (w >> 1) * 2048 + (lane & 15) * 128;
+    const uint32_t x_from = half * 128 + x_row + (((set * 4 + chunk) ^ swz) << 4);
+    const uint32_t x_to0 = sm0 + x_row + (((2 * chunk) ^ swz) << 4), x_to1 = sm0 + x_row + (((2 * chunk + 1) ^ swz) << 4);
+    const uint32_t full0 = cluster_addr(wide_full0, 0);
+    uint32_t raw = 0, raw_phase = 0, slot = set, slot_phase = 1;
     bool ok = true;
     for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
       const Int8Unit un = int8_unit(p, pre, at, width, tile);
-      const int groups = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32;
+      const int tasks = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32 * 2;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = int8_wait_warp(raw_full0 + raw * 8, raw_phase, ab) && int8_wait_warp(wide_empty0 + wide * 8, wide_phase, ab);
+        ok = int8_wait(raw_full0 + raw * 8, raw_phase, ab) && int8_wait(wide_empty0 + slot * 8, slot_phase, ab);
         if (!ok) break;
         tc_fence_after();
         const uint32_t st = raw0 + raw * raw_bytes;
         if (has_weights) {
-          uint32_t v[32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) widen16(lds_v4(st + w_row + (((half * 4 + j) ^ swz) << 4)), v + 8 * j);
-          tc_st32(ta0 + wide * 64, v);
+          const int4 a = lds_v4(st + w0), b = lds_v4(st + w1);
+          uint32_t v[16];
+          widen16(a, v);
+          widen16(b, v + 8);
+          tc_st16(ta0 + slot * 32, v);
         }
-        const uint32_t off = wide * wide_bytes;
-#pragma unroll 2
-        for (int g = 0; g < groups; ++g) {
+        const uint32_t off = slot * slot_bytes;
+        for (int t = w, g = 0; t < tasks; t += 8, g += 8192) {
           uint32_t v[8];
-          widen16(lds_v4(st + x_from + g * 4096), v);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to0 + off + g * 4096), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+          widen16(lds_v4(st + x_from + g), v);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to0 + off + g), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                        : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to1 + off + g * 4096), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to1 + off + g), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                        : "memory");
         }
         tc_wait_st();
@@ -463,29 +466,28 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_at(raw_empty0 + raw * 8);
-          mbar_arrive_at(wide_full0 + wide * 8);
+          mbar_arrive_cluster(full0 + slot * 8);
         }
         if (++raw == raw_stages) {
           raw = 0;
           raw_phase ^= 1;
         }
-        if (++wide == wide_stages) {
-          wide = 0;
-          wide_phase ^= 1;
-        }
+        slot ^= 2;
+        slot_phase ^= slot == set;
       }
     }
-  } else if (warp >= kInt8EpilogueWarp) {
+  } else {
     const uint32_t q = warp & 3;
     const uint32_t my_turn = smem_u32(turn) + q * kInt8TurnWarp;
+    const uint32_t empty0 = cluster_addr(smem_u32(acc_empty), 0);
     uint32_t done = 0;
     for (Int8Cursor at(n_tiles); at.u < units; at.next(), ++done) {
       const Int8Unit un = int8_unit(p, pre, at, width, tile);
       const uint32_t buf = done & 1;
-      const int n = un.n0 + 32 * (int)q;  // the warp's first weight row
-      const int groups = 32 * (int)q < width && n < p.N ? (un.rows + 31) / 32 : 0;
+      const int n = un.n0 + (int)rank * half + 32 * (int)q;  // the warp's first weight row
+      const int groups = 32 * (int)q < half && n < p.N ? (un.rows + 31) / 32 : 0;
       const float wscale = n + lane < p.N && groups ? p.ws[(size_t)un.e * p.N + n + lane] : 0.f;
-      if (!int8_wait_warp(smem_u32(&acc_full[buf]), (done >> 1) & 1, ab)) break;
+      if (!int8_wait(smem_u32(&acc_full[buf]), (done >> 1) & 1, ab)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((32 * q) << 16) + buf * tile;
 #pragma unroll 1
@@ -499,21 +501,21 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
           // the last columns are in registers: the accumulator goes back before they are stored
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[buf]);
+          if (lane == 0) mbar_arrive_cluster(empty0 + buf * 8);
         }
         int8_store<YT, SWIGLU>(p, my_turn, v, wscale, xs, un.row0 + 32 * g, min(32, left), SWIGLU ? n / 2 : n);
       }
       if (groups == 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (lane == 0) mbar_arrive_cluster(empty0 + buf * 8);
       }
     }
   }
 
   __syncthreads();
   if (threadIdx.x == 0) {
-    // the MMAs, and after an abort the copies in flight, end before their memory is given back
+    // the pair's MMAs, and after an abort the copies in flight, end before their memory is given back
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(&drained, 0) && globaltimer_ns() - t0 < 1000000ull) {}
     if (s_abort)
@@ -521,10 +523,12 @@ __global__ void __launch_bounds__(kInt8ProductThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // nor does a CTA leave while the other one may still arrive on its barriers
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
+  cluster_sync();
 }
 
 // ------------------------------------------------------------- any k and alignment
@@ -677,14 +681,16 @@ extern "C" moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const i
   int per_sm = 0;
   if (k % 16 == 0) {
     Int8Maps maps;
-    if (!int8_map(&maps.x, x, (unsigned long long)k, (unsigned long long)W * A, 0, 32) ||
+    if (!int8_map(&maps.x, x, (unsigned long long)k, (unsigned long long)W * A, 0, 16) ||
         !int8_map(&maps.w, w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, 64))
       return MOE_ERR_CUDA;
     const Int8Kernel kernel = y_dtype == MOE_F16 ? (sw ? int8_product_kernel<MOE_F16, true> : int8_product_kernel<MOE_F16, false>)
                                                  : (sw ? int8_product_kernel<MOE_BF16, true> : int8_product_kernel<MOE_BF16, false>);
     if (resident_blocks((const void*)kernel, kInt8ProductThreads, kInt8ProductSmem, &per_sm) != cudaSuccess || per_sm < 1)
       return MOE_ERR_CUDA;
-    PdlLaunch L(dim3((unsigned)(most_units < nsm ? most_units : nsm)), dim3(kInt8ProductThreads), kInt8ProductSmem,
+    const long long pairs = most_units < nsm / 2 ? most_units : nsm / 2;
+    if (pairs < 1) return MOE_ERR_CUDA;
+    PdlLaunch L(dim3((unsigned)(2 * pairs)), dim3(kInt8ProductThreads), kInt8ProductSmem,
                 static_cast<cudaStream_t>(stream));
     if (cudaLaunchKernelEx(&L.cfg, kernel, maps, p) != cudaSuccess) return MOE_ERR_CUDA;
     note_launches(1);
