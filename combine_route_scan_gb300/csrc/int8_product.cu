@@ -14,8 +14,10 @@
 //   * four bytes become two fp16 pairs by (w & 0x00ff00ff) ^ 0x64806480 = 1152 + value, less
 //     1152: bytes 0 and 2, and shifted by 8 bytes 1 and 3. The order of K that this gives is
 //     the same for both operands;
-//   * copies bring 128 elements of K a stage; two sets of eight warps widen 64 of them each, into
-//     two slots a set in turn (four in all: 32 columns of TMEM for the weights);
+//   * copies bring 128 elements of K a stage; two sets of eight warps widen them in turn, a stage
+//     each, into four or six slots of TMEM and shared memory. Two accumulators of more than
+//     128 columns leave TMEM for two such slots: then a slot is half a stage, and each
+//     set has its half of every stage;
 //   * warps: 0 TMA, 1 MMA (of the pair's first CTA), 2..17 widen, 18..21 epilogue. Two accumulators, so
 //     that the next unit's MMAs run while this one is read.
 #include <cuda.h>
@@ -111,9 +113,9 @@ __device__ __forceinline__ uint16_t int8_round(float v) {
 
 // ------------------------------------------------------------- the tensor cores
 
-// Boxes of 16 rows of x and of 64 rows of w, 128 elements of K.
+// Boxes of 16, 32, .. rows of x and of 64 and 128 rows of w, 128 elements of K: one copy of each a stage.
 struct Int8Maps {
-  CUtensorMap x, w;
+  CUtensorMap x[6], w[2];
 };
 
 constexpr int kWidenWarp = 2, kWidenWarps = 16;
@@ -121,12 +123,21 @@ constexpr int kInt8ProductThreads = 22 * 32;
 constexpr int kInt8Stage = 128;    // elements of K a stage
 constexpr int kInt8MostRows = 192; // MMA N
 constexpr int kInt8RawStages = 8;  // at most
-constexpr int kInt8Slots = 4;      // of 64 elements of K, widened
+constexpr int kInt8Slots = 6;      // at most
 // An epilogue warp turns 32 rows x 32 results of 2 bytes around in shared memory, rows 80 bytes apart.
 constexpr uint32_t kInt8TurnRow = 80, kInt8TurnWarp = 32 * kInt8TurnRow;
 constexpr size_t kInt8ProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
 
-__host__ __device__ constexpr uint32_t int8_fixed_smem(int E) { return 4 * kInt8TurnWarp + ((3u * E + 1) * 4 + 127) / 128 * 128; }
+// Behind the ring: the epilogue warps' turning places and row scales, the experts' tiles.
+__host__ __device__ constexpr uint32_t int8_fixed_smem(int E) {
+  return 4 * (kInt8TurnWarp + kInt8MostRows * 4) + ((3u * E + 1) * 4 + 127) / 128 * 128;
+}
+// Halves of a stage in a slot (32 columns of TMEM each), and slots beside two accumulators of `tile` columns.
+__host__ __device__ constexpr int int8_halves(int tile) { return tile > 128 ? 1 : 2; }
+__host__ __device__ constexpr uint32_t int8_slots(int tile) { return tile > 64 ? 4 : 6; }
+static_assert(2 * 192 + int8_slots(192) * 32 * int8_halves(192) <= 512 && 2 * 128 + int8_slots(128) * 32 * int8_halves(128) <= 512 &&
+                  2 * 64 + int8_slots(64) * 32 * int8_halves(64) <= 512, "TMEM");
+static_assert(kInt8MostRows == 192, "six boxes of x");
 
 struct Int8Wait {
   volatile int* flag;
@@ -134,33 +145,42 @@ struct Int8Wait {
   uint64_t limit;
 };
 
+// A barrier's phase, asleep until it comes or some microseconds have passed. (Without the hint the waiting warps' asking
+// took two thirds of the issue slots.)
+__device__ __forceinline__ bool int8_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
 // A wait of the pipeline, bounded by `limit` once it has lasted a while.
 static __device__ __noinline__ bool int8_wait_long(uint32_t bar, uint32_t parity, volatile int* flag, int* status, uint64_t limit) {
   const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 63u) {
-      if (*flag) return false;
-      if (globaltimer_ns() - t0 > limit) {
-        set_error(status, MOE_ERR_TIMEOUT);
-        *flag = 1;
-        return false;
-      }
+  for (;;) {
+    if (int8_sleep(bar, parity)) return true;
+    if (*flag) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      set_error(status, MOE_ERR_TIMEOUT);
+      *flag = 1;
+      return false;
     }
   }
 }
 // All lanes of a warp ask, with one answer for all: nothing of it diverges when the phase is there. (One lane asking for
 // the others cost 330 clocks for a phase that was there.)
 __device__ __forceinline__ bool int8_wait(uint32_t bar, uint32_t parity, const Int8Wait& a) {
-#pragma unroll 1
-  for (int it = 0; it < 64; ++it)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, int8_sleep(bar, parity))) return true;
   return __all_sync(0xffffffffu, int8_wait_long(bar, parity, a.flag, a.status, a.limit));
 }
 
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 __device__ __forceinline__ int4 lds_v4(uint32_t at) {
   int4 v;
@@ -245,31 +265,48 @@ __device__ __forceinline__ Int8Shape int8_shape(int N, int E, int tile, int m_ti
   s.n_tiles = (N + s.width - 1) / s.width;
   s.raw_bytes = (uint32_t)(s.width + tile) * 64;
   s.raw_stages =
-      min((uint32_t)kInt8RawStages, ((uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - kInt8Slots * tile * 64) / s.raw_bytes);
+      min((uint32_t)kInt8RawStages, ((uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - int8_slots(tile) * int8_halves(tile) * tile * 64) / s.raw_bytes);
   return s;
 }
-static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - kInt8Slots * kInt8MostRows * 64) / ((256 + kInt8MostRows) * 64) >= 4,
-              "four stages at least");
+static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - int8_slots(kInt8MostRows) * int8_halves(kInt8MostRows) * kInt8MostRows * 64) /
+                      ((256 + kInt8MostRows) * 64) >= 4, "four stages at least");
 
 // 32 neighbouring columns (rows c0 .. of the tile) of the accumulator by 32 weight rows (a lane each): scaled,
-// through the epilogue, turned around and stored. xs: the lane's row scale (of row c0 + lane).
+// through the epilogue, turned around and stored. xs: where the rows' scales lie.
 template <int YT, bool SWIGLU>
-__device__ __forceinline__ void int8_store(const Int8ProductParams& p, uint32_t turn, const uint32_t (&v)[32], float wscale, float xs,
-                                           int row0, int rows, int col) {
+__device__ __forceinline__ void int8_store(const Int8ProductParams& p, uint32_t turn, const uint32_t (&v)[32], float wscale,
+                                           uint32_t xs, int row0, int rows, int col) {
   const int lane = threadIdx.x & 31;
+  // 16 columns at a time, their scales loaded first and their results stored last: in between nothing orders the
+  // columns, whose chains of some 200 clocks overlap
 #pragma unroll
-  for (int c = 0; c < 32; c += 2) {
-    const float z0 = __uint_as_float(v[c]) * __shfl_sync(0xffffffffu, xs, c) * wscale;
-    const float z1 = __uint_as_float(v[c + 1]) * __shfl_sync(0xffffffffu, xs, c + 1) * wscale;
+  for (int c0 = 0; c0 < 32; c0 += 16) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int4 w = lds_v4(xs + (c0 + 4 * i) * 4);
+      x[4 * i] = __int_as_float(w.x), x[4 * i + 1] = __int_as_float(w.y);
+      x[4 * i + 2] = __int_as_float(w.z), x[4 * i + 3] = __int_as_float(w.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[c0 + i]) * x[i] * wscale;
     if (SWIGLU) {
-      // gates lie in the even lanes, what they gate in the odd ones: the even lane takes row c, the odd one row c + 1
-      const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? z0 : z1, 1);
-      const float h = lane & 1 ? int8_swiglu(got, z1) : int8_swiglu(z0, got);
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (c + (lane & 1)) * kInt8TurnRow + (lane >> 1) * 2), "h"(int8_round<YT>(h))
-                   : "memory");
+      // gates lie in the even lanes, what they gate in the odd ones: of two columns the even lane takes the first, the
+      // odd one the second
+      uint16_t h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[2 * i] : x[2 * i + 1], 1);
+        h[i] = int8_round<YT>(int8_swiglu(lane & 1 ? got : x[2 * i], lane & 1 ? x[2 * i + 1] : got));
+      }
+      const uint32_t to = turn + (c0 + (lane & 1)) * kInt8TurnRow + (lane >> 1) * 2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2 * i * kInt8TurnRow), "h"(h[i]) : "memory");
     } else {
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + c * kInt8TurnRow + lane * 2), "h"(int8_round<YT>(z0)) : "memory");
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (c + 1) * kInt8TurnRow + lane * 2), "h"(int8_round<YT>(z1)) : "memory");
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + (c0 + i) * kInt8TurnRow + lane * 2), "h"(int8_round<YT>(x[i])) : "memory");
     }
   }
   __syncwarp();
@@ -312,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   const uint32_t rank = cluster_rank();
   uint8_t* sm = psm_raw + ((1024u - (smem_u32(psm_raw) & 1023u)) & 1023u);
   uint8_t* turn = sm + kInt8ProductSmem - 1024 - int8_fixed_smem(p.E);
-  int* pre = reinterpret_cast<int*>(turn + 4 * kInt8TurnWarp);
+  int* pre = reinterpret_cast<int*>(turn + 4 * (kInt8TurnWarp + kInt8MostRows * 4));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kInt8RawStages; ++i) {
@@ -354,16 +391,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
   const int half = width >> 1;  // this CTA's weight rows of a unit
   const uint32_t raw_stages = __shfl_sync(0xffffffffu, shape.raw_stages, 0), raw_bytes = __shfl_sync(0xffffffffu, shape.raw_bytes, 0);
-  const uint32_t slot_bytes = tile * 64;
+  const int halves = int8_halves(tile);
+  const uint32_t panel = tile * 64, slot_bytes = panel * halves, slot_cols = 32 * halves, slots = int8_slots(tile);
   const int units = m_tiles * n_tiles;
   // shared memory: the widened rows, then the copies' ring; tensor memory: two accumulators, then the widened weights
-  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + kInt8Slots * slot_bytes, tmem_a = tmem + 2 * tile;
+  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + slots * slot_bytes, tmem_a = tmem + 2 * tile;
   const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty);
   const uint32_t wide_full0 = smem_u32(wide_full), wide_empty0 = smem_u32(wide_empty);
   const Int8Wait ab{&s_abort, p.status, p.timeout_ns};
 
   if (warp == 0) {
-    const int w_boxes = half >> 6;
+    const CUtensorMap* w_map = &maps.w[(half >> 6) - 1];
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
     bool ok = true;
@@ -372,18 +410,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       const int x_boxes = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32;  // of 16 rows, in each CTA
       const int e = __shfl_sync(0xffffffffu, un.e, 0), n0 = at.ni * width + (int)rank * half;
       const int row = __shfl_sync(0xffffffffu, un.row0, 0) + (int)rank * x_boxes * 16;
+      const CUtensorMap* x_map = &maps.x[x_boxes - 1];
       const uint32_t bytes = (uint32_t)(half + x_boxes * 16) * 128u;
       for (int kb = 0; kb < KB; ++kb) {
         ok = int8_wait(raw_empty0 + stage * 8, phase, ab);
         if (!ok) break;
         const uint32_t st = raw0 + stage * raw_bytes, bar = raw_full0 + stage * 8;
         mbar_expect_tx_if(leader, bar, bytes);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          tma_load_3d_if(leader && b < w_boxes, st + b * 8192, &maps.w, kb * kInt8Stage, n0 + b * 64, e, bar);
-#pragma unroll
-        for (int b = 0; b < kInt8MostRows / 32; ++b)
-          tma_load_2d_if(leader && b < x_boxes, st + half * 128 + b * 2048, &maps.x, kb * kInt8Stage, row + b * 16, bar);
+        tma_load_3d_if(leader, st, w_map, kb * kInt8Stage, n0, e, bar);
+        tma_load_2d_if(leader, st + half * 128, x_map, kb * kInt8Stage, row, bar);
         if (++stage == raw_stages) {
           stage = 0;
           phase ^= 1;
@@ -401,84 +436,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
         const int rows = __shfl_sync(0xffffffffu, un.rows, 0);
         const uint32_t idesc = idesc_f16_pair((rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
         ok = int8_wait(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
-        for (int kb = 0; kb < 2 * KB && ok; ++kb) {
+        const int parts = halves == 2 ? KB : 2 * KB;
+        for (int kb = 0; kb < parts && ok; ++kb) {
           ok = int8_wait(wide_full0 + slot * 8, phase, ab);
           if (!ok) break;
           tc_fence_after();
           const uint64_t bdesc = bdesc0 + slot * (slot_bytes >> 4);
-          const uint32_t a = tmem_a + slot * 32, here = slot;
-          if (++slot == kInt8Slots) {
+          const uint32_t a = tmem_a + slot * slot_cols, here = slot;
+          if (++slot == slots) {
             slot = 0;
             phase ^= 1;
           }
-          const int steps = (p.K - kb * (kInt8Stage / 2) + 15) / 16;
+          const int steps = (p.K - kb * (64 * halves) + 15) / 16;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_f16_pair_if(leader && kk < steps, acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
+          if (halves == 2) {
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              tc_mma_f16_pair_if(leader && kk < steps, acc, a + kk * 8, bdesc + (panel >> 4) + (kk - 4) * 2, idesc, true);
+          }
           tc_commit_pair_if(leader, wide_empty0 + here * 8);
-          tc_commit_pair_if(leader && kb + 1 == 2 * KB, smem_u32(&acc_full[buf]));
+          tc_commit_pair_if(leader && kb + 1 == parts, smem_u32(&acc_full[buf]));
         }
       }
       tc_commit_pair_if(leader, smem_u32(&drained));
     }
   } else if (warp < kWidenWarp + kWidenWarps) {
-    // the set's half of each stage: a thread has 32 elements of a weight row, a warp 16 rows x 32 elements of x at a time
+    // of half a stage a thread has 32 elements of a weight row, a warp 16 rows x 32 elements of x at a time
     const uint32_t mine = warp - kWidenWarp, set = mine >> 3, w = mine & 7, q = warp & 3, part = w >> 2;
     const uint32_t swz = lane & 7;  // a row's place in its group of 8, which the copies' and the MMA's swizzle go by
     const bool has_weights = (int)(q * 32) < half;
-    const uint32_t w_row = (q * 32 + lane) * 128, w0 = w_row + (((set * 4 + part * 2) ^ swz) << 4),
-                   w1 = w_row + (((set * 4 + part * 2 + 1) ^ swz) << 4);
+    const uint32_t first = halves == 2 ? 0 : set;  // the first half that is this set's
+    const uint32_t w_row = (q * 32 + lane) * 128, w0 = w_row + (((first * 4 + part * 2) ^ swz) << 4),
+                   w1 = w_row + (((first * 4 + part * 2 + 1) ^ swz) << 4);
     const uint32_t ta0 = tmem_a + ((q * 32) << 16) + part * 16;
     // x: block of 16 rows t >> 1, chunks (t & 1) * 2 and the next, of task t = w, w + 8, ..
     const uint32_t chunk = (w & 1) * 2 + (lane >> 4), x_row = (w >> 1) * 2048 + (lane & 15) * 128;
-    const uint32_t x_from = half * 128 + x_row + (((set * 4 + chunk) ^ swz) << 4);
+    const uint32_t x_from = half * 128 + x_row + (((first * 4 + chunk) ^ swz) << 4);
     const uint32_t x_to0 = sm0 + x_row + (((2 * chunk) ^ swz) << 4), x_to1 = sm0 + x_row + (((2 * chunk + 1) ^ swz) << 4);
     const uint32_t full0 = cluster_addr(wide_full0, 0);
-    uint32_t raw = 0, raw_phase = 0, slot = set, slot_phase = 1;
+    const uint32_t step = halves, begin = halves == 2 ? set : 0;  // stages
+    uint32_t raw = begin, raw_phase = 0, slot = set, slot_phase = 1;
     bool ok = true;
-    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
+    Int8Cursor at(n_tiles);
+    int kb = (int)begin;
+    for (; kb >= KB && at.u < units; kb -= KB) at.next();
+    while (at.u < units && ok) {
       const Int8Unit un = int8_unit(p, pre, at, width, tile);
       const int tasks = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32 * 2;
-      for (int kb = 0; kb < KB; ++kb) {
+      for (; kb < KB; kb += step) {
         ok = int8_wait(raw_full0 + raw * 8, raw_phase, ab) && int8_wait(wide_empty0 + slot * 8, slot_phase, ab);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t st = raw0 + raw * raw_bytes;
-        if (has_weights) {
-          const int4 a = lds_v4(st + w0), b = lds_v4(st + w1);
-          uint32_t v[16];
-          widen16(a, v);
-          widen16(b, v + 8);
-          tc_st16(ta0 + slot * 32, v);
-        }
-        const uint32_t off = slot * slot_bytes;
-        for (int t = w, g = 0; t < tasks; t += 8, g += 8192) {
-          uint32_t v[8];
-          widen16(lds_v4(st + x_from + g), v);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to0 + off + g), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                       : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to1 + off + g), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                       : "memory");
+        uint32_t st = raw0 + raw * raw_bytes, off = slot * slot_bytes, ta = ta0 + slot * slot_cols;
+        // the second half's chunks are 64 bytes away, up or down, in the swizzled rows
+#pragma unroll 1
+        for (uint32_t flip = 0; flip < 64u * step; flip += 64, ta += 32, off += panel) {
+          if (has_weights) {
+            const int4 a = lds_v4(st + (w0 ^ flip)), b = lds_v4(st + (w1 ^ flip));
+            uint32_t v[16];
+            widen16(a, v);
+            widen16(b, v + 8);
+            tc_st16(ta, v);
+          }
+          for (int t = w, g = 0; t < tasks; t += 8, g += 8192) {
+            uint32_t v[8];
+            widen16(lds_v4(st + (x_from ^ flip) + g), v);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to0 + off + g), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to1 + off + g), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                         : "memory");
+          }
         }
         tc_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_at(raw_empty0 + raw * 8);
+          mbar_arrive_at(raw_empty0 + raw * 8, step);  // 16 in all, of one set or of both
           mbar_arrive_cluster(full0 + slot * 8);
         }
-        if (++raw == raw_stages) {
-          raw = 0;
+        if ((raw += step) >= raw_stages) {
+          raw -= raw_stages;
           raw_phase ^= 1;
         }
-        slot ^= 2;
-        slot_phase ^= slot == set;
+        if ((slot += 2) >= slots) {
+          slot = set;
+          slot_phase ^= 1;
+        }
       }
+      if (!ok) break;
+      for (; kb >= KB && at.u < units; kb -= KB) at.next();
     }
   } else {
     const uint32_t q = warp & 3;
-    const uint32_t my_turn = smem_u32(turn) + q * kInt8TurnWarp;
+    const uint32_t my_turn = smem_u32(turn) + q * kInt8TurnWarp, my_xs = smem_u32(turn) + 4 * kInt8TurnWarp + q * kInt8MostRows * 4;
     const uint32_t empty0 = cluster_addr(smem_u32(acc_empty), 0);
     uint32_t done = 0;
     for (Int8Cursor at(n_tiles); at.u < units; at.next(), ++done) {
@@ -487,13 +540,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       const int n = un.n0 + (int)rank * half + 32 * (int)q;  // the warp's first weight row
       const int groups = 32 * (int)q < half && n < p.N ? (un.rows + 31) / 32 : 0;
       const float wscale = n + lane < p.N && groups ? p.ws[(size_t)un.e * p.N + n + lane] : 0.f;
+      for (int g = 0; g < groups; ++g) {
+        const int r = 32 * g + lane;
+        const float v = p.xs && r < un.rows ? p.xs[un.row0 + r] : 1.f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(my_xs + r * 4), "f"(v) : "memory");
+      }
+      __syncwarp();
       if (!int8_wait(smem_u32(&acc_full[buf]), (done >> 1) & 1, ab)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((32 * q) << 16) + buf * tile;
 #pragma unroll 1
       for (int g = 0; g < groups; ++g) {
         const int left = un.rows - 32 * g;
-        const float xs = p.xs && lane < left ? p.xs[un.row0 + 32 * g + lane] : 1.f;
         uint32_t v[32];
         tc_ld32(acc + 32 * g, v);
         tc_wait_ld();
@@ -503,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(empty0 + buf * 8);
         }
-        int8_store<YT, SWIGLU>(p, my_turn, v, wscale, xs, un.row0 + 32 * g, min(32, left), SWIGLU ? n / 2 : n);
+        int8_store<YT, SWIGLU>(p, my_turn, v, wscale, my_xs + g * 128, un.row0 + 32 * g, min(32, left), SWIGLU ? n / 2 : n);
       }
       if (groups == 0) {
         tc_fence_before();
@@ -681,9 +739,12 @@ extern "C" moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const i
   int per_sm = 0;
   if (k % 16 == 0) {
     Int8Maps maps;
-    if (!int8_map(&maps.x, x, (unsigned long long)k, (unsigned long long)W * A, 0, 16) ||
-        !int8_map(&maps.w, w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, 64))
-      return MOE_ERR_CUDA;
+    bool good = true;
+    for (unsigned i = 0; i < 6; ++i)
+      good = good && int8_map(&maps.x[i], x, (unsigned long long)k, (unsigned long long)W * A, 0, 16 * (i + 1));
+    for (unsigned i = 0; i < 2; ++i)
+      good = good && int8_map(&maps.w[i], w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, 64 * (i + 1));
+    if (!good) return MOE_ERR_CUDA;
     const Int8Kernel kernel = y_dtype == MOE_F16 ? (sw ? int8_product_kernel<MOE_F16, true> : int8_product_kernel<MOE_F16, false>)
                                                  : (sw ? int8_product_kernel<MOE_BF16, true> : int8_product_kernel<MOE_BF16, false>);
     if (resident_blocks((const void*)kernel, kInt8ProductThreads, kInt8ProductSmem, &per_sm) != cudaSuccess || per_sm < 1)
