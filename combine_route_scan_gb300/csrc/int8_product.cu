@@ -11,9 +11,8 @@
 //     bytes of shared-memory traffic for each; a row's element, written back as fp16 and
 //     read by the MMA, takes 6. Shared memory's 128 bytes a clock bound a unit of many rows: in one CTA
 //     128 x 192 took 235 bytes for each clock of the MMA, in a pair 139;
-//   * four bytes become two fp16 pairs by (w & 0x00ff00ff) ^ 0x64806480 = 1152 + value, less
-//     1152: bytes 0 and 2, and shifted by 8 bytes 1 and 3. The order of K that this gives is
-//     the same for both operands;
+//   * four bytes become two fp16 pairs, bytes 0 and 2 and bytes 1 and 3 (widen4). The order of K
+//     that this gives is the same for both operands;
 //   * copies bring 128 elements of K a stage; two sets of eight warps widen them in turn, a stage
 //     each, into four or six slots of TMEM and shared memory. Two accumulators of more than
 //     128 columns leave TMEM for two such slots: then a slot is half a stage, and each
@@ -172,6 +171,9 @@ static __device__ __noinline__ bool int8_wait_long(uint32_t bar, uint32_t parity
     }
   }
 }
+__device__ __forceinline__ bool int8_wait_one(uint32_t bar, uint32_t parity, const Int8Wait& a) {
+  return int8_sleep(bar, parity) || int8_wait_long(bar, parity, a.flag, a.status, a.limit);
+}
 // All lanes of a warp ask, with one answer for all: nothing of it diverges when the phase is there. (One lane asking for
 // the others cost 330 clocks for a phase that was there.)
 __device__ __forceinline__ bool int8_wait(uint32_t bar, uint32_t parity, const Int8Wait& a) {
@@ -188,10 +190,11 @@ __device__ __forceinline__ int4 lds_v4(uint32_t at) {
   return v;
 }
 
-// Four int8 as two fp16 pairs, elements (0, 2) and (1, 3), exactly.
+// Four int8 as two fp16 pairs, elements (0, 2) and (1, 3), exactly: 128 added to each, the bytes taken for the mantissas
+// of 1024 + .., and 1152 subtracted. (By masks and a shift instead of byte permutes it took half as long again.)
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& even, uint32_t& odd) {
-  const uint32_t bias = 0x64806480u;  // 1024 + (value + 128) in fp16
-  const uint32_t a = (w & 0x00ff00ffu) ^ bias, b = ((w >> 8) & 0x00ff00ffu) ^ bias;
+  const uint32_t biased = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(biased, 0x64646464u, 0x4240), b = __byte_perm(biased, 0x64646464u, 0x4341);
   const __half2 less = __half2half2(__ushort_as_half(0xe480));  // -1152
   const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&a), less), y = __hadd2(*reinterpret_cast<const __half2*>(&b), less);
   even = *reinterpret_cast<const uint32_t*>(&x);
@@ -229,6 +232,14 @@ struct Int8Cursor {
   }
 };
 
+// Its expert and rows, for a thread by itself and for a whole warp.
+__device__ __forceinline__ Int8Unit int8_unit_one(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int width,
+                                                  int tile) {
+  const int e = int8_expert_of(pre, p.E, at.mt);
+  const int* first = pre + p.E + 1;
+  const int before = (at.mt - pre[e]) * tile;
+  return {e, at.ni * width, min(tile, first[p.E + e] - before), first[e] + before};
+}
 __device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int width, int tile) {
   // found by a whole warp: among every (E/32)th expert, then among those between
   const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
@@ -400,45 +411,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   const uint32_t wide_full0 = smem_u32(wide_full), wide_empty0 = smem_u32(wide_empty);
   const Int8Wait ab{&s_abort, p.status, p.timeout_ns};
 
+  // The copies and the MMAs are one thread's each. (With a whole warp going along, the MMA predicated for one lane,
+  // each MMA took 60 clocks to issue: 32 is its time with 64 rows.)
   if (warp == 0) {
-    const CUtensorMap* w_map = &maps.w[(half >> 6) - 1];
-    const bool leader = elect_one();
-    uint32_t stage = 0, phase = 1;
-    bool ok = true;
-    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
-      const Int8Unit un = int8_unit(p, pre, at, width, tile);
-      const int x_boxes = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32;  // of 16 rows, in each CTA
-      const int e = __shfl_sync(0xffffffffu, un.e, 0), n0 = at.ni * width + (int)rank * half;
-      const int row = __shfl_sync(0xffffffffu, un.row0, 0) + (int)rank * x_boxes * 16;
-      const CUtensorMap* x_map = &maps.x[x_boxes - 1];
-      const uint32_t bytes = (uint32_t)(half + x_boxes * 16) * 128u;
-      for (int kb = 0; kb < KB; ++kb) {
-        ok = int8_wait(raw_empty0 + stage * 8, phase, ab);
-        if (!ok) break;
-        const uint32_t st = raw0 + stage * raw_bytes, bar = raw_full0 + stage * 8;
-        mbar_expect_tx_if(leader, bar, bytes);
-        tma_load_3d_if(leader, st, w_map, kb * kInt8Stage, n0, e, bar);
-        tma_load_2d_if(leader, st + half * 128, x_map, kb * kInt8Stage, row, bar);
-        if (++stage == raw_stages) {
-          stage = 0;
-          phase ^= 1;
+    if (elect_one()) {
+      const CUtensorMap* w_map = &maps.w[(half >> 6) - 1];
+      uint32_t stage = 0, phase = 1;
+      bool ok = true;
+      for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
+        const Int8Unit un = int8_unit_one(p, pre, at, width, tile);
+        const int x_boxes = (un.rows + 31) / 32;  // of 16 rows, in each CTA
+        const int n0 = un.n0 + (int)rank * half, row = un.row0 + (int)rank * x_boxes * 16;
+        const CUtensorMap* x_map = &maps.x[x_boxes - 1];
+        const uint32_t bytes = (uint32_t)(half + x_boxes * 16) * 128u;
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = int8_wait_one(raw_empty0 + stage * 8, phase, ab);
+          if (!ok) break;
+          const uint32_t st = raw0 + stage * raw_bytes, bar = raw_full0 + stage * 8;
+          mbar_expect_tx_if(true, bar, bytes);
+          tma_load_3d_if(true, st, w_map, kb * kInt8Stage, n0, un.e, bar);
+          tma_load_2d_if(true, st + half * 128, x_map, kb * kInt8Stage, row, bar);
+          if (++stage == raw_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && elect_one()) {
       const uint64_t bdesc0 = sw128_desc(sm);
-      const bool leader = elect_one();
       uint32_t slot = 0, phase = 0, done = 0;
       bool ok = true;
       for (Int8Cursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
-        const Int8Unit un = int8_unit(p, pre, at, width, tile);
-        const int rows = __shfl_sync(0xffffffffu, un.rows, 0);
-        const uint32_t idesc = idesc_f16_pair((rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
-        ok = int8_wait(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
+        const Int8Unit un = int8_unit_one(p, pre, at, width, tile);
+        const uint32_t idesc = idesc_f16_pair((un.rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
+        ok = int8_wait_one(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
         const int parts = halves == 2 ? KB : 2 * KB;
         for (int kb = 0; kb < parts && ok; ++kb) {
-          ok = int8_wait(wide_full0 + slot * 8, phase, ab);
+          ok = int8_wait_one(wide_full0 + slot * 8, phase, ab);
           if (!ok) break;
           tc_fence_after();
           const uint64_t bdesc = bdesc0 + slot * (slot_bytes >> 4);
@@ -447,21 +458,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
             slot = 0;
             phase ^= 1;
           }
-          const int steps = (p.K - kb * (64 * halves) + 15) / 16;
+          const int left = p.K - kb * (64 * halves);
+          if (left >= 64 * halves) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16_pair_if(leader && kk < steps, acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
-          if (halves == 2) {
+            for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
+            if (halves == 2) {
 #pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              tc_mma_f16_pair_if(leader && kk < steps, acc, a + kk * 8, bdesc + (panel >> 4) + (kk - 4) * 2, idesc, true);
+              for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + 32 + kk * 8, bdesc + (panel >> 4) + kk * 2, idesc, true);
+            }
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk * 16 < left; ++kk)
+              tc_mma_f16_pair(acc, a + kk * 8, bdesc + (kk >> 2) * (panel >> 4) + (kk & 3) * 2, idesc, kk > 0 || kb > 0);
           }
-          tc_commit_pair_if(leader, wide_empty0 + here * 8);
-          tc_commit_pair_if(leader && kb + 1 == parts, smem_u32(&acc_full[buf]));
+          tc_commit_pair(wide_empty0 + here * 8);
+          if (kb + 1 == parts) tc_commit_pair(smem_u32(&acc_full[buf]));
         }
       }
-      tc_commit_pair_if(leader, smem_u32(&drained));
+      tc_commit_pair(smem_u32(&drained));
     }
+    __syncwarp();
   } else if (warp < kWidenWarp + kWidenWarps) {
     // of half a stage a thread has 32 elements of a weight row, a warp 16 rows x 32 elements of x at a time
     const uint32_t mine = warp - kWidenWarp, set = mine >> 3, w = mine & 7, q = warp & 3, part = w >> 2;

@@ -105,26 +105,21 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Where `go` holds, D[tmem] (+)= A[tmem] * B[smem desc]^T, K = 16, fp16 inputs, fp32 accumulator. A
-// has row i in lane i, two neighbouring elements of K a column.
-__device__ __forceinline__ void tc_mma_f16_pair_if(bool go, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                   bool accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, K = 16, fp16 inputs, fp32 accumulator. A has row i in lane i, two
+// neighbouring elements of K a column.
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)go)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
 // Arrive on `bar` of both CTAs once the pair's tcgen05 operations issued so far by this thread are done.
-__device__ __forceinline__ void tc_commit_pair_if(bool go, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %0, 0;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], %2;\n\t}" ::"r"((uint32_t)go),
-      "r"(bar), "h"((uint16_t)3)
-      : "memory");
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"((uint16_t)3)
+               : "memory");
 }
 
 // Instruction descriptor: fp16 A and B, fp32 D, both K-major, M = 256, N = n.
