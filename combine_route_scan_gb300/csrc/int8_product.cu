@@ -13,10 +13,10 @@
 //     128 x 192 took 235 bytes for each clock of the MMA, in a pair 139;
 //   * four bytes become two fp16 pairs, bytes 0 and 2 and bytes 1 and 3 (widen4). The order of K
 //     that this gives is the same for both operands;
-//   * copies bring 128 elements of K a stage; two sets of eight warps widen them in turn, a stage
+//   * copies bring 128 elements of K a stage; four sets of four warps widen them in turn, a stage
 //     each, into four or six slots of TMEM and shared memory. Two accumulators of more than
-//     128 columns leave TMEM for two such slots: then a slot is half a stage, and each
-//     set has its half of every stage;
+//     128 columns leave TMEM for two such slots: then a slot is half a stage, and so is a
+//     set's turn;
 //   * warps: 0 TMA, 1 MMA (of the pair's first CTA), 2..17 widen, 18..21 epilogue. Two accumulators, so
 //     that the next unit's MMAs run while this one is read.
 #include <cuda.h>
@@ -117,7 +117,7 @@ struct Int8Maps {
   CUtensorMap x[6], w[2];
 };
 
-constexpr int kWidenWarp = 2, kWidenWarps = 16;
+constexpr int kWidenWarp = 2, kSets = 4, kSetWarps = 4;
 constexpr int kInt8ProductThreads = 22 * 32;
 constexpr int kInt8Stage = 128;    // elements of K a stage
 constexpr int kInt8MostRows = 192; // MMA N
@@ -179,6 +179,13 @@ __device__ __forceinline__ bool int8_wait_one(uint32_t bar, uint32_t parity, con
 __device__ __forceinline__ bool int8_wait(uint32_t bar, uint32_t parity, const Int8Wait& a) {
   if (__all_sync(0xffffffffu, int8_sleep(bar, parity))) return true;
   return __all_sync(0xffffffffu, int8_wait_long(bar, parity, a.flag, a.status, a.limit));
+}
+
+// Two barriers' phases at once.
+__device__ __forceinline__ bool int8_wait2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, const Int8Wait& a) {
+  const bool one = int8_sleep(bar0, parity0), two = int8_sleep(bar1, parity1);
+  if (__all_sync(0xffffffffu, one && two)) return true;
+  return int8_wait(bar0, parity0, a) && int8_wait(bar1, parity1, a);
 }
 
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t count) {
@@ -365,10 +372,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kInt8RawStages; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], kWidenWarps);
+      mbar_init(&raw_empty[i], 2 * kSetWarps);  // two sets once, or one twice
     }
     for (int i = 0; i < kInt8Slots; ++i) {
-      mbar_init(&wide_full[i], kWidenWarps);  // a set's eight warps in each CTA
+      mbar_init(&wide_full[i], 2 * kSetWarps);  // a set's warps in each CTA
       mbar_init(&wide_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -478,21 +485,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       tc_commit_pair(smem_u32(&drained));
     }
     __syncwarp();
-  } else if (warp < kWidenWarp + kWidenWarps) {
-    // of half a stage a thread has 32 elements of a weight row, a warp 16 rows x 32 elements of x at a time
-    const uint32_t mine = warp - kWidenWarp, set = mine >> 3, w = mine & 7, q = warp & 3, part = w >> 2;
+  } else if (warp < kWidenWarp + kSets * kSetWarps) {
+    // of half a stage a thread has the 64 elements of a weight row, a warp 16 rows x 32 elements of x at a time
+    const uint32_t mine = warp - kWidenWarp, set = mine / kSetWarps, w = mine % kSetWarps, q = warp & 3;
     const uint32_t swz = lane & 7;  // a row's place in its group of 8, which the copies' and the MMA's swizzle go by
     const bool has_weights = (int)(q * 32) < half;
-    const uint32_t first = halves == 2 ? 0 : set;  // the first half that is this set's
-    const uint32_t w_row = (q * 32 + lane) * 128, w0 = w_row + (((first * 4 + part * 2) ^ swz) << 4),
-                   w1 = w_row + (((first * 4 + part * 2 + 1) ^ swz) << 4);
-    const uint32_t ta0 = tmem_a + ((q * 32) << 16) + part * 16;
-    // x: block of 16 rows t >> 1, chunks (t & 1) * 2 and the next, of task t = w, w + 8, ..
+    const uint32_t first = halves == 2 ? 0 : set & 1;  // the first half that is this set's
+    const uint32_t w_row = (q * 32 + lane) * 128 + ((first * 4 ^ swz) << 4);  // chunk c is 16 c away by exclusive or
+    const uint32_t ta0 = tmem_a + ((q * 32) << 16);
+    // x: block of 16 rows t >> 1, chunks (t & 1) * 2 and the next, of task t = w, w + 4, ..
     const uint32_t chunk = (w & 1) * 2 + (lane >> 4), x_row = (w >> 1) * 2048 + (lane & 15) * 128;
     const uint32_t x_from = half * 128 + x_row + (((first * 4 + chunk) ^ swz) << 4);
     const uint32_t x_to0 = sm0 + x_row + (((2 * chunk) ^ swz) << 4), x_to1 = sm0 + x_row + (((2 * chunk + 1) ^ swz) << 4);
     const uint32_t full0 = cluster_addr(wide_full0, 0);
-    const uint32_t step = halves, begin = halves == 2 ? set : 0;  // stages
+    const uint32_t step = 2 * halves, begin = halves == 2 ? set : set >> 1;  // stages
     uint32_t raw = begin, raw_phase = 0, slot = set, slot_phase = 1;
     bool ok = true;
     Int8Cursor at(n_tiles);
@@ -502,21 +508,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       const Int8Unit un = int8_unit(p, pre, at, width, tile);
       const int tasks = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32 * 2;
       for (; kb < KB; kb += step) {
-        ok = int8_wait(raw_full0 + raw * 8, raw_phase, ab) && int8_wait(wide_empty0 + slot * 8, slot_phase, ab);
+        ok = int8_wait2(raw_full0 + raw * 8, raw_phase, wide_empty0 + slot * 8, slot_phase, ab);
         if (!ok) break;
         tc_fence_after();
-        uint32_t st = raw0 + raw * raw_bytes, off = slot * slot_bytes, ta = ta0 + slot * slot_cols;
+        const uint32_t st = raw0 + raw * raw_bytes;
+        uint32_t off = slot * slot_bytes, ta = ta0 + slot * slot_cols;
         // the second half's chunks are 64 bytes away, up or down, in the swizzled rows
 #pragma unroll 1
-        for (uint32_t flip = 0; flip < 64u * step; flip += 64, ta += 32, off += panel) {
+        for (uint32_t flip = 0; flip < 64u * halves; flip += 64, ta += 32, off += panel) {
           if (has_weights) {
-            const int4 a = lds_v4(st + (w0 ^ flip)), b = lds_v4(st + (w1 ^ flip));
+            const uint32_t from = st + (w_row ^ flip);
+            const int4 c0 = lds_v4(from), c1 = lds_v4(from ^ 16), c2 = lds_v4(from ^ 32), c3 = lds_v4(from ^ 48);
             uint32_t v[16];
-            widen16(a, v);
-            widen16(b, v + 8);
+            widen16(c0, v);
+            widen16(c1, v + 8);
             tc_st16(ta, v);
+            widen16(c2, v);
+            widen16(c3, v + 8);
+            tc_st16(ta + 16, v);
           }
-          for (int t = w, g = 0; t < tasks; t += 8, g += 8192) {
+          for (int t = w, g = 0; t < tasks; t += kSetWarps, g += kSetWarps * 1024) {
             uint32_t v[8];
             widen16(lds_v4(st + (x_from ^ flip) + g), v);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to0 + off + g), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -530,15 +541,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_at(raw_empty0 + raw * 8, step);  // 16 in all, of one set or of both
+          mbar_arrive_at(raw_empty0 + raw * 8, halves);
           mbar_arrive_cluster(full0 + slot * 8);
         }
         if ((raw += step) >= raw_stages) {
           raw -= raw_stages;
           raw_phase ^= 1;
         }
-        if ((slot += 2) >= slots) {
-          slot = set;
+        if ((slot += kSets) >= slots) {
+          slot -= slots;
           slot_phase ^= 1;
         }
       }
