@@ -239,14 +239,7 @@ struct Int8Cursor {
   }
 };
 
-// Its expert and rows, for a thread by itself and for a whole warp.
-__device__ __forceinline__ Int8Unit int8_unit_one(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int width,
-                                                  int tile) {
-  const int e = int8_expert_of(pre, p.E, at.mt);
-  const int* first = pre + p.E + 1;
-  const int before = (at.mt - pre[e]) * tile;
-  return {e, at.ni * width, min(tile, first[p.E + e] - before), first[e] + before};
-}
+// Its expert and rows.
 __device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int width, int tile) {
   // found by a whole warp: among every (E/32)th expert, then among those between
   const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
@@ -386,7 +379,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     mbar_fence_init();
     s_abort = 0;
   }
-  cluster_sync();  // the other CTA's barriers are there before anything arrives on them
+  __syncwarp();
+  cluster_arrive();
   if (warp == 1) {
     tmem_alloc_pair(&tmem_slot, 512);
     tmem_relinquish_pair();
@@ -417,16 +411,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty);
   const uint32_t wide_full0 = smem_u32(wide_full), wide_empty0 = smem_u32(wide_empty);
   const Int8Wait ab{&s_abort, p.status, p.timeout_ns};
+  cluster_wait();  // the other CTA's barriers are there before anything arrives on them
 
-  // The copies and the MMAs are one thread's each. (With a whole warp going along, the MMA predicated for one lane,
-  // each MMA took 60 clocks to issue: 32 is its time with 64 rows.)
+  // A unit's copies and its MMAs are one thread's each. (With a whole warp going along, the MMA predicated for one
+  // lane, each MMA took 60 clocks to issue: 32 is its time with 64 rows.)
   if (warp == 0) {
-    if (elect_one()) {
-      const CUtensorMap* w_map = &maps.w[(half >> 6) - 1];
-      uint32_t stage = 0, phase = 1;
-      bool ok = true;
-      for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
-        const Int8Unit un = int8_unit_one(p, pre, at, width, tile);
+    const CUtensorMap* w_map = &maps.w[(half >> 6) - 1];
+    const bool leader = elect_one();
+    uint32_t stage = 0, phase = 1;
+    bool ok = true;
+    for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
+      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      if (leader) {
         const int x_boxes = (un.rows + 31) / 32;  // of 16 rows, in each CTA
         const int n0 = un.n0 + (int)rank * half, row = un.row0 + (int)rank * x_boxes * 16;
         const CUtensorMap* x_map = &maps.x[x_boxes - 1];
@@ -444,47 +440,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
           }
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
     }
   } else if (warp == 1) {
-    if (rank == 0 && elect_one()) {
+    if (rank == 0) {
       const uint64_t bdesc0 = sw128_desc(sm);
+      const bool leader = elect_one();
       uint32_t slot = 0, phase = 0, done = 0;
       bool ok = true;
       for (Int8Cursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
-        const Int8Unit un = int8_unit_one(p, pre, at, width, tile);
-        const uint32_t idesc = idesc_f16_pair((un.rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
-        ok = int8_wait_one(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
-        const int parts = halves == 2 ? KB : 2 * KB;
-        for (int kb = 0; kb < parts && ok; ++kb) {
-          ok = int8_wait_one(wide_full0 + slot * 8, phase, ab);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t bdesc = bdesc0 + slot * (slot_bytes >> 4);
-          const uint32_t a = tmem_a + slot * slot_cols, here = slot;
-          if (++slot == slots) {
-            slot = 0;
-            phase ^= 1;
-          }
-          const int left = p.K - kb * (64 * halves);
-          if (left >= 64 * halves) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
-            if (halves == 2) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + 32 + kk * 8, bdesc + (panel >> 4) + kk * 2, idesc, true);
+        const Int8Unit un = int8_unit(p, pre, at, width, tile);
+        if (leader) {
+          const uint32_t idesc = idesc_f16_pair((un.rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
+          ok = int8_wait_one(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
+          const int parts = halves == 2 ? KB : 2 * KB;
+          for (int kb = 0; kb < parts && ok; ++kb) {
+            ok = int8_wait_one(wide_full0 + slot * 8, phase, ab);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bdesc = bdesc0 + slot * (slot_bytes >> 4);
+            const uint32_t a = tmem_a + slot * slot_cols, here = slot;
+            if (++slot == slots) {
+              slot = 0;
+              phase ^= 1;
             }
-          } else {
+            const int left = p.K - kb * (64 * halves);
+            if (left >= 64 * halves) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
+              if (halves == 2) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + 32 + kk * 8, bdesc + (panel >> 4) + kk * 2, idesc, true);
+              }
+            } else {
 #pragma unroll 1
-            for (int kk = 0; kk * 16 < left; ++kk)
-              tc_mma_f16_pair(acc, a + kk * 8, bdesc + (kk >> 2) * (panel >> 4) + (kk & 3) * 2, idesc, kk > 0 || kb > 0);
+              for (int kk = 0; kk * 16 < left; ++kk)
+                tc_mma_f16_pair(acc, a + kk * 8, bdesc + (kk >> 2) * (panel >> 4) + (kk & 3) * 2, idesc, kk > 0 || kb > 0);
+            }
+            tc_commit_pair(wide_empty0 + here * 8);
+            if (kb + 1 == parts) tc_commit_pair(smem_u32(&acc_full[buf]));
           }
-          tc_commit_pair(wide_empty0 + here * 8);
-          if (kb + 1 == parts) tc_commit_pair(smem_u32(&acc_full[buf]));
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
-      tc_commit_pair(smem_u32(&drained));
+      if (leader) tc_commit_pair(smem_u32(&drained));
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp < kWidenWarp + kSets * kSetWarps) {
     // of half a stage a thread has the 64 elements of a weight row, a warp 16 rows x 32 elements of x at a time
     const uint32_t mine = warp - kWidenWarp, set = mine / kSetWarps, w = mine % kSetWarps, q = warp & 3;
@@ -601,10 +602,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   __syncthreads();
   if (threadIdx.x == 0) {
     // the pair's MMAs, and after an abort the copies in flight, end before their memory is given back
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(&drained, 0) && globaltimer_ns() - t0 < 1000000ull) {}
-    if (s_abort)
-      while (globaltimer_ns() - t0 < 1000000ull) {}
+    if (!mbar_try_wait(&drained, 0) || s_abort) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&drained, 0) && globaltimer_ns() - t0 < 1000000ull) {}
+      if (s_abort)
+        while (globaltimer_ns() - t0 < 1000000ull) {}
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -613,7 +616,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
-  cluster_sync();
 }
 
 // ------------------------------------------------------------- any k and alignment
