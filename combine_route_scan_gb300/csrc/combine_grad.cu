@@ -19,7 +19,7 @@ constexpr int kGradThreads = 256; // at most
 
 // VEC: rows of 16-byte vectors; else an element at a time.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kGradThreads, 3) combine_grad_kernel(CombineGradParams p) {
+__global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGradParams p) {
   __shared__ const uint8_t* s_src[32];
   __shared__ uint8_t* s_dst[32];
   __shared__ float s_w[32];

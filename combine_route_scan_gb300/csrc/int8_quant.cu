@@ -4,11 +4,14 @@
 //
 // One pass over the data, bound by HBM: a row stays in registers between its maximum
 // and its codes, in a warp's where it has up to 2048 elements, in a block's up to
-// 16384. Rows that 16-byte loads do not fit, and longer ones, are read twice, an
+// 16384; as the codes of its elements are made, the next row's take their registers. Rows
+// that 16-byte loads do not fit, and longer ones, are read twice, an
 // element at a time, the second time from cache.
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "quant_common.cuh"
+
+#include <type_traits>
 
 namespace crs {
 
@@ -82,6 +85,27 @@ struct Int8Unit {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) v[i] = make_int4(0, 0, 0, 0);
   }
+  // The largest magnitude: of 16-bit elements pair by pair, in their own type.
+  __device__ float amax(float m) const {
+    if constexpr (DT == MOE_F32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m = fmax_abs3(m, __int_as_float(v[i].x), __int_as_float(v[i].y));
+        m = fmax_abs3(m, __int_as_float(v[i].z), __int_as_float(v[i].w));
+      }
+      return m;
+    } else {
+      using T = typename std::conditional<DT == MOE_F16, __half2, __nv_bfloat162>::type;
+      const T* h = reinterpret_cast<const T*>(v);
+      const T a = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+      return fmax_abs3(m, __low2float(a), __high2float(a));
+    }
+  }
+  // Keeps what was computed from the elements so far from being held in registers in their place.
+  __device__ void forget() {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) asm volatile("" : "+r"(v[i].x), "+r"(v[i].y), "+r"(v[i].z), "+r"(v[i].w));
+  }
   __device__ void pairs(f32x2 (&o)[4]) const {
     if constexpr (DT == MOE_F32) {
 #pragma unroll
@@ -110,10 +134,38 @@ __device__ __forceinline__ float int8_amax(float m, float (&s_max)[kInt8Threads 
   return m;
 }
 
+template <int DT>
+__device__ __forceinline__ float int8_load(const void* x, size_t i) {
+  if constexpr (DT == MOE_F32) return static_cast<const float*>(x)[i];
+  else return load_elem(x, i, DT);
+}
+
+// The codes of 8 elements, round(v / scale), from r = 1 / scale rounded to nearest: with y = v * r, which is within an
+// ulp of the quotient, y + r * (v - y * scale) is the quotient rounded to nearest (Markstein 1990, by fused
+// multiply-adds), as the division gives it; adding 1.5 * 2^23 leaves the integer in the low byte. For scales whose
+// residuals do not underflow (int8_rcp_ok); a quotient of smaller elements is 0 in any case. (dispatch's token_codes8
+// takes the division where a product is near a half, which of bf16 rows is every other eight: half the largest
+// magnitude, 63.5, is a frequent number.)
+__device__ __forceinline__ bool int8_rcp_ok(float scale) { return scale >= 7.8886091e-31f && scale <= 3.40282347e38f; }  // 2^-100
+__device__ __forceinline__ uint2 int8_codes(const f32x2 (&v)[4], f32x2 scale2, f32x2 rcp2) {
+  const f32x2 shift2 = f2_pack(kRoundShift, kRoundShift);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 y = f2_mul(v[i], rcp2);
+    const f32x2 t = f2_add(f2_fma(f2_fma(y, scale2, v[i]), rcp2, y), shift2);
+    float tl, th;
+    f2_split(t, tl, th);
+    c[2 * i] = __float_as_uint(tl);
+    c[2 * i + 1] = __float_as_uint(th);
+  }
+  return pack8_low(c);
+}
+
 // cols a multiple of 8 that a warp's (BLOCK: the block's) threads hold as NV units each,
 // rows of x 16-byte aligned, codes 8-byte aligned.
 template <int DT, int NV, bool BLOCK>
-__global__ void __launch_bounds__(kInt8Threads) int8_quantize_vec_kernel(Int8QuantParams p) {
+__global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 8 ? 2 : 4) int8_quantize_vec_kernel(Int8QuantParams p) {
   __shared__ int s_pre[kInt8CountedMats + 1];
   __shared__ float s_max[kInt8Threads / 32];
   pdl_wait();
@@ -124,48 +176,43 @@ __global__ void __launch_bounds__(kInt8Threads) int8_quantize_vec_kernel(Int8Qua
   Int8Rows rows(p, s_pre);
   const long long first = BLOCK ? blockIdx.x : blockIdx.x * (kInt8Threads / 32ll) + (threadIdx.x >> 5);
   const long long step = BLOCK ? gridDim.x : gridDim.x * (kInt8Threads / 32ll);
-  for (long long i = first; i < rows.total; i += step) {
-    size_t place;
-    const size_t from = rows.find(i, place);
-    Int8Unit<DT> u[NV];
+  if (first >= rows.total) return;
+  size_t place;
+  size_t from = rows.find(first, place);
+  Int8Unit<DT> u[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (t + j * kThreads < units) u[j].load(p.x, from + (size_t)(t + j * kThreads) * 8);
-      else u[j].zero();
-    }
+  for (int j = 0; j < NV; ++j) {
+    if (t + j * kThreads < units) u[j].load(p.x, from + (size_t)(t + j * kThreads) * 8);
+    else u[j].zero();
+  }
+  for (long long i = first; i < rows.total; i += step) {
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      f32x2 v[4];
-      u[j].pairs(v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float lo, hi;
-        f2_split(v[k], lo, hi);
-        m = fmax_abs3(m, lo, hi);
-      }
+      m = u[j].amax(m);
+      u[j].forget();
     }
     m = int8_amax<BLOCK>(m, s_max);
     const float scale = __fdiv_rn(m, 127.0f);
-    const bool fast = token_rcp_ok(scale);
-    const float rcp = fast ? __frcp_rn(scale) : 0.f;
-    const f32x2 rcp2 = f2_pack(rcp, rcp);
+    const float rcp = __frcp_rn(scale);
+    const f32x2 rcp2 = f2_pack(rcp, rcp), scale2 = f2_pack(-scale, -scale);
     int8_t* out = p.codes + place * p.cols;
+    if (t == 0) p.scales[place] = scale;
+    if (!int8_rcp_ok(scale)) {  // zeros, infinities, the smallest numbers: by the division, an element at a time
+#pragma unroll 1
+      for (int c = t; c < p.cols; c += kThreads) out[c] = (int8_t)(m == 0.f ? 0 : token_q(int8_load<DT>(p.x, from + c), scale));
+    }
+    const bool fast = int8_rcp_ok(scale), more = i + step < rows.total;
+    if (more) from = rows.find(i + step, place);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (t + j * kThreads >= units) break;
       f32x2 v[4];
       u[j].pairs(v);
-      *reinterpret_cast<uint2*>(out + (size_t)(t + j * kThreads) * 8) = token_codes8(v, scale, m, fast, rcp2);
+      if (more) u[j].load(p.x, from + (size_t)(t + j * kThreads) * 8);  // of the next row, under way while this one's codes are made
+      if (fast) *reinterpret_cast<uint2*>(out + (size_t)(t + j * kThreads) * 8) = int8_codes(v, scale2, rcp2);
     }
-    if (t == 0) p.scales[place] = scale;
   }
-}
-
-template <int DT>
-__device__ __forceinline__ float int8_load(const void* x, size_t i) {
-  if constexpr (DT == MOE_F32) return static_cast<const float*>(x)[i];
-  else return load_elem(x, i, DT);
 }
 
 // Any columns and alignment: a warp or (BLOCK) a block a row, read twice.
