@@ -17,8 +17,8 @@ namespace crs {
 constexpr int kGradBatch = 8;     // picks whose loads are in flight together
 constexpr int kGradThreads = 256; // at most
 
-// VEC: rows of 16-byte vectors; else an element at a time.
-template <int DT, bool VEC>
+// VEC: rows of 16-byte vectors; else an element at a time. SEARCH: without a row map (rows.cuh).
+template <int DT, bool VEC, bool SEARCH>
 __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGradParams p) {
   __shared__ const uint8_t* s_src[32];
   __shared__ uint8_t* s_dst[32];
@@ -44,18 +44,20 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
     uint8_t* dst = nullptr;
     float w = 0.f;
     bool has = false, copies = false;
+    const int cls = lane < sh.K ? classify_pick(p.ids, p.mask, sh, tau, lane) : kPickInactive;
+    if (SEARCH) r = find_rows(p, tau, cls);
     if (lane < sh.K) {
       const size_t pk = tau * sh.K + lane;
-      r = p.inv[pk];
+      if (!SEARCH) r = p.inv[pk];
       w = static_cast<const float*>(p.scales)[pk];
-      const int cls = classify_pick(p.ids, p.mask, sh, tau, lane);
       if (cls >= 0) {
         d = cls / sh.L;
         const long long row = r - (long long)d * sh.A;
         if (row >= 0 && row < sh.A && MOE_IN_BOUNDS(p.status, r, (long long)sh.W * sh.A)) {
           src = static_cast<const uint8_t*>(p.expert_out) + r * (long long)sh.row_in;
           if (p.grad_rows) dst = static_cast<uint8_t*>(p.grad_rows) + r * (long long)sh.row_in;
-          has = check = true;
+          has = true;
+          check = !SEARCH;
         } else {
           set_error(p.status, MOE_ERR_BAD_ASSIST);
         }
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = __fmul_rn(w, g[i]);
-            st_v4(dst + off, Vec<DT>::pack(o));
+            __stcs(reinterpret_cast<int4*>(dst + off), Vec<DT>::pack(o));
           }
           if (dots) {
             float f[8];
@@ -194,7 +196,8 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
   }
 }
 
-cudaError_t launch_combine_grad(const CombineGradParams& p, cudaStream_t st, int num_sms) {
+template <bool SEARCH>
+static cudaError_t launch_grad(const CombineGradParams& p, cudaStream_t st, int num_sms) {
   const Shape& sh = p.sh;
   const long long n_tok = (long long)sh.W * sh.bs;
   if (n_tok == 0) return cudaSuccess;
@@ -206,10 +209,14 @@ cudaError_t launch_combine_grad(const CombineGradParams& p, cudaStream_t st, int
   const int batches = (sh.K + kGradBatch - 1) / kGradBatch;
   PdlLaunch L(dim3((unsigned)n_tok, (unsigned)(n_tok < num_sms * 4LL ? batches : 1)), dim3(threads), 0, st);
   if (vec)
-    return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_F16, true>, p)
-                                 : cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_BF16, true>, p);
-  return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_F16, false>, p)
-                               : cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_BF16, false>, p);
+    return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_F16, true, SEARCH>, p)
+                                 : cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_BF16, true, SEARCH>, p);
+  return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_F16, false, SEARCH>, p)
+                               : cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_BF16, false, SEARCH>, p);
+}
+
+cudaError_t launch_combine_grad(const CombineGradParams& p, bool search, cudaStream_t st, int num_sms) {
+  return search ? launch_grad<true>(p, st, num_sms) : launch_grad<false>(p, st, num_sms);
 }
 
 }  // namespace crs

@@ -698,18 +698,22 @@ moe_status_t grad_params(const moe_config_t* cfg, const int32_t* assist_info, co
   return MOE_OK;
 }
 
-// The pick -> row map, as moe_combine takes it, then `launch`.
+// The pick -> row map, as moe_combine takes it, then `launch`; or, for batches whose time is the launches', `launch`
+// alone, looking for the rows.
+constexpr int kSearchBs = 256, kSearchPicks = 8192;
 template <class P, class F>
 moe_status_t run_grad(const moe_config_t* cfg, const P& p, void* ws, cudaStream_t s, F launch) {
   const int nsm = num_sms_of_current_device();
   if (nsm <= 0) return MOE_ERR_CUDA;
-  if (!map_owned_by(ws, p.assist, p.ep_recv_count, s)) {
+  const bool owned = map_owned_by(ws, p.assist, p.ep_recv_count, s);
+  const bool search = !owned && p.sh.bs <= kSearchBs && (long long)p.sh.W * p.sh.bs * p.sh.K <= kSearchPicks;
+  if (!owned && !search) {
     drop_map_owner(ws, s);
     if (launch_combine_inverse(p, s) != cudaSuccess) return MOE_ERR_CUDA;
     note_launches(1);
   }
   if (record(cfg->prof_events, 0, s) != MOE_OK) return MOE_ERR_CUDA;
-  if (launch(p, s, nsm) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch(p, search, s, nsm) != cudaSuccess) return MOE_ERR_CUDA;
   note_launches(1);
   return record(cfg->prof_events, 1, s);
 }

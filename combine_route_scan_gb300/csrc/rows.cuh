@@ -85,4 +85,56 @@ __device__ __forceinline__ int4 ld_v4(const void* p) {
   return v;
 }
 
+// The flat row of each lane's routed pick (class cls >= 0; lanes beyond the token's picks have another) without a
+// pick -> row map: the rows of a segment (expert, source rank) are at most bs, so that a warp looks through 32 of a pick's
+// at a time. -1 where no row names the pick, or counts are out of range. All lanes of a warp take part.
+__device__ __forceinline__ long long find_rows(const CombineParams& p, size_t tau, int cls) {
+  const Shape& sh = p.sh;
+  const int lane = threadIdx.x & 31, s = (int)(tau / sh.bs), t = (int)(tau % sh.bs), LW = sh.L * sh.W;
+  int lo = 0, hi = 0;
+  if (cls >= 0) {
+    const int32_t* ep = p.ep_recv_count + (size_t)(cls / sh.L) * LW;
+    const int seg = cls % sh.L * sh.W + s;
+    hi = ep[seg];
+    lo = seg ? ep[seg - 1] : 0;
+    if (lo < 0 || hi < lo || hi > sh.A || ep[LW - 1] > sh.A) lo = hi = 0;
+  }
+  const long long first = (long long)(cls >= 0 ? cls / sh.L : 0) * sh.A;
+  long long found = -1;
+  // the first 32 rows of all picks are asked for before any is looked at
+  constexpr int kAhead = 8;
+  for (int k0 = 0; k0 < sh.K; k0 += kAhead) {
+    int at[kAhead], ak[kAhead], as[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const long long base = __shfl_sync(0xffffffffu, first + lo, (k0 + j) & 31);
+      const int n = k0 + j < sh.K ? __shfl_sync(0xffffffffu, hi - lo, (k0 + j) & 31) : 0;
+      as[j] = -1;
+      if (lane < n) {
+        const int32_t* a = p.assist + (base + lane) * 3;
+        as[j] = a[0], at[j] = a[1], ak[j] = a[2];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j;
+      if (k >= sh.K) break;
+      const long long base = __shfl_sync(0xffffffffu, first + lo, k);
+      const int n = __shfl_sync(0xffffffffu, hi - lo, k);
+      uint32_t match = __ballot_sync(0xffffffffu, as[j] == s && at[j] == t && ak[j] == k);
+      int r = 0;
+      for (; !match && r + 32 < n; r += 32) {
+        bool here = false;
+        if (r + 32 + lane < n) {
+          const int32_t* a = p.assist + (base + r + 32 + lane) * 3;
+          here = a[0] == s && a[1] == t && a[2] == k;
+        }
+        match = __ballot_sync(0xffffffffu, here);
+      }
+      if (lane == k && match) found = base + r + __ffs(match) - 1;
+    }
+  }
+  return found;
+}
+
 }  // namespace crs
