@@ -74,22 +74,20 @@ struct ReduceTable {
   int n;
 };
 
-template <bool SEARCH, class P>
+template <class P>
 __device__ __forceinline__ void build_reduce_table(const P& p, size_t tau, ReduceTable& tab) {
   constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
   const Shape& sh = p.sh;
   const int lane = threadIdx.x & 31;
   const uint8_t* src = nullptr;
   uint32_t w = 0;
-  long long r = -1;
-  if (SEARCH) r = find_rows(p, tau, lane < sh.K ? classify_pick(p.ids, p.mask, sh, tau, lane) : kPickInactive);
   if (lane < sh.K) {
     const int c = classify_pick(p.ids, p.mask, sh, tau, lane);
     if (c == kPickBad) {
       set_error(p.status, MOE_ERR_BAD_EXPERT_ID);
     } else if (c >= 0) {
       const int s = (int)(tau / sh.bs), t = (int)(tau % sh.bs);
-      if (!SEARCH) r = p.inv[tau * sh.K + lane];
+      const long long r = p.inv[tau * sh.K + lane];
       const int LW = sh.L * sh.W;
       const int d = c / sh.L;
       const long long row = r - (long long)d * sh.A;
@@ -174,8 +172,7 @@ __device__ __forceinline__ void reduce_vector(const uint8_t* const* src, const u
 
 // At most 64 registers a thread: four CTAs (32 warps) per SM keep enough
 // loads in flight to cover HBM latency.
-// SEARCH (gradients): without a row map (rows.cuh).
-template <int DT, class P, bool SEARCH>
+template <int DT, class P>
 __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(P p, int chunks, int vpl) {
   constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
   MOE_PHASE_BEGIN(p, kPhaseReduce);
@@ -201,16 +198,11 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(P p, 
   uint32_t w = 0;
   long long r = -1;
   int d = -1;
-  int mine = kPickInactive;
-  if (SEARCH) {
-    if (lane < sh.K) mine = classify_pick(p.ids, p.mask, sh, tau, lane);
-    r = find_rows(p, tau, mine);
-  }
   if (lane < sh.K) {
     const size_t pk = tau * sh.K + lane;
-    if (!SEARCH) r = p.inv[pk];
+    r = p.inv[pk];
     w = kGrad ? __float_as_uint(1.f) : reinterpret_cast<const uint32_t*>(p.scales)[pk];
-    const int cls = SEARCH ? mine : classify_pick(p.ids, p.mask, sh, tau, lane);
+    const int cls = classify_pick(p.ids, p.mask, sh, tau, lane);
     if (cls >= 0) {
       d = cls / sh.L;
       const long long row = r - (long long)d * sh.A;
@@ -239,7 +231,7 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(P p, 
 
   // deferred consistency check of the row map (loads issued now, compared last)
   int a0 = 0, a1 = 0, a2 = 0, cnt = 0;
-  const bool check = !SEARCH && d >= 0 && src != nullptr && c == 0;
+  const bool check = d >= 0 && src != nullptr && c == 0;
   if (check) {
     const int32_t* a = p.assist + r * 3;
     a0 = a[0];
@@ -270,14 +262,14 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(P p, 
 }
 
 // Element-wise fallback for rows that are not 16-byte multiples.
-template <int DT, class P, bool SEARCH>
+template <int DT, class P>
 __global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(P p) {
   __shared__ ReduceTable tab;
   const Shape sh = p.sh;
   pdl_wait();
   pdl_launch_dependents();
   for (size_t tau = blockIdx.x; tau < (size_t)sh.W * sh.bs; tau += gridDim.x) {
-    if (threadIdx.x < 32) build_reduce_table<SEARCH>(p, tau, tab);
+    if (threadIdx.x < 32) build_reduce_table(p, tau, tab);
     __syncthreads();
     const int n = tab.n;
     for (int j = threadIdx.x; j < sh.h; j += kReduceThreads) {
@@ -307,7 +299,7 @@ cudaError_t launch_combine_inverse(const CombineParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&L.cfg, combine_inverse_kernel, p);
 }
 
-template <bool SEARCH, class P>
+template <class P>
 static cudaError_t launch_reduce(const P& p, cudaStream_t st, int num_sms) {
   constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
   const Shape& sh = p.sh;
@@ -317,10 +309,10 @@ static cudaError_t launch_reduce(const P& p, cudaStream_t st, int num_sms) {
     const int grid = (int)(n_tok < num_sms * 8LL ? n_tok : num_sms * 8LL);
     PdlLaunch L(dim3(grid), dim3(kReduceThreads), 0, st);
     if constexpr (!kGrad) {
-      if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_I32, P, false>, p);
+      if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_I32, P>, p);
     }
-    if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_F16, P, SEARCH>, p);
-    return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_BF16, P, SEARCH>, p);
+    if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_F16, P>, p);
+    return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_BF16, P>, p);
   }
   const int nvec = sh.row_in / 16;
   // smaller work items when the batch is too small to give every SM ~16 warps
@@ -332,17 +324,17 @@ static cudaError_t launch_reduce(const P& p, cudaStream_t st, int num_sms) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   PdlLaunch L(dim3((unsigned)grid), dim3(kReduceThreads), 0, st);
   if constexpr (!kGrad) {
-    if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_I32, P, false>, p, chunks, vpl);
+    if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_I32, P>, p, chunks, vpl);
   }
-  if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_F16, P, SEARCH>, p, chunks, vpl);
-  return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_BF16, P, SEARCH>, p, chunks, vpl);
+  if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_F16, P>, p, chunks, vpl);
+  return cudaLaunchKernelEx(&L.cfg, combine_reduce_kernel<MOE_BF16, P>, p, chunks, vpl);
 }
 
 cudaError_t launch_combine_reduce(const CombineParams& p, cudaStream_t st, int num_sms) {
-  return launch_reduce<false>(p, st, num_sms);
+  return launch_reduce(p, st, num_sms);
 }
-cudaError_t launch_dispatch_grad(const DispatchGradParams& p, bool search, cudaStream_t st, int num_sms) {
-  return search ? launch_reduce<true>(p, st, num_sms) : launch_reduce<false>(p, st, num_sms);
+cudaError_t launch_dispatch_grad_reduce(const DispatchGradParams& p, cudaStream_t st, int num_sms) {
+  return launch_reduce(p, st, num_sms);
 }
 
 }  // namespace crs

@@ -224,6 +224,7 @@ cudaError_t launch_combine_inverse(const CombineParams& p, cudaStream_t st);
 cudaError_t launch_combine_reduce(const CombineParams& p, cudaStream_t st, int num_sms);
 // The gradients; search: by looking for each pick's row, where the workspace has no row map of these buffers.
 cudaError_t launch_dispatch_grad(const DispatchGradParams& p, bool search, cudaStream_t st, int num_sms);
+cudaError_t launch_dispatch_grad_reduce(const DispatchGradParams& p, cudaStream_t st, int num_sms);
 cudaError_t launch_combine_grad(const CombineGradParams& p, bool search, cudaStream_t st, int num_sms);
 cudaError_t launch_combine_two_phase(const CombineParams& p, cudaStream_t st, int num_sms);
 cudaError_t launch_ffn(const FfnLaunch& f, cudaStream_t st, int num_sms, void* const* prof_events);

@@ -698,22 +698,20 @@ moe_status_t grad_params(const moe_config_t* cfg, const int32_t* assist_info, co
   return MOE_OK;
 }
 
-// The pick -> row map, as moe_combine takes it, then `launch`; or, for batches whose time is the launches', `launch`
-// alone, looking for the rows.
-constexpr int kSearchBs = 256, kSearchPicks = 8192;
+// `launch` with the pick -> row map of the dispatch that wrote these buffers, where the workspace has it; else looking
+// for the rows (search), or with a map rebuilt as moe_combine does.
 template <class P, class F>
-moe_status_t run_grad(const moe_config_t* cfg, const P& p, void* ws, cudaStream_t s, F launch) {
+moe_status_t run_grad(const moe_config_t* cfg, const P& p, bool search, void* ws, cudaStream_t s, F launch) {
   const int nsm = num_sms_of_current_device();
   if (nsm <= 0) return MOE_ERR_CUDA;
   const bool owned = map_owned_by(ws, p.assist, p.ep_recv_count, s);
-  const bool search = !owned && p.sh.bs <= kSearchBs && (long long)p.sh.W * p.sh.bs * p.sh.K <= kSearchPicks;
   if (!owned && !search) {
     drop_map_owner(ws, s);
     if (launch_combine_inverse(p, s) != cudaSuccess) return MOE_ERR_CUDA;
     note_launches(1);
   }
   if (record(cfg->prof_events, 0, s) != MOE_OK) return MOE_ERR_CUDA;
-  if (launch(p, search, s, nsm) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch(p, search && !owned, s, nsm) != cudaSuccess) return MOE_ERR_CUDA;
   note_launches(1);
   return record(cfg->prof_events, 1, s);
 }
@@ -745,7 +743,9 @@ moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out,
   p.grad_rows = grad_expert_out;
   p.grad_scales = grad_scales;
   p.grad_x = grad_x;
-  return run_grad(cfg, p, ws, static_cast<cudaStream_t>(stream), launch_combine_grad);
+  // Looking for the rows costs less than the map's launch at every size (with and without: 16 tokens of hidden 256 5.3 and
+  // 7.1 us, 512 of 2048 10.6 and 12.1, 4096 of 7168 158 and 161).
+  return run_grad(cfg, p, true, ws, static_cast<cudaStream_t>(stream), launch_combine_grad);
 }
 
 moe_status_t moe_dispatch_backward(const moe_config_t* cfg, const void* grad_expand_x, const int32_t* assist_info,
@@ -767,7 +767,12 @@ moe_status_t moe_dispatch_backward(const moe_config_t* cfg, const void* grad_exp
   p.residual = residual;
   p.row_weights = grad_expand_scales;
   p.pick_weights = grad_scales;
-  return run_grad(cfg, p, ws, static_cast<cudaStream_t>(stream), launch_dispatch_grad);
+  // A block a token that looks for its rows, or the map and the combine's reduce, whose warps need no barrier: the first
+  // for small batches and long rows (512 tokens of hidden 2048 6.4 and 8.4 us, 4096 of 7168 86 and 89), the second for
+  // many tokens of short ones (2048 of 2048 16.5 and 17.9, 4096 of 2048 29.8 and 31.5; nothing between 4 and 14 KB was
+  // measured).
+  const bool search = p.sh.row_in >= 8192 || (long long)p.sh.W * p.sh.bs * p.sh.K <= 8192;
+  return run_grad(cfg, p, search, ws, static_cast<cudaStream_t>(stream), launch_dispatch_grad);
 }
 
 moe_status_t moe_get_device_status(void* ws, void* stream, int32_t* status) {

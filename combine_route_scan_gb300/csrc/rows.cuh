@@ -85,56 +85,48 @@ __device__ __forceinline__ int4 ld_v4(const void* p) {
   return v;
 }
 
-// The flat row of each lane's routed pick (class cls >= 0; lanes beyond the token's picks have another) without a
-// pick -> row map: the rows of a segment (expert, source rank) are at most bs, so that a warp looks through 32 of a pick's
-// at a time. -1 where no row names the pick, or counts are out of range. All lanes of a warp take part.
-__device__ __forceinline__ long long find_rows(const CombineParams& p, size_t tau, int cls) {
+// The flat row of pick (s, t, k), routed to expert e, without a pick -> row map: a warp looks through the rows of the
+// segment (e, s), at most bs of them, 32 at a time; of more than 32, which dispatch leaves in ascending t, first where t
+// should be and then, should the rows be in another order, through all. -1 where none names the pick, or counts are out
+// of range.
+__device__ __forceinline__ long long find_row(const CombineParams& p, int s, int t, int k, int e) {
   const Shape& sh = p.sh;
-  const int lane = threadIdx.x & 31, s = (int)(tau / sh.bs), t = (int)(tau % sh.bs), LW = sh.L * sh.W;
-  int lo = 0, hi = 0;
-  if (cls >= 0) {
-    const int32_t* ep = p.ep_recv_count + (size_t)(cls / sh.L) * LW;
-    const int seg = cls % sh.L * sh.W + s;
-    hi = ep[seg];
-    lo = seg ? ep[seg - 1] : 0;
-    if (lo < 0 || hi < lo || hi > sh.A || ep[LW - 1] > sh.A) lo = hi = 0;
-  }
-  const long long first = (long long)(cls >= 0 ? cls / sh.L : 0) * sh.A;
-  long long found = -1;
-  // the first 32 rows of all picks are asked for before any is looked at
-  constexpr int kAhead = 8;
-  for (int k0 = 0; k0 < sh.K; k0 += kAhead) {
-    int at[kAhead], ak[kAhead], as[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const long long base = __shfl_sync(0xffffffffu, first + lo, (k0 + j) & 31);
-      const int n = k0 + j < sh.K ? __shfl_sync(0xffffffffu, hi - lo, (k0 + j) & 31) : 0;
-      as[j] = -1;
-      if (lane < n) {
-        const int32_t* a = p.assist + (base + lane) * 3;
-        as[j] = a[0], at[j] = a[1], ak[j] = a[2];
+  const int lane = threadIdx.x & 31, d = e / sh.L, seg = e % sh.L * sh.W + s, LW = sh.L * sh.W;
+  const int32_t* ep = p.ep_recv_count + (size_t)d * LW;
+  const int hi = ep[seg], lo = seg ? ep[seg - 1] : 0;
+  if (lo < 0 || hi > sh.A || ep[LW - 1] > sh.A) return -1;
+  const int32_t* assist = p.assist + (long long)d * sh.A * 3;
+  const auto look = [&](int from, int to) {
+    for (int r = from; r < to; r += 32) {
+      bool here = false;
+      if (r + lane < to) {
+        const int32_t* a = assist + (long long)(r + lane) * 3;
+        here = a[0] == s && a[1] == t && a[2] == k;
       }
+      const uint32_t match = __ballot_sync(0xffffffffu, here);
+      if (match) return (long long)d * sh.A + r + __ffs(match) - 1;
     }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = k0 + j;
-      if (k >= sh.K) break;
-      const long long base = __shfl_sync(0xffffffffu, first + lo, k);
-      const int n = __shfl_sync(0xffffffffu, hi - lo, k);
-      uint32_t match = __ballot_sync(0xffffffffu, as[j] == s && at[j] == t && ak[j] == k);
-      int r = 0;
-      for (; !match && r + 32 < n; r += 32) {
-        bool here = false;
-        if (r + 32 + lane < n) {
-          const int32_t* a = p.assist + (base + r + 32 + lane) * 3;
-          here = a[0] == s && a[1] == t && a[2] == k;
-        }
-        match = __ballot_sync(0xffffffffu, here);
-      }
-      if (lane == k && match) found = base + r + __ffs(match) - 1;
-    }
+    return -1ll;
+  };
+  if (hi - lo > 32) {
+    const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, probe < hi && assist[(long long)probe * 3 + 1] <= t);
+    const int at = lo + max(0, __popc(below) - 1) * step;
+    const long long r = look(at, min(hi, at + step));
+    if (r >= 0) return r;
   }
-  return found;
+  return look(lo, hi);
+}
+
+// The rows of a token's picks into s_row[K], by all warps of the block; ends with a barrier.
+__device__ __forceinline__ void find_rows(const CombineParams& p, size_t tau, long long* s_row) {
+  const Shape& sh = p.sh;
+  for (int k = threadIdx.x >> 5; k < sh.K; k += blockDim.x >> 5) {
+    const int c = classify_pick(p.ids, p.mask, sh, tau, k);
+    const long long r = c >= 0 ? find_row(p, (int)(tau / sh.bs), (int)(tau % sh.bs), k, c) : -1;
+    if ((threadIdx.x & 31) == 0) s_row[k] = r;
+  }
+  __syncthreads();
 }
 
 }  // namespace crs
