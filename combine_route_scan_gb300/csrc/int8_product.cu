@@ -28,6 +28,7 @@
 
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
+#include "quant_common.cuh"
 #include "tcgen05.cuh"
 
 namespace crs {
@@ -43,58 +44,82 @@ struct Int8ProductParams {
   long long A;
   int* status;
   uint64_t timeout_ns;
+  uint8_t raw_stages[6][2];  // of the copies' ring, for row tiles of 32, 64, .. and 2 x 64 and 2 x 128 weight rows a unit
 };
 
-// SwiGLU of a gate and what it gates. exp and the reciprocal are the fast ones, within a
-// few ulps (exp: plus |gate| / 2^23 of its value), far below the rounding to 16 bits that
-// follows; the divisor stays within [1, 2], where the fast reciprocal holds.
+// SwiGLU of a gate and what it gates. exp and the reciprocal are the fast ones, within a few ulps (exp: plus
+// |gate| / 2^23 of its value), far below the rounding to 16 bits that follows; a gate below -87, whose exponential is
+// beyond the reciprocal's range, gives 0.
 __device__ __forceinline__ float int8_swiglu(float gate, float up) {
-  const float t = __expf(-fabsf(gate));
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-  return (gate < 0.f ? gate * t : gate) * r * up;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-gate)));
+  return gate * r * up;
 }
 
-// The experts' rows: first flat row [E] and row count [E] behind the tiles pre[E + 1]. The
-// calling thread's largest count is returned; no barrier.
-template <int THREADS>
-__device__ __forceinline__ int int8_expert_rows(const Int8ProductParams& p, int* pre) {
+// The experts' rows: first flat row [E] and row count [E] behind the tiles pre[E + 1]. Thread t has experts per * t, ..;
+// its largest count is returned; no barrier. `begin` is run once the counts' places are known and before they are read.
+template <int THREADS, class F>
+__device__ __forceinline__ int int8_expert_rows(const Int8ProductParams& p, int* pre, F begin) {
   int* first = pre + p.E + 1;
   int* count = first + p.E;
+  const int per = (p.E + THREADS - 1) / THREADS;
+  int e = per * (int)threadIdx.x, d = e / p.L, le = e - d * p.L;
+  begin();
   int most = 0;
-  for (int e = threadIdx.x; e < p.E; e += THREADS) {
-    const int le = e % p.L;
-    const int32_t* ep = p.ep + (size_t)(e / p.L) * p.L * p.W;
+  for (int i = 0; i < per && e < p.E; ++i, ++e) {
+    const int32_t* ep = p.ep + (size_t)d * p.L * p.W;
     const int hi = ep[le * p.W + p.W - 1], lo = le ? ep[le * p.W - 1] : 0;
     const bool good = lo >= 0 && hi >= lo && hi <= p.A;
     if (!good && blockIdx.x == 0) set_error(p.status, MOE_ERR_BAD_ASSIST);
-    first[e] = (int)(e / p.L * p.A) + (good ? lo : 0);  // flat rows fit 32 bits
+    first[e] = (int)(d * p.A) + (good ? lo : 0);  // flat rows fit 32 bits
     count[e] = good ? hi - lo : 0;
     most = max(most, count[e]);
+    if (++le == p.L) {
+      le = 0;
+      ++d;
+    }
   }
   return most;
 }
 
 // Running tiles of `tile` rows, pre[E + 1], of counts that the same threads have written; false
-// (for every thread) where counts overlap to more tiles than dispatch's can make. All
-// threads of the block take part.
+// (for every thread) where counts overlap to more tiles than dispatch's can make. All threads of the block take part;
+// ends with a barrier. s_warp: two words for each warp.
 template <int THREADS>
-__device__ __forceinline__ bool int8_row_tiles(const Int8ProductParams& p, int tile, int* pre, long long* scratch) {
+__device__ __forceinline__ bool int8_row_tiles(const Int8ProductParams& p, int tile, int* pre, uint32_t (*s_warp)[2]) {
+  constexpr int kWarps = THREADS / 32;
   const int* count = pre + 2 * p.E + 1;
-  long long carry = 0;
-  for (int e0 = 0; e0 < p.E; e0 += THREADS) {
-    const int e = e0 + (int)threadIdx.x;
-    const long long tiles = e < p.E ? (count[e] + tile - 1) / tile : 0;
-    const long long before = carry + block_exclusive_scan(tiles, scratch);
-    if (e < p.E) {
-      pre[e] = (int)min(before, 1ll << 30);
-      if (e == p.E - 1) pre[p.E] = (int)min(before + tiles, 1ll << 30);
-    }
-    __syncthreads();
-    const int last = min(p.E, e0 + THREADS) - 1;
-    carry = pre[last] + (count[last] + tile - 1) / tile;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = (p.E + THREADS - 1) / THREADS;
+  const int e0 = per * (int)threadIdx.x, e1 = min(p.E, e0 + per);
+  uint32_t mine = 0, high = 0;  // the running sums wrap where they are not used: the total in two parts says so
+  for (int e = e0; e < e1; ++e) {
+    const uint32_t t = (uint32_t)(count[e] + tile - 1) / (uint32_t)tile;
+    mine += t;
+    high += t >> 16;
   }
-  return pre[p.E] <= (long long)p.W * p.A / tile + p.E;
+  uint32_t sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t below = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += below;
+  }
+  high = __reduce_add_sync(0xffffffffu, high);
+  if (lane == 31) {
+    s_warp[warp][0] = sum;
+    s_warp[warp][1] = high;
+  }
+  __syncthreads();
+  const uint32_t w = lane < kWarps ? s_warp[lane][0] : 0;
+  uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + sum - mine;
+  const uint32_t total = __reduce_add_sync(0xffffffffu, w);
+  high = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[lane][1] : 0);
+  for (int e = e0; e < e1; ++e) {
+    pre[e] = (int)at;
+    at += (uint32_t)(count[e] + tile - 1) / (uint32_t)tile;
+  }
+  if (threadIdx.x == 0) pre[p.E] = (int)total;
+  __syncthreads();
+  return high <= 1u << 15 && total <= (long long)p.W * p.A / tile + p.E;
 }
 
 // The expert whose tiles hold mt: the last one whose tiles begin at or before it.
@@ -223,9 +248,10 @@ struct Int8Cursor {
   int u, mt, ni, m_step, n_step, n_tiles;
   __device__ Int8Cursor(int n_tiles_) : u(blockIdx.x >> 1), n_tiles(n_tiles_) {
     const int pairs = gridDim.x >> 1;
-    mt = u / n_tiles;
+    const float one = 1.0f / (float)n_tiles;  // of numbers below 2^16, halves away from a whole quotient
+    mt = (int)(((float)u + 0.5f) * one);
     ni = u - mt * n_tiles;
-    m_step = pairs / n_tiles;
+    m_step = (int)(((float)pairs + 0.5f) * one);
     n_step = pairs - m_step * n_tiles;
   }
   __device__ void next() {
@@ -259,25 +285,30 @@ struct Int8Shape {
   uint32_t raw_stages, raw_bytes;
 };
 
-__device__ __forceinline__ Int8Shape int8_shape(int N, int E, int tile, int m_tiles) {
+__device__ __forceinline__ Int8Shape int8_shape(const Int8ProductParams& p, int tile, int m_tiles) {
   Int8Shape s;
   const int pairs = gridDim.x >> 1;
   // 2 x 64 weight rows a unit where 2 x 128 would leave pairs without one
-  int best = 0x7fffffff;
+  float best = 3e38f;
   s.width = 256;
+#pragma unroll
   for (int b = 2; b >= 1; --b) {
-    const int units = m_tiles * ((N + 128 * b - 1) / (128 * b));
-    const int cost = (units + pairs - 1) / pairs * (max(356 * b, 128 * b + 3 * tile) + 64);
+    const float units = (float)m_tiles * (float)((p.N + 128 * b - 1) / (128 * b));
+    const float cost = ceilf(__fdividef(units, (float)pairs) - 0.001f) * (float)(max(356 * b, 128 * b + 3 * tile) + 64);
     if (cost < best) {
       best = cost;
       s.width = 128 * b;
     }
   }
-  s.n_tiles = (N + s.width - 1) / s.width;
+  s.n_tiles = (p.N + s.width - 1) >> (s.width == 256 ? 8 : 7);
   s.raw_bytes = (uint32_t)(s.width + tile) * 64;
-  s.raw_stages =
-      min((uint32_t)kInt8RawStages, ((uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - int8_slots(tile) * int8_halves(tile) * tile * 64) / s.raw_bytes);
+  s.raw_stages = p.raw_stages[(tile >> 5) - 1][(s.width >> 7) - 1];
   return s;
+}
+static uint8_t int8_raw_stages(int E, int tile, int width) {
+  const uint32_t room = (uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - int8_slots(tile) * int8_halves(tile) * tile * 64;
+  const uint32_t stages = room / ((uint32_t)(width + tile) * 64);
+  return (uint8_t)(stages < kInt8RawStages ? stages : kInt8RawStages);
 }
 static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - int8_slots(kInt8MostRows) * int8_halves(kInt8MostRows) * kInt8MostRows * 64) /
                       ((256 + kInt8MostRows) * 64) >= 4, "four stages at least");
@@ -292,15 +323,18 @@ __device__ __forceinline__ void int8_store(const Int8ProductParams& p, uint32_t 
   // columns, whose chains of some 200 clocks overlap
 #pragma unroll
   for (int c0 = 0; c0 < 32; c0 += 16) {
-    float x[16];
+    f32x2 s[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int4 w = lds_v4(xs + (c0 + 4 * i) * 4);
-      x[4 * i] = __int_as_float(w.x), x[4 * i + 1] = __int_as_float(w.y);
-      x[4 * i + 2] = __int_as_float(w.z), x[4 * i + 3] = __int_as_float(w.w);
+      s[2 * i] = f2_pack(__int_as_float(w.x), __int_as_float(w.y));
+      s[2 * i + 1] = f2_pack(__int_as_float(w.z), __int_as_float(w.w));
     }
+    float x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[c0 + i]) * x[i] * wscale;
+    for (int i = 0; i < 8; ++i)
+      f2_split(f2_mul(f2_mul(f2_pack(__uint_as_float(v[c0 + 2 * i]), __uint_as_float(v[c0 + 2 * i + 1])), s[i]),
+                      f2_pack(wscale, wscale)), x[2 * i], x[2 * i + 1]);
     if (SWIGLU) {
       // gates lie in the even lanes, what they gate in the odd ones: of two columns the even lane takes the first, the
       // odd one the second
@@ -346,13 +380,13 @@ __device__ __forceinline__ void int8_store(const Int8ProductParams& p, uint32_t 
 
 template <int YT, bool SWIGLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads, 1)
-    int8_product_kernel(const __grid_constant__ Int8Maps maps, Int8ProductParams p) {
+    int8_product_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
   __shared__ __align__(8) uint64_t raw_full[kInt8RawStages], raw_empty[kInt8RawStages];
   __shared__ __align__(8) uint64_t wide_full[kInt8Slots], wide_empty[kInt8Slots];  // full: of the first CTA, for both
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drained;              // empty: of the first CTA, for both
   __shared__ uint32_t tmem_slot;
-  __shared__ long long scan_scratch[32];
+  __shared__ uint32_t s_warp[kInt8ProductThreads / 32][2];
   __shared__ int s_most[kInt8ProductThreads / 32];
   __shared__ volatile int s_abort;
 
@@ -362,44 +396,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   uint8_t* turn = sm + kInt8ProductSmem - 1024 - int8_fixed_smem(p.E);
   int* pre = reinterpret_cast<int*>(turn + 4 * (kInt8TurnWarp + kInt8MostRows * 4));
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kInt8RawStages; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 2 * kSetWarps);  // two sets once, or one twice
+  if (warp == 0) {  // a lane has a barrier of each kind
+    if (lane < kInt8RawStages) {
+      mbar_init(&raw_full[lane], 1);
+      mbar_init(&raw_empty[lane], 2 * kSetWarps);  // two sets once, or one twice
     }
-    for (int i = 0; i < kInt8Slots; ++i) {
-      mbar_init(&wide_full[i], 2 * kSetWarps);  // a set's warps in each CTA
-      mbar_init(&wide_empty[i], 1);
+    if (lane < kInt8Slots) {
+      mbar_init(&wide_full[lane], 2 * kSetWarps);  // a set's warps in each CTA
+      mbar_init(&wide_empty[lane], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+    if (lane < 2) {
+      mbar_init(&acc_full[lane], 1);
+      mbar_init(&acc_empty[lane], 8);
     }
-    mbar_init(&drained, 1);
+    if (lane == 2) mbar_init(&drained, 1);
+    if (lane == 3) s_abort = 0;
     mbar_fence_init();
-    s_abort = 0;
+    __syncwarp();
   }
-  __syncwarp();
   cluster_arrive();
   if (warp == 1) {
     tmem_alloc_pair(&tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  pdl_wait();
-  pdl_launch_dependents();
-
-  int most = __reduce_max_sync(0xffffffffu, int8_expert_rows<kInt8ProductThreads>(p, pre));
+  int most = __reduce_max_sync(0xffffffffu, int8_expert_rows<kInt8ProductThreads>(p, pre, [] {
+    pdl_wait();
+    pdl_launch_dependents();
+  }));
   if (lane == 0) s_most[warp] = most;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   most = __reduce_max_sync(0xffffffffu, lane < kInt8ProductThreads / 32 ? s_most[lane] : 0);
   const int tile = min(kInt8MostRows, max(32, (most + 31) / 32 * 32));
-  const bool countable = int8_row_tiles<kInt8ProductThreads>(p, tile, pre, scan_scratch);
+  const bool countable = int8_row_tiles<kInt8ProductThreads>(p, tile, pre, s_warp);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   // overlapping experts can have more row tiles than the units' numbers hold: then none is worked on
   const int m_tiles = countable ? __shfl_sync(0xffffffffu, pre[p.E], 0) : 0, KB = (p.K + kInt8Stage - 1) / kInt8Stage;
-  const Int8Shape shape = int8_shape(p.N, p.E, tile, m_tiles);
+  const Int8Shape shape = int8_shape(p, tile, m_tiles);
   const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
   const int half = width >> 1;  // this CTA's weight rows of a unit
   const uint32_t raw_stages = __shfl_sync(0xffffffffu, shape.raw_stages, 0), raw_bytes = __shfl_sync(0xffffffffu, shape.raw_bytes, 0);
@@ -466,12 +500,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
             }
             const int left = p.K - kb * (64 * halves);
             if (left >= 64 * halves) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + kk * 8, bdesc + kk * 2, idesc, kk > 0 || kb > 0);
-              if (halves == 2) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) tc_mma_f16_pair(acc, a + 32 + kk * 8, bdesc + (panel >> 4) + kk * 2, idesc, true);
-              }
+              tc_mma4_f16_pair(acc, a, bdesc, idesc, kb > 0);
+              if (halves == 2) tc_mma4_f16_pair(acc, a + 32, bdesc + (panel >> 4), idesc, true);
             } else {
 #pragma unroll 1
               for (int kk = 0; kk * 16 < left; ++kk)
@@ -528,14 +558,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
             widen16(c3, v + 8);
             tc_st16(ta + 16, v);
           }
-          for (int t = w, g = 0; t < tasks; t += kSetWarps, g += kSetWarps * 1024) {
-            uint32_t v[8];
-            widen16(lds_v4(st + (x_from ^ flip) + g), v);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to0 + off + g), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(x_to1 + off + g), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                         : "memory");
-          }
+          const uint32_t from = st + (x_from ^ flip), to0 = x_to0 + off, to1 = x_to1 + off;
+#pragma unroll
+          for (int i = 0; i < kInt8MostRows / 32 * 2 / kSetWarps; ++i)
+            if ((int)w + i * kSetWarps < tasks) {
+              const uint32_t g = i * kSetWarps * 1024;
+              uint32_t v[8];
+              widen16(lds_v4(from + g), v);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to0 + g), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to1 + g), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                           : "memory");
+            }
         }
         tc_wait_st();
         fence_proxy_async_smem();
@@ -628,12 +662,13 @@ constexpr int kPlainThreads = 256, kPlainRows = 32, kPlainCols = 64, kPlainK = 1
 template <int YT, bool SWIGLU>
 __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8ProductParams p) {
   __shared__ int s_x[kPlainRows][kPlainK / 4 + 1], s_w[kPlainCols][kPlainK / 4 + 1];
-  __shared__ long long scratch[32];
+  __shared__ uint32_t s_warp[kPlainThreads / 32][2];
   extern __shared__ int pre[];
-  pdl_wait();
-  pdl_launch_dependents();
-  int8_expert_rows<kPlainThreads>(p, pre);
-  if (!int8_row_tiles<kPlainThreads>(p, kPlainRows, pre, scratch)) return;
+  int8_expert_rows<kPlainThreads>(p, pre, [] {
+    pdl_wait();
+    pdl_launch_dependents();
+  });
+  if (!int8_row_tiles<kPlainThreads>(p, kPlainRows, pre, s_warp)) return;
   const int* first = pre + p.E + 1;
   const int* count = first + p.E;
   const int n_tiles = (p.N + kPlainCols - 1) / kPlainCols;
@@ -774,6 +809,8 @@ extern "C" moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const i
     for (unsigned i = 0; i < 2; ++i)
       good = good && int8_map(&maps.w[i], w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, 64 * (i + 1));
     if (!good) return MOE_ERR_CUDA;
+    for (int t = 0; t < 6; ++t)
+      for (int b = 0; b < 2; ++b) p.raw_stages[t][b] = int8_raw_stages(E, 32 * (t + 1), 128 * (b + 1));
     const Int8Kernel kernel = y_dtype == MOE_F16 ? (sw ? int8_product_kernel<MOE_F16, true> : int8_product_kernel<MOE_F16, false>)
                                                  : (sw ? int8_product_kernel<MOE_BF16, true> : int8_product_kernel<MOE_BF16, false>);
     if (resident_blocks((const void*)kernel, kInt8ProductThreads, kInt8ProductSmem, &per_sm) != cudaSuccess || per_sm < 1)
