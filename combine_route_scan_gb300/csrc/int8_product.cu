@@ -56,15 +56,20 @@ __device__ __forceinline__ float int8_swiglu(float gate, float up) {
   return gate * r * up;
 }
 
+// A barrier of the block's first THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ void int8_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
 // The experts' rows: first flat row [E] and row count [E] behind the tiles pre[E + 1]. Thread t has experts per * t, ..;
-// its largest count is returned; no barrier. `begin` is run once the counts' places are known and before they are read.
-template <int THREADS, class F>
-__device__ __forceinline__ int int8_expert_rows(const Int8ProductParams& p, int* pre, F begin) {
+// its largest count is returned; no barrier.
+template <int THREADS>
+__device__ __forceinline__ int int8_expert_rows(const Int8ProductParams& p, int* pre) {
   int* first = pre + p.E + 1;
   int* count = first + p.E;
   const int per = (p.E + THREADS - 1) / THREADS;
   int e = per * (int)threadIdx.x, d = e / p.L, le = e - d * p.L;
-  begin();
   int most = 0;
   for (int i = 0; i < per && e < p.E; ++i, ++e) {
     const int32_t* ep = p.ep + (size_t)d * p.L * p.W;
@@ -83,43 +88,46 @@ __device__ __forceinline__ int int8_expert_rows(const Int8ProductParams& p, int*
 }
 
 // Running tiles of `tile` rows, pre[E + 1], of counts that the same threads have written; false
-// (for every thread) where counts overlap to more tiles than dispatch's can make. All threads of the block take part;
-// ends with a barrier. s_warp: two words for each warp.
+// (for every thread) where counts overlap to more tiles than dispatch's can make. The block's first THREADS threads take
+// part; ends with their barrier. s_warp: a word for each warp, and one that is 0.
 template <int THREADS>
-__device__ __forceinline__ bool int8_row_tiles(const Int8ProductParams& p, int tile, int* pre, uint32_t (*s_warp)[2]) {
+__device__ __forceinline__ bool int8_row_tiles(const Int8ProductParams& p, int tile, int* pre, uint32_t* s_warp) {
   constexpr int kWarps = THREADS / 32;
   const int* count = pre + 2 * p.E + 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = (p.E + THREADS - 1) / THREADS;
   const int e0 = per * (int)threadIdx.x, e1 = min(p.E, e0 + per);
-  uint32_t mine = 0, high = 0;  // the running sums wrap where they are not used: the total in two parts says so
+  const auto running = [lane](uint32_t sum) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t below = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += below;
+    }
+    return sum;
+  };
+  uint32_t mine = 0;
   for (int e = e0; e < e1; ++e) {
     const uint32_t t = (uint32_t)(count[e] + tile - 1) / (uint32_t)tile;
     mine += t;
-    high += t >> 16;
+    if (t >> 16) s_warp[kWarps] = 1;
   }
-  uint32_t sum = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t below = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += below;
+  const uint32_t sum = running(mine);
+  if (lane == 31) s_warp[warp] = sum;
+  int8_barrier<THREADS>();
+  const uint32_t below = running(lane < kWarps ? s_warp[lane] : 0);
+  const uint32_t total = __shfl_sync(0xffffffffu, below, 31), before = __shfl_sync(0xffffffffu, below, (warp + 31) & 31);
+  uint32_t at = (warp ? before : 0) + sum - mine;
+  long long whole = total;
+  if (s_warp[kWarps]) {  // an expert of millions of rows: the sums may have wrapped
+    whole = 0;
+    for (int e = 0; e < p.E; ++e) whole += (count[e] + tile - 1) / tile;
   }
-  high = __reduce_add_sync(0xffffffffu, high);
-  if (lane == 31) {
-    s_warp[warp][0] = sum;
-    s_warp[warp][1] = high;
-  }
-  __syncthreads();
-  const uint32_t w = lane < kWarps ? s_warp[lane][0] : 0;
-  uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + sum - mine;
-  const uint32_t total = __reduce_add_sync(0xffffffffu, w);
-  high = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_warp[lane][1] : 0);
   for (int e = e0; e < e1; ++e) {
     pre[e] = (int)at;
     at += (uint32_t)(count[e] + tile - 1) / (uint32_t)tile;
   }
   if (threadIdx.x == 0) pre[p.E] = (int)total;
-  __syncthreads();
-  return high <= 1u << 15 && total <= (long long)p.W * p.A / tile + p.E;
+  int8_barrier<THREADS>();
+  return whole <= (long long)p.W * p.A / tile + p.E;
 }
 
 // The expert whose tiles hold mt: the last one whose tiles begin at or before it.
@@ -143,7 +151,7 @@ struct Int8Maps {
 };
 
 constexpr int kWidenWarp = 2, kSets = 4, kSetWarps = 4;
-constexpr int kInt8ProductThreads = 22 * 32;
+constexpr int kInt8ProductThreads = 22 * 32, kInt8PlanThreads = 8 * 32;
 constexpr int kInt8Stage = 128;    // elements of K a stage
 constexpr int kInt8MostRows = 192; // MMA N
 constexpr int kInt8RawStages = 8;  // at most
@@ -281,8 +289,8 @@ __device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const 
 
 // How a launch cuts its work: weight rows a unit (half of them for each CTA), and as many stages as shared memory holds.
 struct Int8Shape {
-  int width, n_tiles;
-  uint32_t raw_stages, raw_bytes;
+  int tile, width, n_tiles, units;
+  uint32_t raw_stages;
 };
 
 __device__ __forceinline__ Int8Shape int8_shape(const Int8ProductParams& p, int tile, int m_tiles) {
@@ -301,7 +309,8 @@ __device__ __forceinline__ Int8Shape int8_shape(const Int8ProductParams& p, int 
     }
   }
   s.n_tiles = (p.N + s.width - 1) >> (s.width == 256 ? 8 : 7);
-  s.raw_bytes = (uint32_t)(s.width + tile) * 64;
+  s.tile = tile;
+  s.units = m_tiles * s.n_tiles;
   s.raw_stages = p.raw_stages[(tile >> 5) - 1][(s.width >> 7) - 1];
   return s;
 }
@@ -386,8 +395,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   __shared__ __align__(8) uint64_t wide_full[kInt8Slots], wide_empty[kInt8Slots];  // full: of the first CTA, for both
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drained;              // empty: of the first CTA, for both
   __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t s_warp[kInt8ProductThreads / 32][2];
-  __shared__ int s_most[kInt8ProductThreads / 32];
+  __shared__ uint32_t s_warp[kInt8PlanThreads / 32 + 1];
+  __shared__ int s_most;
+  __shared__ Int8Shape s_shape;
   __shared__ volatile int s_abort;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -410,36 +420,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       mbar_init(&acc_empty[lane], 8);
     }
     if (lane == 2) mbar_init(&drained, 1);
-    if (lane == 3) s_abort = 0;
+    if (lane == 3) s_abort = 0, s_most = 0, s_warp[kInt8PlanThreads / 32] = 0;
     mbar_fence_init();
     __syncwarp();
   }
   cluster_arrive();
-  if (warp == 1) {
+  pdl_wait();
+  pdl_launch_dependents();
+  // Eight warps count the experts' tiles: all of them took twice as long over it, for their instructions.
+  if (threadIdx.x < kInt8PlanThreads) {
+    int8_barrier<kInt8PlanThreads>();  // s_most and the last of s_warp are 0
+    const int most = __reduce_max_sync(0xffffffffu, int8_expert_rows<kInt8PlanThreads>(p, pre));
+    if (lane == 0 && most) atomicMax(&s_most, most);
+    int8_barrier<kInt8PlanThreads>();
+    const int tile = min(kInt8MostRows, max(32, (s_most + 31) >> 5 << 5));
+    // overlapping experts can have more row tiles than the units' numbers hold: then none is worked on
+    const bool countable = int8_row_tiles<kInt8PlanThreads>(p, tile, pre, s_warp);
+    if (threadIdx.x == 0) s_shape = int8_shape(p, tile, countable ? pre[p.E] : 0);
+  } else if (warp == kInt8PlanThreads / 32) {
     tmem_alloc_pair(&tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  int most = __reduce_max_sync(0xffffffffu, int8_expert_rows<kInt8ProductThreads>(p, pre, [] {
-    pdl_wait();
-    pdl_launch_dependents();
-  }));
-  if (lane == 0) s_most[warp] = most;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  most = __reduce_max_sync(0xffffffffu, lane < kInt8ProductThreads / 32 ? s_most[lane] : 0);
-  const int tile = min(kInt8MostRows, max(32, (most + 31) / 32 * 32));
-  const bool countable = int8_row_tiles<kInt8ProductThreads>(p, tile, pre, s_warp);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  // overlapping experts can have more row tiles than the units' numbers hold: then none is worked on
-  const int m_tiles = countable ? __shfl_sync(0xffffffffu, pre[p.E], 0) : 0, KB = (p.K + kInt8Stage - 1) / kInt8Stage;
-  const Int8Shape shape = int8_shape(p, tile, m_tiles);
-  const int width = __shfl_sync(0xffffffffu, shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, shape.n_tiles, 0);
+  const int tile = __shfl_sync(0xffffffffu, s_shape.tile, 0), KB = (p.K + kInt8Stage - 1) / kInt8Stage;
+  const int width = __shfl_sync(0xffffffffu, s_shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, s_shape.n_tiles, 0);
+  const int units = __shfl_sync(0xffffffffu, s_shape.units, 0);
+  const uint32_t raw_stages = __shfl_sync(0xffffffffu, s_shape.raw_stages, 0), raw_bytes = (uint32_t)(width + tile) * 64;
   const int half = width >> 1;  // this CTA's weight rows of a unit
-  const uint32_t raw_stages = __shfl_sync(0xffffffffu, shape.raw_stages, 0), raw_bytes = __shfl_sync(0xffffffffu, shape.raw_bytes, 0);
   const int halves = int8_halves(tile);
   const uint32_t panel = tile * 64, slot_bytes = panel * halves, slot_cols = 32 * halves, slots = int8_slots(tile);
-  const int units = m_tiles * n_tiles;
   // shared memory: the widened rows, then the copies' ring; tensor memory: two accumulators, then the widened weights
   const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + slots * slot_bytes, tmem_a = tmem + 2 * tile;
   const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty);
@@ -646,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // nor does a CTA leave while the other one may still arrive on its barriers
-  if (warp == 1) {
+  if (warp == kInt8PlanThreads / 32) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -662,12 +674,13 @@ constexpr int kPlainThreads = 256, kPlainRows = 32, kPlainCols = 64, kPlainK = 1
 template <int YT, bool SWIGLU>
 __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8ProductParams p) {
   __shared__ int s_x[kPlainRows][kPlainK / 4 + 1], s_w[kPlainCols][kPlainK / 4 + 1];
-  __shared__ uint32_t s_warp[kPlainThreads / 32][2];
+  __shared__ uint32_t s_warp[kPlainThreads / 32 + 1];
   extern __shared__ int pre[];
-  int8_expert_rows<kPlainThreads>(p, pre, [] {
-    pdl_wait();
-    pdl_launch_dependents();
-  });
+  if (threadIdx.x == 0) s_warp[kPlainThreads / 32] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  int8_expert_rows<kPlainThreads>(p, pre);
   if (!int8_row_tiles<kPlainThreads>(p, kPlainRows, pre, s_warp)) return;
   const int* first = pre + p.E + 1;
   const int* count = first + p.E;
