@@ -572,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
           }
           const uint32_t from = st + (x_from ^ flip), to0 = x_to0 + off, to1 = x_to1 + off;
 #pragma unroll
-          for (int i = 0; i < kInt8MostRows / 32 * 2 / kSetWarps; ++i)
+          for (int i = 0; i < (kInt8MostRows / 32 * 2 + kSetWarps - 1) / kSetWarps; ++i)
             if ((int)w + i * kSetWarps < tasks) {
               const uint32_t g = i * kSetWarps * 1024;
               uint32_t v[8];
