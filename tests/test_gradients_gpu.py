@@ -323,6 +323,26 @@ def test_two_batches_of_one_workspace():
     b.check_combine(b.combine_backward(g, y), g64, y64)
 
 
+@pytest.mark.parametrize("bs", [20, 90, 700])
+def test_rows_in_another_order(bs):
+    """Rows permuted within their segments, as combine takes them: found all the same, by each gradient and with a map."""
+    r = Routed(2, bs, 2, 4, 32, 0, 1, 2, "bf16", seed=bs)
+    y, y64 = r.expert_rows()
+    g, g64 = r.rows((2, bs, 32))
+    order = np.tile(np.arange(r.A), (2, 1))
+    for d in range(2):
+        edges = [0, *r.ep[d]]
+        for lo, hi in zip(edges[:-1], edges[1:]):
+            order[d, lo:hi] = lo + r.rng.permutation(hi - lo)
+    r.assist = np.take_along_axis(r.assist, order[..., None], 1)
+    r.out["assist_info"] = torch.from_numpy(r.assist).cuda()  # in a buffer of its own: no map is its
+    r.where = {tuple(r.assist[d, i]): (d, i) for d in range(2) for i in range(r.ep[d, -1])}
+    r.check_combine(r.combine_backward(g, y, x=True), g64, y64)
+    got = r.dispatch_backward(y, g)
+    r.check_dispatch(got, y64, g64)
+    assert M.get_device_status(r.ws) == 0
+
+
 def test_rows_beyond_32_bits():
     """Rows that begin behind 2^31 elements of their array: two ranks of 33000 tokens, each with room for all of them."""
     W, bs, h = 2, 33000, 16448

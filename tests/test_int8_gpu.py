@@ -103,6 +103,48 @@ def test_quantize_edges(cols):
     assert scales[1] == np.inf and not codes[1].any() and scales[3] == 0
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_quantize_edges_of_16_bits(dtype):
+    """The largest magnitude is taken pair by pair there: NaN in either half, infinities, the type's ends, zeros."""
+    cols, t = 64, DT[dtype]
+    x = torch.randn(9, cols, generator=torch.Generator().manual_seed(3)).to(t)
+    x[0], x[1, 7], x[2, 8], x[3] = 0, float("nan"), float("nan"), float("nan")
+    x[4, 63], x[5, 62] = float("inf"), -float("inf")
+    x[6, 5], x[7] = torch.finfo(t).min, torch.finfo(t).tiny / 4 if dtype == "f16" else 1e-40
+    x[8, 11] = 0.0
+    codes, scales = M.alloc_int8(x.cuda())
+    M.int8_quantize(x.cuda(), codes, scales)
+    torch.cuda.synchronize()
+    q, s = quantized(x.float().numpy())
+    there = ~torch.isnan(x).numpy()
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy()[there], q[there])
+
+
+@pytest.mark.parametrize("cols", [256, 250])
+@pytest.mark.parametrize("exponent", [-140, -126, -101, -100, -90, -3, 0, 40, 119])
+def test_quantize_next_to_half_steps(exponent, cols):
+    """Elements whose quotient is half a step and its neighbours in fp32, at scales from the smallest to the largest."""
+    rng = np.random.default_rng(exponent + 200)
+    rows = 400
+    scale = np.ldexp(rng.uniform(1, 2, rows), exponent).astype(np.float32)
+    x = np.zeros((rows, cols), dtype=np.float32)
+    amax = (scale * np.float32(127)).astype(np.float32)
+    x[:, 0] = np.where(np.isfinite(amax), amax, np.float32(3.4e38))
+    scale = (x[:, 0] / np.float32(127)).astype(np.float32)
+    half = rng.integers(-127, 127, (rows, cols - 1)) + 0.5
+    near = (half * scale[:, None].astype(np.float64)).astype(np.float32)
+    for _ in range(2):  # up to two steps of fp32 to either side
+        step = rng.integers(-1, 2, near.shape)
+        near = np.where(step < 0, np.nextafter(near, np.float32(-np.inf)), np.where(step > 0, np.nextafter(near, np.float32(np.inf)), near))
+    x[:, 1:] = np.clip(near, -x[:, :1], x[:, :1])
+    t = torch.from_numpy(x).cuda()
+    codes, scales = M.alloc_int8(t)
+    M.int8_quantize(t, codes, scales)
+    torch.cuda.synchronize()
+    q, s = quantized(x)
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), q)
+
+
 @pytest.mark.parametrize("cols,dtype", [(64, "bf16"), (66, "f16"), (4096, "f32"), (3000, "bf16")])
 def test_quantize_received_rows(cols, dtype):
     """With counts, rows beyond the last count of a rank are neither read nor written."""
@@ -287,6 +329,29 @@ def test_product_largest_sums(k):
         got = y[d, lo:hi].double().cpu().numpy()
         # an addition of 16 products may be cut instead of rounded: one step of fp32 each
         assert (np.abs(got - want) <= (2.0 ** -8 + 2 * EPS * (k / 16 + 1)) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("k", [64, 67])
+def test_product_of_no_rows(k):
+    """Tokens that all went elsewhere: counts of zero, and one expert with a row among many without."""
+    for counts in ([0, 0, 0, 0], [0, 0, 1, 0]):
+        pr = Product(2, 8, 2, counts, 96, k, seed=8)
+        pr.check(pr.run("bf16", False), "bf16", False)
+
+
+def test_product_calls_that_overlap():
+    """Two streams, one workspace: the product writes nothing there."""
+    a, b = Product(2, 80, 2, [129, 31, 0, 160], 512, 320, seed=5), Product(2, 80, 2, [3, 90, 100, 1], 512, 320, seed=6)
+    want = [pr.run("bf16", True) for pr in (a, b)]
+    dev = [[torch.from_numpy(t).cuda() for t in (pr.x, pr.xs, pr.ep, pr.w, pr.ws)] for pr in (a, b)]
+    ys, ws = [torch.full_like(w, 777.0) for w in want], M.alloc_workspace(a.cfg)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, y, st in zip(dev, ys, streams):
+            M.expert_product_int8(a.cfg, *d, y, M.EPI_SWIGLU, ws, st)
+    torch.cuda.synchronize()
+    assert M.get_device_status(ws) == 0 and all(torch.equal(y, w) for y, w in zip(ys, want))
 
 
 def test_product_without_row_scales():
