@@ -192,7 +192,7 @@ def measured_peaks() -> dict:
 KERNEL_SOURCES = {
     "scatter": ("scatter.cu", "scatter_common.cuh", "common.cuh", "internal.h"),
     "scatter_quant": ("scatter_quant.cu", "scatter_common.cuh", "common.cuh", "internal.h"),
-    "combine_reduce": ("combine.cu", "common.cuh", "internal.h"),
+    "combine_reduce": ("combine.cu", "rows.cuh", "gradients.h", "common.cuh", "internal.h"),
 }
 
 

@@ -19,6 +19,7 @@
 // residual[token] + sum_k grad_expand_x[row of (token, k)].
 #include <type_traits>
 
+#include "gradients.h"
 #include "rows.cuh"
 
 namespace crs {
@@ -262,8 +263,8 @@ __global__ void __launch_bounds__(kReduceThreads, 4) combine_reduce_kernel(P p, 
 }
 
 // Element-wise fallback for rows that are not 16-byte multiples.
-template <int DT, class P>
-__global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(P p) {
+template <int DT>
+__global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(CombineParams p) {
   __shared__ ReduceTable tab;
   const Shape sh = p.sh;
   pdl_wait();
@@ -279,12 +280,15 @@ __global__ void __launch_bounds__(kReduceThreads) combine_reduce_plain_kernel(P 
         reinterpret_cast<uint32_t*>(p.x_out)[tau * sh.h + j] = acc;
       } else {
         float acc = 0.f;
-        if constexpr (std::is_same<P, DispatchGradParams>::value) {
-          if (p.residual) acc = elem_to_float<DT>(static_cast<const uint16_t*>(p.residual)[tau * sh.h + j]);
+        for (int q = 0; q < n; ++q) {
+          const uint16_t b = reinterpret_cast<const uint16_t*>(tab.src[q])[j];
+          const float y = DT == MOE_F16 ? __half2float(__ushort_as_half(b))
+                                        : __bfloat162float(__ushort_as_bfloat16(b));
+          acc = __fmaf_rn(__uint_as_float(tab.w[q]), y, acc);
         }
-        for (int q = 0; q < n; ++q)
-          acc = __fmaf_rn(__uint_as_float(tab.w[q]), elem_to_float<DT>(reinterpret_cast<const uint16_t*>(tab.src[q])[j]), acc);
-        reinterpret_cast<uint16_t*>(p.x_out)[tau * sh.h + j] = float_to_elem<DT>(acc);
+        uint16_t o = DT == MOE_F16 ? __half_as_ushort(__float2half_rn(acc))
+                                   : __bfloat16_as_ushort(__float2bfloat16_rn(acc));
+        reinterpret_cast<uint16_t*>(p.x_out)[tau * sh.h + j] = o;
       }
     }
     __syncthreads();
@@ -305,14 +309,14 @@ static cudaError_t launch_reduce(const P& p, cudaStream_t st, int num_sms) {
   const Shape& sh = p.sh;
   const long long n_tok = (long long)sh.W * sh.bs;
   if (n_tok == 0) return cudaSuccess;
-  if (sh.row_in % 16 != 0) {
-    const int grid = (int)(n_tok < num_sms * 8LL ? n_tok : num_sms * 8LL);
-    PdlLaunch L(dim3(grid), dim3(kReduceThreads), 0, st);
-    if constexpr (!kGrad) {
-      if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_I32, P>, p);
+  if constexpr (!kGrad) {  // the gradient of such rows takes another way (combine_grad.cu)
+    if (sh.row_in % 16 != 0) {
+      const int grid = (int)(n_tok < num_sms * 8LL ? n_tok : num_sms * 8LL);
+      PdlLaunch L(dim3(grid), dim3(kReduceThreads), 0, st);
+      if (sh.x_dtype == MOE_I32) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_I32>, p);
+      if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_F16>, p);
+      return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_BF16>, p);
     }
-    if (sh.x_dtype == MOE_F16) return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_F16, P>, p);
-    return cudaLaunchKernelEx(&L.cfg, combine_reduce_plain_kernel<MOE_BF16, P>, p);
   }
   const int nvec = sh.row_in / 16;
   // smaller work items when the batch is too small to give every SM ~16 warps

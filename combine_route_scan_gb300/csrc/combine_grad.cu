@@ -8,9 +8,16 @@
 // expert, row after row, it would come K times from L2), and goes through the row's
 // 16-byte vectors with the loads of up to 8 picks in flight; the products' sums stay
 // in registers and are joined over the lanes and then the warps in a fixed order.
-// The rows come from the pick -> row map of the dispatch, checked against assist_info as combine's reduce does, or, where
-// the workspace has no such map, by looking through assist_info (rows.cuh). Bound by HBM: the tokens and the rows,
-// read, and the rows, written: 4096 tokens of hidden 7168 with 27000 rows 150 us, 5.9 TB/s.
+// The rows come from the pick -> row map of the dispatch, checked against assist_info
+// as combine's reduce does, or, where the workspace has no such map, by looking
+// through assist_info. Bound by HBM: the tokens and the rows, read, and the
+// rows, written: 4096 tokens of hidden 7168 with 27000 rows 143 us, 6.3 TB/s. A small
+// batch is one block's chain of steps: 16 tokens of hidden 256 4.1 us.
+//
+// Rows that do not align to 16 bytes are taken in pieces of 8, 4 or 2 bytes, eight
+// elements a thread at a time: 2048 tokens of hidden 2048 29 us, 2044 38, 2046 43, 2047
+// 64 (an element at a time 117).
+#include "gradients.h"
 #include "rows.cuh"
 
 namespace crs {
@@ -18,9 +25,102 @@ namespace crs {
 constexpr int kGradBatch = 8;     // picks whose loads are in flight together
 constexpr int kGradThreads = 256; // at most
 
-// VEC: rows of 16-byte vectors; else an element at a time. SEARCH: without a row map (rows.cuh).
-template <int DT, bool VEC, bool SEARCH>
-__global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGradParams p, int active) {
+// 8 elements of a row in pieces of BYTES (16, 8, 4 or 2), `apart` bytes from one another from `off` on; those beyond the
+// row's end are zeros, and not stored. load_own: of what the kernel may write too.
+template <int BYTES>
+struct RowUnit {
+  static constexpr int kPieces = 16 / BYTES;
+  template <class F>
+  static __device__ __forceinline__ int4 gather(uint32_t off, uint32_t apart, uint32_t end, F read) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const uint32_t at = off + q * apart;
+      if constexpr (BYTES == 8) {
+        const uint2 v = at < end ? read(at, uint2{}) : uint2{0, 0};
+        w[2 * q] = v.x, w[2 * q + 1] = v.y;
+      } else if constexpr (BYTES == 4) {
+        w[q] = at < end ? read(at, uint32_t{}) : 0u;
+      } else {
+        const uint32_t v = at < end ? (uint32_t)read(at, uint16_t{}) : 0u;
+        if (q & 1) w[q / 2] |= v << 16;
+        else w[q / 2] = v;
+      }
+    }
+    return make_int4((int)w[0], (int)w[1], (int)w[2], (int)w[3]);
+  }
+  static __device__ __forceinline__ int4 load(const uint8_t* row, uint32_t off, uint32_t apart, uint32_t end) {
+    if constexpr (BYTES == 16) return ld_nc_v4(row + off);
+    else return gather(off, apart, end, [&](uint32_t at, auto t) { return __ldg(reinterpret_cast<const decltype(t)*>(row + at)); });
+  }
+  static __device__ __forceinline__ int4 load_own(const uint8_t* row, uint32_t off, uint32_t apart, uint32_t end) {
+    if constexpr (BYTES == 16) return ld_v4(row + off);
+    else return gather(off, apart, end, [&](uint32_t at, auto t) { return *reinterpret_cast<const decltype(t)*>(row + at); });
+  }
+  static __device__ __forceinline__ void store(uint8_t* row, uint32_t off, uint32_t apart, uint32_t end, int4 v) {
+    if constexpr (BYTES == 16) {
+      __stcs(reinterpret_cast<int4*>(row + off), v);
+    } else {
+      const uint32_t w[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const uint32_t at = off + q * apart;
+        if (at >= end) break;
+        if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(row + at) = make_uint2(w[2 * q], w[2 * q + 1]);
+        else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(row + at) = w[q];
+        else *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
+      }
+    }
+  }
+};
+
+// The flat row of pick (s, t, k), routed to expert e, without a pick -> row map: a warp looks through the rows of the
+// segment (e, s), at most bs of them, 32 at a time; of more than 32, which dispatch leaves in ascending t, first where t
+// should be and then, should the rows be in another order, through all. -1 where none names the pick, or counts are out
+// of range.
+__device__ __forceinline__ long long find_row(const CombineParams& p, int s, int t, int k, int e) {
+  const Shape& sh = p.sh;
+  const int lane = threadIdx.x & 31, d = e / sh.L, seg = e % sh.L * sh.W + s, LW = sh.L * sh.W;
+  const int32_t* ep = p.ep_recv_count + (size_t)d * LW;
+  const int hi = ep[seg], lo = seg ? ep[seg - 1] : 0;
+  if (lo < 0 || hi > sh.A || ep[LW - 1] > sh.A) return -1;
+  const int32_t* assist = p.assist + (long long)d * sh.A * 3;
+  const auto look = [&](int from, int to) {
+    for (int r = from; r < to; r += 32) {
+      bool here = false;
+      if (r + lane < to) {
+        const int32_t* a = assist + (long long)(r + lane) * 3;
+        here = a[0] == s && a[1] == t && a[2] == k;
+      }
+      const uint32_t match = __ballot_sync(0xffffffffu, here);
+      if (match) return (long long)d * sh.A + r + __ffs(match) - 1;
+    }
+    return -1ll;
+  };
+  if (hi - lo > 32) {
+    const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, probe < hi && assist[(long long)probe * 3 + 1] <= t);
+    const int at = lo + max(0, __popc(below) - 1) * step;
+    const long long r = look(at, min(hi, at + step));
+    if (r >= 0) return r;
+  }
+  return look(lo, hi);
+}
+
+// The rows of a token's picks into s_row[K], by all warps of the block; ends with a barrier.
+__device__ __forceinline__ void find_rows(const CombineParams& p, size_t tau, long long* s_row) {
+  const Shape& sh = p.sh;
+  for (int k = threadIdx.x >> 5; k < sh.K; k += blockDim.x >> 5) {
+    const int c = classify_pick(p.ids, p.mask, sh, tau, k);
+    const long long r = c >= 0 ? find_row(p, (int)(tau / sh.bs), (int)(tau % sh.bs), k, c) : -1;
+    if ((threadIdx.x & 31) == 0) s_row[k] = r;
+  }
+  __syncthreads();
+}
+
+// BYTES: what a load takes of a row, 16, 8, 4 or 2 as rows align (RowUnit). SEARCH: without a row map.
+template <int DT, int BYTES, bool SEARCH>
+__global__ void __launch_bounds__(kGradThreads, BYTES == 16 ? 4 : 3) combine_grad_kernel(CombineGradParams p, int active) {
   __shared__ const uint8_t* s_src[32];
   __shared__ uint8_t* s_dst[32];
   __shared__ float s_w[32];
@@ -33,7 +133,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
   const Shape sh = p.sh;
   // the threads that go through the row: with a map or without, sums have one order
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = active >> 5;
-  const size_t begin = (int)threadIdx.x < active ? threadIdx.x : (size_t)1 << 32;
+  const uint32_t begin = (int)threadIdx.x < active ? threadIdx.x * BYTES : 0x7fffffffu;  // rows are 2^30 bytes at most
   const size_t tau = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
@@ -108,47 +208,37 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
   const size_t row0 = tau * (size_t)sh.row_in;
   const uint8_t* g_row = static_cast<const uint8_t*>(p.grad_out) + row0;
   const bool dots = p.grad_scales != nullptr;
-  constexpr int kStep = VEC ? 16 : 2;  // bytes a thread takes at a time
+  using Unit = RowUnit<BYTES>;
+  const uint32_t apart = active * BYTES;  // a unit's pieces
   for (int j0 = blockIdx.y * kGradBatch; j0 < n; j0 += gridDim.y * kGradBatch) {
     const int here = min(kGradBatch, n - j0);
     float acc[kGradBatch];
 #pragma unroll
     for (int j = 0; j < kGradBatch; ++j) acc[j] = 0.f;
-    for (size_t off = begin * kStep; off < (size_t)sh.row_in; off += (size_t)active * kStep) {
-      if constexpr (VEC) {
-        int4 y[kGradBatch];
-        const int4 gv = ld_nc_v4(g_row + off);
+    for (uint32_t off = begin; off < (uint32_t)sh.row_in; off += apart * Unit::kPieces) {
+      int4 y[kGradBatch];
+      const int4 gv = Unit::load(g_row, off, apart, sh.row_in);
 #pragma unroll
-        for (int j = 0; j < kGradBatch; ++j)
-          if (dots && j < here) y[j] = ld_nc_v4(s_src[j0 + j] + off);
-        float g[8];
-        Vec<DT>::unpack(g, gv);
+      for (int j = 0; j < kGradBatch; ++j)
+        if (dots && j < here) y[j] = Unit::load(s_src[j0 + j], off, apart, sh.row_in);
+      float g[8];
+      Vec<DT>::unpack(g, gv);
 #pragma unroll
-        for (int j = 0; j < kGradBatch; ++j) {
-          if (j >= here) break;
-          uint8_t* dst = s_dst[j0 + j];
-          if (dst) {
-            const float w = s_w[j0 + j];
-            float o[8];
+      for (int j = 0; j < kGradBatch; ++j) {
+        if (j >= here) break;
+        uint8_t* dst = s_dst[j0 + j];
+        if (dst) {
+          const float w = s_w[j0 + j];
+          float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __fmul_rn(w, g[i]);
-            __stcs(reinterpret_cast<int4*>(dst + off), Vec<DT>::pack(o));
-          }
-          if (dots) {
-            float f[8];
-            Vec<DT>::unpack(f, y[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[j] = __fmaf_rn(g[i], f[i], acc[j]);
-          }
+          for (int i = 0; i < 8; ++i) o[i] = __fmul_rn(w, g[i]);
+          Unit::store(dst, off, apart, sh.row_in, Vec<DT>::pack(o));
         }
-      } else {
-        const float g = elem_to_float<DT>(*reinterpret_cast<const uint16_t*>(g_row + off));
+        if (dots) {
+          float f[8];
+          Vec<DT>::unpack(f, y[j]);
 #pragma unroll
-        for (int j = 0; j < kGradBatch; ++j) {
-          if (j >= here) break;
-          uint8_t* dst = s_dst[j0 + j];
-          if (dst) *reinterpret_cast<uint16_t*>(dst + off) = float_to_elem<DT>(__fmul_rn(s_w[j0 + j], g));
-          if (dots) acc[j] = __fmaf_rn(g, elem_to_float<DT>(*reinterpret_cast<const uint16_t*>(s_src[j0 + j] + off)), acc[j]);
+          for (int i = 0; i < 8; ++i) acc[j] = __fmaf_rn(g[i], f[i], acc[j]);
         }
       }
     }
@@ -175,22 +265,16 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
     const float w = s_copy;
     const bool some = s_copies;  // without one grad_out is not read: zeros, whatever it holds
     uint8_t* out = static_cast<uint8_t*>(p.grad_x) + row0;
-    for (size_t off = begin * kStep; off < (size_t)sh.row_in; off += (size_t)active * kStep) {
-      if constexpr (VEC) {
-        float g[8];
-        if (some) {
-          Vec<DT>::unpack(g, ld_nc_v4(g_row + off));
+    for (uint32_t off = begin; off < (uint32_t)sh.row_in; off += apart * Unit::kPieces) {
+      float g[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(w, g[i]);
-        } else {
+      for (int i = 0; i < 8; ++i) g[i] = 0.f;
+      if (some) {
+        Vec<DT>::unpack(g, Unit::load(g_row, off, apart, sh.row_in));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = 0.f;
-        }
-        st_v4(out + off, Vec<DT>::pack(g));
-      } else {
-        const float g = some ? __fmul_rn(w, elem_to_float<DT>(*reinterpret_cast<const uint16_t*>(g_row + off))) : 0.f;
-        *reinterpret_cast<uint16_t*>(out + off) = float_to_elem<DT>(g);
+        for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(w, g[i]);
       }
+      Unit::store(out, off, apart, sh.row_in, Vec<DT>::pack(g));
     }
   }
 
@@ -201,7 +285,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) combine_grad_kernel(CombineGr
 }
 
 // Dispatch's gradient where a batch is too small for a row map to pay: a block has one token, as above.
-template <int DT, bool VEC>
+template <int DT, int BYTES>
 __global__ void __launch_bounds__(kGradThreads) dispatch_grad_token_kernel(DispatchGradParams p) {
   __shared__ const uint8_t* s_src[32];
   __shared__ long long s_row[32];
@@ -233,35 +317,32 @@ __global__ void __launch_bounds__(kGradThreads) dispatch_grad_token_kernel(Dispa
   const size_t row0 = tau * (size_t)sh.row_in;
   const uint8_t* residual = p.residual ? static_cast<const uint8_t*>(p.residual) + row0 : nullptr;
   uint8_t* out = static_cast<uint8_t*>(p.x_out) + row0;
-  constexpr int kStep = VEC ? 16 : 2;
-  for (size_t off = (size_t)threadIdx.x * kStep; off < (size_t)sh.row_in; off += (size_t)blockDim.x * kStep) {
-    if constexpr (VEC) {
-      float acc[8];
+  using Unit = RowUnit<BYTES>;
+  const uint32_t apart = blockDim.x * BYTES;
+  for (uint32_t off = threadIdx.x * BYTES; off < (uint32_t)sh.row_in; off += apart * Unit::kPieces) {
+    float acc[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-      // an ordinary load: the residual may be what this thread then writes
-      if (residual) Vec<DT>::fma(acc, 1.f, ld_v4(residual + off));
-      for (int j0 = 0; j0 < n; j0 += kGradBatch) {
-        int4 y[kGradBatch];
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    if (residual) Vec<DT>::fma(acc, 1.f, Unit::load_own(residual, off, apart, sh.row_in));
+    for (int j0 = 0; j0 < n; j0 += kGradBatch) {
+      int4 y[kGradBatch];
 #pragma unroll
-        for (int j = 0; j < kGradBatch; ++j)
-          if (j0 + j < n) y[j] = ld_nc_v4(s_src[j0 + j] + off);
+      for (int j = 0; j < kGradBatch; ++j)
+        if (j0 + j < n) y[j] = Unit::load(s_src[j0 + j], off, apart, sh.row_in);
 #pragma unroll
-        for (int j = 0; j < kGradBatch; ++j)
-          if (j0 + j < n) Vec<DT>::fma(acc, 1.f, y[j]);
-      }
-      st_v4(out + off, Vec<DT>::pack(acc));
-    } else {
-      float acc = residual ? elem_to_float<DT>(*reinterpret_cast<const uint16_t*>(residual + off)) : 0.f;
-      for (int j = 0; j < n; ++j) acc += elem_to_float<DT>(*reinterpret_cast<const uint16_t*>(s_src[j] + off));
-      *reinterpret_cast<uint16_t*>(out + off) = float_to_elem<DT>(acc);
+      for (int j = 0; j < kGradBatch; ++j)
+        if (j0 + j < n) Vec<DT>::fma(acc, 1.f, y[j]);
     }
+    Unit::store(out, off, apart, sh.row_in, Vec<DT>::pack(acc));
   }
 }
 
+// The widest pieces that rows, which lie one after the other, align for.
+static int row_piece(const Shape& sh) { return sh.row_in % 16 == 0 ? 16 : sh.row_in % 8 == 0 ? 8 : sh.row_in % 4 == 0 ? 4 : 2; }
+
 // As few threads as go through a row in as many steps as 256 would; where rows are looked for, a warp for each pick.
 static int grad_threads(const Shape& sh, bool search) {
-  const int items = sh.row_in % 16 == 0 ? sh.row_in / 16 : sh.h;
+  const int items = (sh.row_in + 15) / 16;
   const int steps = (items + kGradThreads - 1) / kGradThreads;
   const int threads = ((items + steps - 1) / steps + 31) / 32 * 32, picks = 32 * (sh.K < 8 ? sh.K : 8);
   return search && threads < picks ? picks : threads;
@@ -274,11 +355,15 @@ static cudaError_t launch_grad(const CombineGradParams& p, cudaStream_t st, int 
   if (n_tok == 0) return cudaSuccess;
   const int batches = (sh.K + kGradBatch - 1) / kGradBatch, active = grad_threads(sh, false);
   PdlLaunch L(dim3((unsigned)n_tok, (unsigned)(n_tok < num_sms * 4LL ? batches : 1)), dim3(grad_threads(sh, SEARCH)), 0, st);
-  if (sh.row_in % 16 == 0)
-    return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_F16, true, SEARCH>, p, active)
-                                 : cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_BF16, true, SEARCH>, p, active);
-  return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_F16, false, SEARCH>, p, active)
-                               : cudaLaunchKernelEx(&L.cfg, combine_grad_kernel<MOE_BF16, false, SEARCH>, p, active);
+  const auto launch = [&](auto f16, auto bf16) {
+    return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, f16, p, active) : cudaLaunchKernelEx(&L.cfg, bf16, p, active);
+  };
+  switch (row_piece(sh)) {
+    case 16: return launch(combine_grad_kernel<MOE_F16, 16, SEARCH>, combine_grad_kernel<MOE_BF16, 16, SEARCH>);
+    case 8: return launch(combine_grad_kernel<MOE_F16, 8, SEARCH>, combine_grad_kernel<MOE_BF16, 8, SEARCH>);
+    case 4: return launch(combine_grad_kernel<MOE_F16, 4, SEARCH>, combine_grad_kernel<MOE_BF16, 4, SEARCH>);
+    default: return launch(combine_grad_kernel<MOE_F16, 2, SEARCH>, combine_grad_kernel<MOE_BF16, 2, SEARCH>);
+  }
 }
 
 cudaError_t launch_combine_grad(const CombineGradParams& p, bool search, cudaStream_t st, int num_sms) {
@@ -286,14 +371,18 @@ cudaError_t launch_combine_grad(const CombineGradParams& p, bool search, cudaStr
 }
 
 cudaError_t launch_dispatch_grad(const DispatchGradParams& p, bool search, cudaStream_t st, int num_sms) {
-  if (!search) return launch_dispatch_grad_reduce(p, st, num_sms);
   const Shape& sh = p.sh;
+  if (!search && sh.row_in % 16 == 0) return launch_dispatch_grad_reduce(p, st, num_sms);
   PdlLaunch L(dim3((unsigned)(sh.W * sh.bs)), dim3(grad_threads(sh, true)), 0, st);
-  if (sh.row_in % 16 == 0)
-    return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, dispatch_grad_token_kernel<MOE_F16, true>, p)
-                                 : cudaLaunchKernelEx(&L.cfg, dispatch_grad_token_kernel<MOE_BF16, true>, p);
-  return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, dispatch_grad_token_kernel<MOE_F16, false>, p)
-                               : cudaLaunchKernelEx(&L.cfg, dispatch_grad_token_kernel<MOE_BF16, false>, p);
+  const auto launch = [&](auto f16, auto bf16) {
+    return sh.x_dtype == MOE_F16 ? cudaLaunchKernelEx(&L.cfg, f16, p) : cudaLaunchKernelEx(&L.cfg, bf16, p);
+  };
+  switch (row_piece(sh)) {
+    case 16: return launch(dispatch_grad_token_kernel<MOE_F16, 16>, dispatch_grad_token_kernel<MOE_BF16, 16>);
+    case 8: return launch(dispatch_grad_token_kernel<MOE_F16, 8>, dispatch_grad_token_kernel<MOE_BF16, 8>);
+    case 4: return launch(dispatch_grad_token_kernel<MOE_F16, 4>, dispatch_grad_token_kernel<MOE_BF16, 4>);
+    default: return launch(dispatch_grad_token_kernel<MOE_F16, 2>, dispatch_grad_token_kernel<MOE_BF16, 2>);
+  }
 }
 
 }  // namespace crs

@@ -29,7 +29,7 @@
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "quant_common.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_pair.cuh"
 
 namespace crs {
 

@@ -4,9 +4,9 @@
 //
 // One pass over the data, bound by HBM: a row stays in registers between its maximum
 // and its codes, in a warp's where it has up to 2048 elements, in a block's up to
-// 16384; as the codes of its elements are made, the next row's take their registers. Rows
-// that 16-byte loads do not fit, and longer ones, are read twice, an
-// element at a time, the second time from cache.
+// 16384; as the codes of its elements are made, the next row's take their registers.
+// Rows go in pieces of 8 elements (16-byte loads), 2 or 1, as they align. Longer rows are
+// read twice, the second time from cache.
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "quant_common.cuh"
@@ -71,19 +71,52 @@ struct Int8Rows {
   }
 };
 
-// 8 elements as loaded, and as fp32 pairs.
-template <int DT>
+// 8 elements of a row as loaded, and as fp32 pairs: PIECE neighbours (8, 2 or 1, as the rows align) at a time, unit j's
+// pieces THREADS * PIECE elements apart; zeros beyond the row's end.
+template <int DT, int PIECE, int THREADS>
 struct Int8Unit {
-  static constexpr int kLoads = DT == MOE_F32 ? 2 : 1;
+  static constexpr int kLoads = DT == MOE_F32 ? 2 : 1, kPieces = 8 / PIECE;
   int4 v[kLoads];
-  __device__ void load(const void* x, size_t at) {
+  static __device__ int element(int t, int j, int piece) { return ((j * kPieces + piece) * THREADS + t) * PIECE; }
+  // `row` begins at the row's first element
+  __device__ void load(const uint8_t* row, int t, int j, int cols) {
+    if constexpr (PIECE == 8) {
+      const int c = element(t, j, 0);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      v[i] = ld_nc_v4(static_cast<const uint8_t*>(x) + at * (DT == MOE_F32 ? 4 : 2) + i * 16);
+      for (int i = 0; i < kLoads; ++i)
+        v[i] = c < cols ? ld_nc_v4(row + (size_t)c * (DT == MOE_F32 ? 4 : 2) + i * 16) : make_int4(0, 0, 0, 0);
+    } else {
+      uint32_t w[4 * kLoads];
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const int c = element(t, j, q);
+        if constexpr (DT == MOE_F32 && PIECE == 2) {
+          const float2 f = c < cols ? __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(row) + c)) : float2{0.f, 0.f};
+          w[2 * q] = __float_as_uint(f.x), w[2 * q + 1] = __float_as_uint(f.y);
+        } else if constexpr (DT == MOE_F32) {
+          w[q] = c < cols ? __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + c)) : 0u;
+        } else if constexpr (PIECE == 2) {
+          w[q] = c < cols ? __ldg(reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(row) + c)) : 0u;
+        } else {
+          const uint32_t h = c < cols ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row) + c) : 0u;
+          if (q & 1) w[q / 2] |= h << 16;
+          else w[q / 2] = h;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) v[i] = make_int4((int)w[4 * i], (int)w[4 * i + 1], (int)w[4 * i + 2], (int)w[4 * i + 3]);
+    }
   }
-  __device__ void zero() {
+  static __device__ void store(int8_t* out, int t, int j, int cols, uint2 codes) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) v[i] = make_int4(0, 0, 0, 0);
+    for (int q = 0; q < kPieces; ++q) {
+      const int c = element(t, j, q);
+      if (c >= cols) break;
+      if constexpr (PIECE == 8) *reinterpret_cast<uint2*>(out + c) = codes;
+      else if constexpr (PIECE == 2)
+        *reinterpret_cast<uint16_t*>(out + c) = (uint16_t)((q < 2 ? codes.x : codes.y) >> (16 * (q & 1)));
+      else out[c] = (int8_t)((q < 4 ? codes.x : codes.y) >> (8 * (q & 3)));
+    }
   }
   // The largest magnitude: of 16-bit elements pair by pair, in their own type.
   __device__ float amax(float m) const {
@@ -162,29 +195,27 @@ __device__ __forceinline__ uint2 int8_codes(const f32x2 (&v)[4], f32x2 scale2, f
   return pack8_low(c);
 }
 
-// cols a multiple of 8 that a warp's (BLOCK: the block's) threads hold as NV units each,
-// rows of x 16-byte aligned, codes 8-byte aligned.
-template <int DT, int NV, bool BLOCK>
-__global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 8 ? 2 : 4) int8_quantize_vec_kernel(Int8QuantParams p) {
+// Rows that a warp's (BLOCK: the block's) threads hold as NV units each; x, its strides, cols and codes
+// aligned for pieces of PIECE elements (with 8: 16 bytes of x).
+template <int DT, int PIECE, int NV, bool BLOCK>
+__global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 8 ? 2 : 4) int8_quantize_kernel(Int8QuantParams p) {
   __shared__ int s_pre[kInt8CountedMats + 1];
   __shared__ float s_max[kInt8Threads / 32];
   pdl_wait();
   pdl_launch_dependents();
   constexpr int kThreads = BLOCK ? kInt8Threads : 32;
   const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
-  const int units = p.cols >> 3;
+  const uint8_t* x = static_cast<const uint8_t*>(p.x);
+  constexpr size_t kEs = DT == MOE_F32 ? 4 : 2;
   Int8Rows rows(p, s_pre);
   const long long first = BLOCK ? blockIdx.x : blockIdx.x * (kInt8Threads / 32ll) + (threadIdx.x >> 5);
   const long long step = BLOCK ? gridDim.x : gridDim.x * (kInt8Threads / 32ll);
   if (first >= rows.total) return;
   size_t place;
   size_t from = rows.find(first, place);
-  Int8Unit<DT> u[NV];
+  Int8Unit<DT, PIECE, kThreads> u[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (t + j * kThreads < units) u[j].load(p.x, from + (size_t)(t + j * kThreads) * 8);
-    else u[j].zero();
-  }
+  for (int j = 0; j < NV; ++j) u[j].load(x + from * kEs, t, j, p.cols);
   for (long long i = first; i < rows.total; i += step) {
     float m = 0.f;
 #pragma unroll
@@ -206,44 +237,40 @@ __global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 
     if (more) from = rows.find(i + step, place);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (t + j * kThreads >= units) break;
+      if (u[j].element(t, j, 0) >= p.cols) break;
       f32x2 v[4];
       u[j].pairs(v);
-      if (more) u[j].load(p.x, from + (size_t)(t + j * kThreads) * 8);  // of the next row, under way while this one's codes are made
-      if (fast) *reinterpret_cast<uint2*>(out + (size_t)(t + j * kThreads) * 8) = int8_codes(v, scale2, rcp2);
+      if (more) u[j].load(x + from * kEs, t, j, p.cols);  // of the next row, under way while this one's codes are made
+      if (fast) u[j].store(out, t, j, p.cols, int8_codes(v, scale2, rcp2));
     }
   }
 }
 
-// Any columns and alignment: a warp or (BLOCK) a block a row, read twice.
-template <int DT, bool BLOCK>
-__global__ void __launch_bounds__(kInt8Threads) int8_quantize_plain_kernel(Int8QuantParams p) {
+// Rows that a block's registers do not hold: read twice, an element at a time, the second time from cache.
+template <int DT>
+__global__ void __launch_bounds__(kInt8Threads) int8_quantize_long_kernel(Int8QuantParams p) {
   __shared__ int s_pre[kInt8CountedMats + 1];
   __shared__ float s_max[kInt8Threads / 32];
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kThreads = BLOCK ? kInt8Threads : 32;
-  const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
   Int8Rows rows(p, s_pre);
-  const long long first = BLOCK ? blockIdx.x : blockIdx.x * (kInt8Threads / 32ll) + (threadIdx.x >> 5);
-  const long long step = BLOCK ? gridDim.x : gridDim.x * (kInt8Threads / 32ll);
-  for (long long i = first; i < rows.total; i += step) {
+  for (long long i = blockIdx.x; i < rows.total; i += gridDim.x) {
     size_t place;
     const size_t from = rows.find(i, place);
     float m = 0.f;
 #pragma unroll 8
-    for (int c = t; c < p.cols; c += kThreads) m = fmaxf(m, fabsf(int8_load<DT>(p.x, from + c)));
-    m = int8_amax<BLOCK>(m, s_max);
+    for (int c = threadIdx.x; c < p.cols; c += kInt8Threads) m = fmaxf(m, fabsf(int8_load<DT>(p.x, from + c)));
+    m = int8_amax<true>(m, s_max);
     const float scale = __fdiv_rn(m, 127.0f);
     const bool fast = token_rcp_ok(scale);
     const float rcp = fast ? __frcp_rn(scale) : 0.f;
     int8_t* out = p.codes + place * p.cols;
 #pragma unroll 8
-    for (int c = t; c < p.cols; c += kThreads) {
+    for (int c = threadIdx.x; c < p.cols; c += kInt8Threads) {
       const float v = int8_load<DT>(p.x, from + c);
       out[c] = (int8_t)(fast ? token_code(v, scale, rcp) : m == 0.f ? 0u : (uint32_t)token_q(v, scale));
     }
-    if (t == 0) p.scales[place] = scale;
+    if (threadIdx.x == 0) p.scales[place] = scale;
   }
 }
 
@@ -252,17 +279,20 @@ struct Int8QuantKernel {
   bool block;
 };
 
-// Where rows align for 16-byte loads, the narrowest group of threads that holds one.
+// The narrowest group of threads that holds a row.
+template <int DT, int PIECE>
+Int8QuantKernel int8_quant_kernel(int cols) {
+  if (cols <= 256) return {int8_quantize_kernel<DT, PIECE, 1, false>, false};
+  if (cols <= 512) return {int8_quantize_kernel<DT, PIECE, 2, false>, false};
+  if (cols <= 1024) return {int8_quantize_kernel<DT, PIECE, 4, false>, false};
+  if (cols <= 2048) return {int8_quantize_kernel<DT, PIECE, 8, false>, false};
+  if (cols <= 8192) return {int8_quantize_kernel<DT, PIECE, 4, true>, true};
+  if (cols <= 16384) return {int8_quantize_kernel<DT, PIECE, 8, true>, true};
+  return {int8_quantize_long_kernel<DT>, true};
+}
 template <int DT>
-Int8QuantKernel int8_quant_kernel(int cols, bool vec) {
-  if (vec && cols <= 256) return {int8_quantize_vec_kernel<DT, 1, false>, false};
-  if (vec && cols <= 512) return {int8_quantize_vec_kernel<DT, 2, false>, false};
-  if (vec && cols <= 1024) return {int8_quantize_vec_kernel<DT, 4, false>, false};
-  if (vec && cols <= 2048) return {int8_quantize_vec_kernel<DT, 8, false>, false};
-  if (vec && cols <= 8192) return {int8_quantize_vec_kernel<DT, 4, true>, true};
-  if (vec && cols <= 16384) return {int8_quantize_vec_kernel<DT, 8, true>, true};
-  if (cols <= 1024) return {int8_quantize_plain_kernel<DT, false>, false};
-  return {int8_quantize_plain_kernel<DT, true>, true};
+Int8QuantKernel int8_quant_kernel(int cols, int piece) {
+  return piece == 8 ? int8_quant_kernel<DT, 8>(cols) : piece == 2 ? int8_quant_kernel<DT, 2>(cols) : int8_quant_kernel<DT, 1>(cols);
 }
 
 }  // namespace crs
@@ -282,11 +312,14 @@ extern "C" moe_status_t moe_int8_quantize(const void* x, int32_t x_dtype, int32_
   const int nsm = num_sms_of_current_device();
   if (nsm <= 0) return MOE_ERR_CUDA;
   const Int8QuantParams p{x, counts, codes, scales, rows, row_stride, mat_stride, mats, cols, counts_len};
-  const bool vec = cols % 8 == 0 && (uintptr_t)x % 16 == 0 && (mats * rows == 1 || row_stride * es % 16 == 0) &&
-                   (mats == 1 || mat_stride * es % 16 == 0) && (uintptr_t)codes % 8 == 0;
-  const Int8QuantKernel k = x_dtype == MOE_F32   ? int8_quant_kernel<MOE_F32>(cols, vec)
-                            : x_dtype == MOE_F16 ? int8_quant_kernel<MOE_F16>(cols, vec)
-                                                 : int8_quant_kernel<MOE_BF16>(cols, vec);
+  const auto fits = [&](int piece, unsigned bytes) {  // of x that a piece's load takes
+    return cols % piece == 0 && (uintptr_t)x % bytes == 0 && (mats * rows == 1 || row_stride * es % bytes == 0) &&
+           (mats == 1 || mat_stride * es % bytes == 0) && (uintptr_t)codes % piece == 0;
+  };
+  const int piece = fits(8, 16) ? 8 : fits(2, 2 * es) ? 2 : 1;
+  const Int8QuantKernel k = x_dtype == MOE_F32   ? int8_quant_kernel<MOE_F32>(cols, piece)
+                            : x_dtype == MOE_F16 ? int8_quant_kernel<MOE_F16>(cols, piece)
+                                                 : int8_quant_kernel<MOE_BF16>(cols, piece);
   int per_sm = 0;
   if (resident_blocks((const void*)k.kernel, kInt8Threads, 0, &per_sm) != cudaSuccess || per_sm < 1) return MOE_ERR_CUDA;
   const long long need = k.block ? mats * rows : (mats * rows + kInt8Threads / 32 - 1) / (kInt8Threads / 32);

@@ -10,6 +10,7 @@
 
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
+#include "gradients.h"
 #include "internal.h"
 
 namespace crs {
@@ -770,8 +771,9 @@ moe_status_t moe_dispatch_backward(const moe_config_t* cfg, const void* grad_exp
   // A block a token that looks for its rows, or the map and the combine's reduce, whose warps need no barrier: the first
   // for small batches and long rows (512 tokens of hidden 2048 6.4 and 8.4 us, 4096 of 7168 86 and 89), the second for
   // many tokens of short ones (2048 of 2048 16.5 and 17.9, 4096 of 2048 29.8 and 31.5; nothing between 4 and 14 KB was
-  // measured).
-  const bool search = p.sh.row_in >= 8192 || (long long)p.sh.W * p.sh.bs * p.sh.K <= 8192;
+  // measured). Rows that do not align to 16 bytes, which the reduce would take an element at a time (2048 tokens of
+  // hidden 2047 53 us, 48 in pieces of 2 bytes, 24 of 2044 in pieces of 8), go the first way, with a map too.
+  const bool search = p.sh.row_in >= 8192 || p.sh.row_in % 16 || (long long)p.sh.W * p.sh.bs * p.sh.K <= 8192;
   return run_grad(cfg, p, search, ws, static_cast<cudaStream_t>(stream), launch_dispatch_grad);
 }
 

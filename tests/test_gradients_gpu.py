@@ -167,6 +167,10 @@ CASES = [
     (2, 2, 2, 4, 16400, 0, 1, 0, "f16"),
     (2, 3, 17, 24, 300, 0, 1, 0, "bf16"),
     (2, 400, 3, 4, 24, 0, 1, 2, "f16"),
+    (2, 3, 4, 8, 2044, 0, 1, 0, "bf16"),
+    (2, 3, 4, 8, 2046, 1, 0, 2, "f16"),
+    (2, 3, 9, 16, 2047, 0, 1, 2, "bf16"),
+    (2, 2, 2, 4, 9001, 0, 1, 0, "f16"),
 ]
 ids_of = lambda c: "-".join(map(str, c))  # noqa: E731
 
