@@ -14,9 +14,8 @@
 //   * four bytes become two fp16 pairs, bytes 0 and 2 and bytes 1 and 3 (widen4). The order of K
 //     that this gives is the same for both operands;
 //   * copies bring 128 elements of K a stage; four sets of four warps widen them in turn, a stage
-//     each, into four or six slots of TMEM and shared memory. Two accumulators of more than
-//     128 columns leave TMEM for two such slots: then a slot is half a stage, and so is a
-//     set's turn;
+//     each, into a slot of TMEM and shared memory that each has. Two accumulators of more than
+//     128 columns leave TMEM for half as much: then a slot is half a stage, and so is a set's turn;
 //   * warps: 0 TMA, 1 MMA (of the pair's first CTA), 2..17 widen, 18..21 epilogue. Two accumulators, so
 //     that the next unit's MMAs run while this one is read.
 #include <cuda.h>
@@ -44,7 +43,7 @@ struct Int8ProductParams {
   long long A;
   int* status;
   uint64_t timeout_ns;
-  uint8_t raw_stages[6][2];  // of the copies' ring, for row tiles of 32, 64, .. and 2 x 64 and 2 x 128 weight rows a unit
+  uint8_t raw_stages[6];  // of the copies' ring, for row tiles of 32, 64, ..
 };
 
 // SwiGLU of a gate and what it gates. exp and the reciprocal are the fast ones, within a few ulps (exp: plus
@@ -145,17 +144,17 @@ __device__ __forceinline__ uint16_t int8_round(float v) {
 
 // ------------------------------------------------------------- the tensor cores
 
-// Boxes of 16, 32, .. rows of x and of 64 and 128 rows of w, 128 elements of K: one copy of each a stage.
+// Boxes of 16, 32, .. rows of x and of 128 rows of w, 128 elements of K: one copy of each a stage.
 struct Int8Maps {
-  CUtensorMap x[6], w[2];
+  CUtensorMap x[6], w;
 };
 
 constexpr int kWidenWarp = 2, kSets = 4, kSetWarps = 4;
 constexpr int kInt8ProductThreads = 22 * 32, kInt8PlanThreads = 8 * 32;
 constexpr int kInt8Stage = 128;    // elements of K a stage
+constexpr int kInt8Half = 128, kInt8Width = 2 * kInt8Half;  // weight rows of a unit in each CTA, and in both
 constexpr int kInt8MostRows = 192; // MMA N
 constexpr int kInt8RawStages = 8;  // at most
-constexpr int kInt8Slots = 6;      // at most
 // An epilogue warp turns 32 rows x 32 results of 2 bytes around in shared memory, rows 80 bytes apart.
 constexpr uint32_t kInt8TurnRow = 80, kInt8TurnWarp = 32 * kInt8TurnRow;
 constexpr size_t kInt8ProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers and 1 KB of alignment aside
@@ -164,11 +163,11 @@ constexpr size_t kInt8ProductSmem = 227 * 1024 - 1024;  // dynamic; the barriers
 __host__ __device__ constexpr uint32_t int8_fixed_smem(int E) {
   return 4 * (kInt8TurnWarp + kInt8MostRows * 4) + ((3u * E + 1) * 4 + 127) / 128 * 128;
 }
-// Halves of a stage in a slot (32 columns of TMEM each), and slots beside two accumulators of `tile` columns.
+// Halves of a stage in a set's slot, 32 columns of TMEM each, beside two accumulators of `tile` columns. (With half a
+// stage a slot everywhere 4096 rows of 128 experts, 2048 -> 1024, took 56.7 us where whole stages take 50.4: twice the
+// hand-overs. Six slots where TMEM holds them were no faster than four.)
 __host__ __device__ constexpr int int8_halves(int tile) { return tile > 128 ? 1 : 2; }
-__host__ __device__ constexpr uint32_t int8_slots(int tile) { return tile > 64 ? 4 : 6; }
-static_assert(2 * 192 + int8_slots(192) * 32 * int8_halves(192) <= 512 && 2 * 128 + int8_slots(128) * 32 * int8_halves(128) <= 512 &&
-                  2 * 64 + int8_slots(64) * 32 * int8_halves(64) <= 512, "TMEM");
+static_assert(2 * 192 + kSets * 32 * int8_halves(192) <= 512 && 2 * 128 + kSets * 32 * int8_halves(128) <= 512, "TMEM");
 static_assert(kInt8MostRows == 192, "six boxes of x");
 
 struct Int8Wait {
@@ -274,7 +273,7 @@ struct Int8Cursor {
 };
 
 // Its expert and rows.
-__device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int width, int tile) {
+__device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const int* pre, const Int8Cursor& at, int tile) {
   // found by a whole warp: among every (E/32)th expert, then among those between
   const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
   const int far = lane * step;
@@ -284,43 +283,17 @@ __device__ __forceinline__ Int8Unit int8_unit(const Int8ProductParams& p, const 
   const int* first = pre + p.E + 1;
   const int* count = first + p.E;
   const int before = (at.mt - pre[e]) * tile;
-  return {e, at.ni * width, min(tile, count[e] - before), first[e] + before};
+  return {e, at.ni * kInt8Width, min(tile, count[e] - before), first[e] + before};
 }
 
-// How a launch cuts its work: weight rows a unit (half of them for each CTA), and as many stages as shared memory holds.
-struct Int8Shape {
-  int tile, width, n_tiles, units;
-  uint32_t raw_stages;
-};
-
-__device__ __forceinline__ Int8Shape int8_shape(const Int8ProductParams& p, int tile, int m_tiles) {
-  Int8Shape s;
-  const int pairs = gridDim.x >> 1;
-  // 2 x 64 weight rows a unit where 2 x 128 would leave pairs without one
-  float best = 3e38f;
-  s.width = 256;
-#pragma unroll
-  for (int b = 2; b >= 1; --b) {
-    const float units = (float)m_tiles * (float)((p.N + 128 * b - 1) / (128 * b));
-    const float cost = ceilf(__fdividef(units, (float)pairs) - 0.001f) * (float)(max(356 * b, 128 * b + 3 * tile) + 64);
-    if (cost < best) {
-      best = cost;
-      s.width = 128 * b;
-    }
-  }
-  s.n_tiles = (p.N + s.width - 1) >> (s.width == 256 ? 8 : 7);
-  s.tile = tile;
-  s.units = m_tiles * s.n_tiles;
-  s.raw_stages = p.raw_stages[(tile >> 5) - 1][(s.width >> 7) - 1];
-  return s;
-}
-static uint8_t int8_raw_stages(int E, int tile, int width) {
-  const uint32_t room = (uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - int8_slots(tile) * int8_halves(tile) * tile * 64;
-  const uint32_t stages = room / ((uint32_t)(width + tile) * 64);
+// Stages of the copies' ring, as many as shared memory holds beside the sets' slots.
+static uint8_t int8_raw_stages(int E, int tile) {
+  const uint32_t room = (uint32_t)kInt8ProductSmem - 1024 - int8_fixed_smem(E) - kSets * int8_halves(tile) * tile * 64;
+  const uint32_t stages = room / ((uint32_t)(kInt8Width + tile) * 64);
   return (uint8_t)(stages < kInt8RawStages ? stages : kInt8RawStages);
 }
-static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - int8_slots(kInt8MostRows) * int8_halves(kInt8MostRows) * kInt8MostRows * 64) /
-                      ((256 + kInt8MostRows) * 64) >= 4, "four stages at least");
+static_assert((kInt8ProductSmem - 1024 - int8_fixed_smem(1024) - kSets * int8_halves(kInt8MostRows) * kInt8MostRows * 64) /
+                      ((kInt8Width + kInt8MostRows) * 64) >= 4, "four stages at least");
 
 // 32 neighbouring columns (rows c0 .. of the tile) of the accumulator by 32 weight rows (a lane each): scaled,
 // through the epilogue, turned around and stored. xs: where the rows' scales lie.
@@ -392,12 +365,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     int8_product_kernel(const __grid_constant__ Int8Maps maps, const __grid_constant__ Int8ProductParams p) {
   extern __shared__ __align__(1024) uint8_t psm_raw[];
   __shared__ __align__(8) uint64_t raw_full[kInt8RawStages], raw_empty[kInt8RawStages];
-  __shared__ __align__(8) uint64_t wide_full[kInt8Slots], wide_empty[kInt8Slots];  // full: of the first CTA, for both
+  __shared__ __align__(8) uint64_t wide_full[kSets], wide_empty[kSets];  // full: of the first CTA, for both
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drained;              // empty: of the first CTA, for both
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t s_warp[kInt8PlanThreads / 32 + 1];
   __shared__ int s_most;
-  __shared__ Int8Shape s_shape;
+  __shared__ int s_units;
   __shared__ volatile int s_abort;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -411,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       mbar_init(&raw_full[lane], 1);
       mbar_init(&raw_empty[lane], 2 * kSetWarps);  // two sets once, or one twice
     }
-    if (lane < kInt8Slots) {
+    if (lane < kSets) {
       mbar_init(&wide_full[lane], 2 * kSetWarps);  // a set's warps in each CTA
       mbar_init(&wide_empty[lane], 1);
     }
@@ -436,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     const int tile = min(kInt8MostRows, max(32, (s_most + 31) >> 5 << 5));
     // overlapping experts can have more row tiles than the units' numbers hold: then none is worked on
     const bool countable = int8_row_tiles<kInt8PlanThreads>(p, tile, pre, s_warp);
-    if (threadIdx.x == 0) s_shape = int8_shape(p, tile, countable ? pre[p.E] : 0);
+    if (threadIdx.x == 0) s_units = countable ? pre[p.E] * ((p.N + kInt8Width - 1) / kInt8Width) : 0;
   } else if (warp == kInt8PlanThreads / 32) {
     tmem_alloc_pair(&tmem_slot, 512);
     tmem_relinquish_pair();
@@ -445,15 +418,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  const int tile = __shfl_sync(0xffffffffu, s_shape.tile, 0), KB = (p.K + kInt8Stage - 1) / kInt8Stage;
-  const int width = __shfl_sync(0xffffffffu, s_shape.width, 0), n_tiles = __shfl_sync(0xffffffffu, s_shape.n_tiles, 0);
-  const int units = __shfl_sync(0xffffffffu, s_shape.units, 0);
-  const uint32_t raw_stages = __shfl_sync(0xffffffffu, s_shape.raw_stages, 0), raw_bytes = (uint32_t)(width + tile) * 64;
-  const int half = width >> 1;  // this CTA's weight rows of a unit
+  const int tile = min(kInt8MostRows, max(32, (__shfl_sync(0xffffffffu, s_most, 0) + 31) >> 5 << 5));
+  const int KB = (p.K + kInt8Stage - 1) / kInt8Stage, n_tiles = (p.N + kInt8Width - 1) / kInt8Width;
+  const int units = __shfl_sync(0xffffffffu, s_units, 0);
+  const uint32_t raw_stages = p.raw_stages[(tile >> 5) - 1], raw_bytes = (uint32_t)(kInt8Width + tile) * 64;
   const int halves = int8_halves(tile);
-  const uint32_t panel = tile * 64, slot_bytes = panel * halves, slot_cols = 32 * halves, slots = int8_slots(tile);
+  const uint32_t panel = tile * 64, slot_bytes = panel * halves, slot_cols = 32 * halves;
   // shared memory: the widened rows, then the copies' ring; tensor memory: two accumulators, then the widened weights
-  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + slots * slot_bytes, tmem_a = tmem + 2 * tile;
+  const uint32_t sm0 = smem_u32(sm), raw0 = sm0 + kSets * slot_bytes, tmem_a = tmem + 2 * tile;
   const uint32_t raw_full0 = smem_u32(raw_full), raw_empty0 = smem_u32(raw_empty);
   const uint32_t wide_full0 = smem_u32(wide_full), wide_empty0 = smem_u32(wide_empty);
   const Int8Wait ab{&s_abort, p.status, p.timeout_ns};
@@ -462,24 +434,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   // A unit's copies and its MMAs are one thread's each. (With a whole warp going along, the MMA predicated for one
   // lane, each MMA took 60 clocks to issue: 32 is its time with 64 rows.)
   if (warp == 0) {
-    const CUtensorMap* w_map = &maps.w[(half >> 6) - 1];
     const bool leader = elect_one();
     uint32_t stage = 0, phase = 1;
     bool ok = true;
     for (Int8Cursor at(n_tiles); at.u < units && ok; at.next()) {
-      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const Int8Unit un = int8_unit(p, pre, at, tile);
       if (leader) {
         const int x_boxes = (un.rows + 31) / 32;  // of 16 rows, in each CTA
-        const int n0 = un.n0 + (int)rank * half, row = un.row0 + (int)rank * x_boxes * 16;
+        const int n0 = un.n0 + (int)rank * kInt8Half, row = un.row0 + (int)rank * x_boxes * 16;
         const CUtensorMap* x_map = &maps.x[x_boxes - 1];
-        const uint32_t bytes = (uint32_t)(half + x_boxes * 16) * 128u;
+        const uint32_t bytes = (uint32_t)(kInt8Half + x_boxes * 16) * 128u;
         for (int kb = 0; kb < KB; ++kb) {
           ok = int8_wait_one(raw_empty0 + stage * 8, phase, ab);
           if (!ok) break;
           const uint32_t st = raw0 + stage * raw_bytes, bar = raw_full0 + stage * 8;
           mbar_expect_tx_if(true, bar, bytes);
-          tma_load_3d_if(true, st, w_map, kb * kInt8Stage, n0, un.e, bar);
-          tma_load_2d_if(true, st + half * 128, x_map, kb * kInt8Stage, row, bar);
+          tma_load_3d_if(true, st, &maps.w, kb * kInt8Stage, n0, un.e, bar);
+          tma_load_2d_if(true, st + kInt8Half * 128, x_map, kb * kInt8Stage, row, bar);
           if (++stage == raw_stages) {
             stage = 0;
             phase ^= 1;
@@ -495,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       uint32_t slot = 0, phase = 0, done = 0;
       bool ok = true;
       for (Int8Cursor at(n_tiles); at.u < units && ok; at.next(), ++done) {
-        const Int8Unit un = int8_unit(p, pre, at, width, tile);
+        const Int8Unit un = int8_unit(p, pre, at, tile);
         if (leader) {
           const uint32_t idesc = idesc_f16_pair((un.rows + 31) / 32 * 32), buf = done & 1, acc = tmem + buf * tile;
           ok = int8_wait_one(smem_u32(&acc_empty[buf]), ((done >> 1) & 1) ^ 1, ab);
@@ -506,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
             tc_fence_after();
             const uint64_t bdesc = bdesc0 + slot * (slot_bytes >> 4);
             const uint32_t a = tmem_a + slot * slot_cols, here = slot;
-            if (++slot == slots) {
+            if (++slot == kSets) {
               slot = 0;
               phase ^= 1;
             }
@@ -532,34 +503,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     // of half a stage a thread has the 64 elements of a weight row, a warp 16 rows x 32 elements of x at a time
     const uint32_t mine = warp - kWidenWarp, set = mine / kSetWarps, w = mine % kSetWarps, q = warp & 3;
     const uint32_t swz = lane & 7;  // a row's place in its group of 8, which the copies' and the MMA's swizzle go by
-    const bool has_weights = (int)(q * 32) < half;
     const uint32_t first = halves == 2 ? 0 : set & 1;  // the first half that is this set's
     const uint32_t w_row = (q * 32 + lane) * 128 + ((first * 4 ^ swz) << 4);  // chunk c is 16 c away by exclusive or
     const uint32_t ta0 = tmem_a + ((q * 32) << 16);
     // x: block of 16 rows t >> 1, chunks (t & 1) * 2 and the next, of task t = w, w + 4, ..
     const uint32_t chunk = (w & 1) * 2 + (lane >> 4), x_row = (w >> 1) * 2048 + (lane & 15) * 128;
-    const uint32_t x_from = half * 128 + x_row + (((first * 4 + chunk) ^ swz) << 4);
+    const uint32_t x_from = kInt8Half * 128 + x_row + (((first * 4 + chunk) ^ swz) << 4);
     const uint32_t x_to0 = sm0 + x_row + (((2 * chunk) ^ swz) << 4), x_to1 = sm0 + x_row + (((2 * chunk + 1) ^ swz) << 4);
     const uint32_t full0 = cluster_addr(wide_full0, 0);
     const uint32_t step = 2 * halves, begin = halves == 2 ? set : set >> 1;  // stages
-    uint32_t raw = begin, raw_phase = 0, slot = set, slot_phase = 1;
+    uint32_t raw = begin, raw_phase = 0, slot_phase = 1;
     bool ok = true;
     Int8Cursor at(n_tiles);
     int kb = (int)begin;
     for (; kb >= KB && at.u < units; kb -= KB) at.next();
     while (at.u < units && ok) {
-      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const Int8Unit un = int8_unit(p, pre, at, tile);
       const int tasks = (__shfl_sync(0xffffffffu, un.rows, 0) + 31) / 32 * 2;
       for (; kb < KB; kb += step) {
-        ok = int8_wait2(raw_full0 + raw * 8, raw_phase, wide_empty0 + slot * 8, slot_phase, ab);
+        ok = int8_wait2(raw_full0 + raw * 8, raw_phase, wide_empty0 + set * 8, slot_phase, ab);
         if (!ok) break;
         tc_fence_after();
         const uint32_t st = raw0 + raw * raw_bytes;
-        uint32_t off = slot * slot_bytes, ta = ta0 + slot * slot_cols;
+        uint32_t off = set * slot_bytes, ta = ta0 + set * slot_cols;
         // the second half's chunks are 64 bytes away, up or down, in the swizzled rows
 #pragma unroll 1
         for (uint32_t flip = 0; flip < 64u * halves; flip += 64, ta += 32, off += panel) {
-          if (has_weights) {
+          {
             const uint32_t from = st + (w_row ^ flip);
             const int4 c0 = lds_v4(from), c1 = lds_v4(from ^ 16), c2 = lds_v4(from ^ 32), c3 = lds_v4(from ^ 48);
             uint32_t v[16];
@@ -589,16 +559,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_at(raw_empty0 + raw * 8, halves);
-          mbar_arrive_cluster(full0 + slot * 8);
+          mbar_arrive_cluster(full0 + set * 8);
         }
         if ((raw += step) >= raw_stages) {
           raw -= raw_stages;
           raw_phase ^= 1;
         }
-        if ((slot += kSets) >= slots) {
-          slot -= slots;
-          slot_phase ^= 1;
-        }
+        slot_phase ^= 1;
       }
       if (!ok) break;
       for (; kb >= KB && at.u < units; kb -= KB) at.next();
@@ -609,10 +576,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     const uint32_t empty0 = cluster_addr(smem_u32(acc_empty), 0);
     uint32_t done = 0;
     for (Int8Cursor at(n_tiles); at.u < units; at.next(), ++done) {
-      const Int8Unit un = int8_unit(p, pre, at, width, tile);
+      const Int8Unit un = int8_unit(p, pre, at, tile);
       const uint32_t buf = done & 1;
-      const int n = un.n0 + (int)rank * half + 32 * (int)q;  // the warp's first weight row
-      const int groups = 32 * (int)q < half && n < p.N ? (un.rows + 31) / 32 : 0;
+      const int n = un.n0 + (int)rank * kInt8Half + 32 * (int)q;  // the warp's first weight row
+      const int groups = n < p.N ? (un.rows + 31) / 32 : 0;
       const float wscale = n + lane < p.N && groups ? p.ws[(size_t)un.e * p.N + n + lane] : 0.f;
       for (int g = 0; g < groups; ++g) {
         const int r = 32 * g + lane;
@@ -667,13 +634,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
 // ------------------------------------------------------------- any k and alignment
 
 // Rows whose length the tensor kernel's copies cannot take (k not a multiple of 16): 32 rows
-// x 64 features a unit, four products an instruction (dp4a), 32-bit sums. Bound by those
-// instructions; a shape of this kind is no one's production size.
+// x 64 features a unit, four products an instruction (dp4a), 32-bit sums. A warp loads 128
+// bytes of a row as aligned words, which neighbouring lanes put together, while the stage
+// before is worked on.
 constexpr int kPlainThreads = 256, kPlainRows = 32, kPlainCols = 64, kPlainK = 128;
 
+// A lane's four of the 128 bytes at `at` of a matrix of `total` bytes, the first `left` of them, the rest zeros.
+__device__ __forceinline__ uint32_t plain_word(const int8_t* m, long long total, long long at, int left) {
+  const int lane = threadIdx.x & 31, skip = (int)(at & 3);
+  const auto word = [&](int i) {
+    uint32_t v = 0;
+    const long long b = (at - skip) + 4 * i;
+    if (4 * i < left + skip) {
+      if (b + 4 <= total) {
+        v = __ldg(reinterpret_cast<const unsigned int*>(m + b));
+      } else {
+        for (int q = 0; b + q < total; ++q) v |= (uint32_t)(uint8_t)m[b + q] << (8 * q);
+      }
+    }
+    return v;
+  };
+  const uint32_t lo = word(lane);
+  uint32_t hi = __shfl_down_sync(0xffffffffu, lo, 1);
+  if (lane == 31) hi = skip ? word(32) : 0;
+  const uint32_t v = __funnelshift_r(lo, hi, 8 * skip);
+  const int mine = left - 4 * lane;
+  return mine >= 4 ? v : mine <= 0 ? 0 : v & (0xffffffffu >> (32 - 8 * mine));
+}
+
 template <int YT, bool SWIGLU>
-__global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8ProductParams p) {
-  __shared__ int s_x[kPlainRows][kPlainK / 4 + 1], s_w[kPlainCols][kPlainK / 4 + 1];
+__global__ void __launch_bounds__(kPlainThreads, 2) int8_product_plain_kernel(Int8ProductParams p) {
+  // feature 4 t + b of a unit lies in row t + 16 b: eight lanes' 16 bytes are in different banks
+  __shared__ __align__(16) int s_x[kPlainRows][kPlainK / 4 + 4], s_w[kPlainCols][kPlainK / 4 + 4];
   __shared__ uint32_t s_warp[kPlainThreads / 32 + 1];
   extern __shared__ int pre[];
   if (threadIdx.x == 0) s_warp[kPlainThreads / 32] = 0;
@@ -693,27 +685,41 @@ __global__ void __launch_bounds__(kPlainThreads) int8_product_plain_kernel(Int8P
     const int before = (mt - pre[e]) * kPlainRows, rows = min(kPlainRows, count[e] - before);
     const long long row0 = first[e] + before;
     int acc[2][4] = {};
+    constexpr int kWarps = kPlainThreads / 32, kXLoads = kPlainRows / kWarps, kLoads = (kPlainRows + kPlainCols) / kWarps;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t next[kLoads];
+    const auto load = [&](int k0) {
+      const int left = min(kPlainK, p.K - k0);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kWarps + warp, c = n0 + r - kPlainRows;
+        next[i] = i < kXLoads ? plain_word(p.x, (long long)p.W * p.A * p.K, (row0 + r) * p.K + k0, r < rows ? left : 0)
+                              : plain_word(p.w, (long long)p.E * p.N * p.K, ((long long)e * p.N + c) * p.K + k0, c < p.N ? left : 0);
+      }
+    };
+    load(0);
     for (int k0 = 0; k0 < p.K; k0 += kPlainK) {
       __syncthreads();
-      for (int i = threadIdx.x; i < (kPlainRows + kPlainCols) * kPlainK; i += kPlainThreads) {
-        const int r = i / kPlainK, c = i % kPlainK;
-        int8_t v = 0;
-        if (r < kPlainRows) {
-          if (r < rows && k0 + c < p.K) v = p.x[(size_t)(row0 + r) * p.K + k0 + c];
-          reinterpret_cast<int8_t*>(s_x[r])[c] = v;
-        } else {
-          const int j = r - kPlainRows;
-          if (n0 + j < p.N && k0 + c < p.K) v = p.w[((size_t)e * p.N + n0 + j) * p.K + k0 + c];
-          reinterpret_cast<int8_t*>(s_w[j])[c] = v;
-        }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kWarps + warp, c = r - kPlainRows;
+        (i < kXLoads ? s_x[r] : s_w[(c >> 2) + 16 * (c & 3)])[lane] = (int)next[i];
       }
       __syncthreads();
-#pragma unroll 4
-      for (int k = 0; k < kPlainK / 4; ++k)
+      if (k0 + kPlainK < p.K) load(k0 + kPlainK);
+#pragma unroll 2
+      for (int k = 0; k < kPlainK / 4; k += 4) {
+        int4 x[2], w[4];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) x[a] = *reinterpret_cast<const int4*>(&s_x[ty * 2 + a][k]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) w[b] = *reinterpret_cast<const int4*>(&s_w[tx + 16 * b][k]);
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int b = 0; b < 4; ++b) acc[a][b] = __dp4a(s_x[ty * 2 + a][k], s_w[tx * 4 + b][k], acc[a][b]);
+          for (int b = 0; b < 4; ++b)
+            acc[a][b] = __dp4a(x[a].w, w[b].w, __dp4a(x[a].z, w[b].z, __dp4a(x[a].y, w[b].y, __dp4a(x[a].x, w[b].x, acc[a][b]))));
+      }
     }
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
@@ -819,11 +825,9 @@ extern "C" moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const i
     bool good = true;
     for (unsigned i = 0; i < 6; ++i)
       good = good && int8_map(&maps.x[i], x, (unsigned long long)k, (unsigned long long)W * A, 0, 16 * (i + 1));
-    for (unsigned i = 0; i < 2; ++i)
-      good = good && int8_map(&maps.w[i], w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, 64 * (i + 1));
+    good = good && int8_map(&maps.w, w, (unsigned long long)k, (unsigned long long)n, (unsigned long long)E, kInt8Half);
     if (!good) return MOE_ERR_CUDA;
-    for (int t = 0; t < 6; ++t)
-      for (int b = 0; b < 2; ++b) p.raw_stages[t][b] = int8_raw_stages(E, 32 * (t + 1), 128 * (b + 1));
+    for (int t = 0; t < 6; ++t) p.raw_stages[t] = int8_raw_stages(E, 32 * (t + 1));
     const Int8Kernel kernel = y_dtype == MOE_F16 ? (sw ? int8_product_kernel<MOE_F16, true> : int8_product_kernel<MOE_F16, false>)
                                                  : (sw ? int8_product_kernel<MOE_BF16, true> : int8_product_kernel<MOE_BF16, false>);
     if (resident_blocks((const void*)kernel, kInt8ProductThreads, kInt8ProductSmem, &per_sm) != cudaSuccess || per_sm < 1)
