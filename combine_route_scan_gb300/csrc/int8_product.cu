@@ -18,6 +18,13 @@
 //     128 columns leave TMEM for half as much: then a slot is half a stage, and so is a set's turn;
 //   * warps: 0 TMA, 1 MMA (of the pair's first CTA), 2..17 widen, 18..21 epilogue. Two accumulators, so
 //     that the next unit's MMAs run while this one is read.
+//
+// Measured: 4096 rows of 128 experts, 2048 -> 1024 with SwiGLU, 50 us, 5.6 TB/s; 512 -> 2048, 35 us;
+// 32768 rows of 256 experts, 7168 -> 1024, 458 us, 4.7 TB/s and 1.05 PFLOP/s; 131072 rows of 128 experts, 2048
+// -> 1024, 390 us, 1.4 PFLOP/s; 8 rows 10.2 us. Few rows are bound by HBM, and by some 5 us before
+// the first product and behind the last (a unit's copies, widening, MMAs and epilogue end to end). Many
+// are bound by the widening and the way of a slot through it: without widening prefill takes 273 us of 387,
+// without x 318, without weights 313, without the epilogue 356.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -634,38 +641,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
 // ------------------------------------------------------------- any k and alignment
 
 // Rows whose length the tensor kernel's copies cannot take (k not a multiple of 16): 32 rows
-// x 64 features a unit, four products an instruction (dp4a), 32-bit sums. A warp loads 128
-// bytes of a row as aligned words, which neighbouring lanes put together, while the stage
-// before is worked on.
+// x 64 features a unit, by a warp's integer products (mma.sync, sums in 32-bit integers). A
+// warp loads 128 bytes of a row as aligned words, which neighbouring lanes put together,
+// while the stage before is worked on. 4096 rows of 128 experts, 2040 -> 1024: 372 us, where
+// the tensor kernel takes 52 with 2032; bound by the words' loads and their putting together
+// (a stage has 96 of these for 8 products a warp).
 constexpr int kPlainThreads = 256, kPlainRows = 32, kPlainCols = 64, kPlainK = 128;
 
-// A lane's four of the 128 bytes at `at` of a matrix of `total` bytes, the first `left` of them, the rest zeros.
-__device__ __forceinline__ uint32_t plain_word(const int8_t* m, long long total, long long at, int left) {
-  const int lane = threadIdx.x & 31, skip = (int)(at & 3);
-  const auto word = [&](int i) {
-    uint32_t v = 0;
-    const long long b = (at - skip) + 4 * i;
-    if (4 * i < left + skip) {
-      if (b + 4 <= total) {
-        v = __ldg(reinterpret_cast<const unsigned int*>(m + b));
-      } else {
-        for (int q = 0; b + q < total; ++q) v |= (uint32_t)(uint8_t)m[b + q] << (8 * q);
-      }
-    }
-    return v;
-  };
-  const uint32_t lo = word(lane);
-  uint32_t hi = __shfl_down_sync(0xffffffffu, lo, 1);
-  if (lane == 31) hi = skip ? word(32) : 0;
-  const uint32_t v = __funnelshift_r(lo, hi, 8 * skip);
-  const int mine = left - 4 * lane;
-  return mine >= 4 ? v : mine <= 0 ? 0 : v & (0xffffffffu >> (32 - 8 * mine));
+// A matrix's rows from one of them on, `left` of its bytes: 32-bit offsets from an aligned address, which `skip` bytes of
+// other rows may follow.
+struct PlainRows {
+  const int8_t* base;
+  uint32_t skip, left;
+  __device__ PlainRows(const int8_t* m, long long total, long long at)
+      : base(m + (at & ~3ll)), skip((uint32_t)at & 3), left((uint32_t)min(total - (at & ~3ll), 0x7fffffffll)) {}
+  // a lane's aligned word of the `bytes` bytes at `at`, and the one behind lane 31's; the words that hold
+  // the matrix's last bytes and others are left out
+  __device__ __forceinline__ void load(uint32_t at, int bytes, uint32_t& word, uint32_t& behind) const {
+    const uint32_t lane = threadIdx.x & 31, byte = (at & ~3u) + 4 * lane;
+    const bool here = (int)(4 * lane) < bytes + (int)(at & 3);
+    word = here && byte + 4 <= left ? __ldg(reinterpret_cast<const unsigned int*>(base + byte)) : 0u;
+    behind = here && lane == 31 && (at & 3) && byte + 8 <= left ? __ldg(reinterpret_cast<const unsigned int*>(base + byte + 4)) : 0u;
+  }
+  // a lane's four of those bytes, zeros beyond them
+  __device__ __forceinline__ uint32_t four(uint32_t at, int bytes, uint32_t word, uint32_t behind) const {
+    const uint32_t lane = threadIdx.x & 31, byte = (at & ~3u) + 4 * lane;
+    const auto last = [&](uint32_t from, uint32_t& v) {  // the matrix's last word, if bytes follow it that are not its own
+      if (from < left && from + 4 > left)
+        for (uint32_t q = 0; from + q < left; ++q) v |= (uint32_t)(uint8_t)base[from + q] << (8 * q);
+    };
+    last(byte, word);
+    if (lane == 31) last(byte + 4, behind);
+    uint32_t next = __shfl_down_sync(0xffffffffu, word, 1);
+    if (lane == 31) next = behind;
+    const uint32_t v = __funnelshift_r(word, next, 8 * (at & 3));
+    const int mine = bytes - 4 * (int)lane;
+    return mine >= 4 ? v : mine <= 0 ? 0 : v & (0xffffffffu >> (32 - 8 * mine));
+  }
+};
+
+// 16 rows by 8 features, 32 products each: a lane (g, t) of 8 x 4 has row g's and row g + 8's words t and t + 4 of x, feature
+// g's of w, and results (g, 2 t), (g, 2 t + 1) and those of row g + 8.
+__device__ __forceinline__ void plain_mma(int (&d)[4], const int (&a)[4], int b0, int b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 template <int YT, bool SWIGLU>
 __global__ void __launch_bounds__(kPlainThreads, 2) int8_product_plain_kernel(Int8ProductParams p) {
-  // feature 4 t + b of a unit lies in row t + 16 b: eight lanes' 16 bytes are in different banks
-  __shared__ __align__(16) int s_x[kPlainRows][kPlainK / 4 + 4], s_w[kPlainCols][kPlainK / 4 + 4];
+  // 4 words beyond a row's: a fragment's eight rows of four words are in different banks
+  __shared__ int s_x[kPlainRows][kPlainK / 4 + 4], s_w[kPlainCols][kPlainK / 4 + 4];
   __shared__ uint32_t s_warp[kPlainThreads / 32 + 1];
   extern __shared__ int pre[];
   if (threadIdx.x == 0) s_warp[kPlainThreads / 32] = 0;
@@ -678,66 +704,70 @@ __global__ void __launch_bounds__(kPlainThreads, 2) int8_product_plain_kernel(In
   const int* count = first + p.E;
   const int n_tiles = (p.N + kPlainCols - 1) / kPlainCols;
   const long long units = (long long)pre[p.E] * n_tiles;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int m0 = 16 * (warp & 1), f0 = 16 * (warp >> 1);  // the warp's 16 rows and 16 features
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int mt = (int)(u / n_tiles), n0 = (int)(u % n_tiles) * kPlainCols;
     const int e = int8_expert_of(pre, p.E, mt);
     const int before = (mt - pre[e]) * kPlainRows, rows = min(kPlainRows, count[e] - before);
     const long long row0 = first[e] + before;
-    int acc[2][4] = {};
-    constexpr int kWarps = kPlainThreads / 32, kXLoads = kPlainRows / kWarps, kLoads = (kPlainRows + kPlainCols) / kWarps;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t next[kLoads];
+    int acc[2][4] = {};  // of 16 x 8 each
+    constexpr int kPitch = kPlainK / 4 + 4, kWarps = kPlainThreads / 32, kXLoads = kPlainRows / kWarps, kLoads = (kPlainRows + kPlainCols) / kWarps;
+    const PlainRows xr(p.x, (long long)p.W * p.A * p.K, row0 * p.K);
+    const PlainRows wr(p.w, (long long)p.E * p.N * p.K, ((long long)e * p.N + n0) * p.K);
+    uint32_t next[kLoads], behind[kLoads];
+    // all loads of a stage before anything waits for one of them
     const auto load = [&](int k0) {
-      const int left = min(kPlainK, p.K - k0);
+      const int bytes = min(kPlainK, p.K - k0);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = i * kWarps + warp, c = n0 + r - kPlainRows;
-        next[i] = i < kXLoads ? plain_word(p.x, (long long)p.W * p.A * p.K, (row0 + r) * p.K + k0, r < rows ? left : 0)
-                              : plain_word(p.w, (long long)p.E * p.N * p.K, ((long long)e * p.N + c) * p.K + k0, c < p.N ? left : 0);
+        const int r = (i < kXLoads ? i : i - kXLoads) * kWarps + warp;
+        const PlainRows& m = i < kXLoads ? xr : wr;
+        m.load(m.skip + r * p.K + k0, r < (i < kXLoads ? rows : p.N - n0) ? bytes : -4, next[i], behind[i]);
       }
     };
     load(0);
     for (int k0 = 0; k0 < p.K; k0 += kPlainK) {
+      const int bytes = min(kPlainK, p.K - k0);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = i * kWarps + warp, c = r - kPlainRows;
-        (i < kXLoads ? s_x[r] : s_w[(c >> 2) + 16 * (c & 3)])[lane] = (int)next[i];
+        const int r = (i < kXLoads ? i : i - kXLoads) * kWarps + warp;
+        const PlainRows& m = i < kXLoads ? xr : wr;
+        (i < kXLoads ? s_x[r] : s_w[r])[lane] =
+            (int)m.four(m.skip + r * p.K + k0, r < (i < kXLoads ? rows : p.N - n0) ? bytes : -4, next[i], behind[i]);
       }
       __syncthreads();
       if (k0 + kPlainK < p.K) load(k0 + kPlainK);
-#pragma unroll 2
-      for (int k = 0; k < kPlainK / 4; k += 4) {
-        int4 x[2], w[4];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) x[a] = *reinterpret_cast<const int4*>(&s_x[ty * 2 + a][k]);
+      for (int k = 0; k < kPlainK / 4; k += 8) {
+        const int* x = &s_x[m0 + g][k + t];
+        const int a[4] = {x[0], x[8 * kPitch], x[4], x[8 * kPitch + 4]};
 #pragma unroll
-        for (int b = 0; b < 4; ++b) w[b] = *reinterpret_cast<const int4*>(&s_w[tx + 16 * b][k]);
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            acc[a][b] = __dp4a(x[a].w, w[b].w, __dp4a(x[a].z, w[b].z, __dp4a(x[a].y, w[b].y, __dp4a(x[a].x, w[b].x, acc[a][b]))));
+        for (int b = 0; b < 2; ++b) {
+          const int* w = &s_w[f0 + 8 * b + g][k + t];
+          plain_mma(acc[b], a, w[0], w[4]);
+        }
       }
     }
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const int r = ty * 2 + a;
+      const int r = m0 + g + 8 * a;
       if (r >= rows) continue;
       const float xs = p.xs ? p.xs[row0 + r] : 1.f;
-      float z[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = n0 + tx * 4 + b;
-        z[b] = j < p.N ? (float)acc[a][b] * xs * p.ws[(size_t)e * p.N + j] : 0.f;
-      }
+      for (int b = 0; b < 2; ++b) {
+        const int j = n0 + f0 + 8 * b + 2 * t;  // and the next
+        float z[2];
 #pragma unroll
-      for (int b = 0; b < (SWIGLU ? 2 : 4); ++b) {
-        const int c = (SWIGLU ? n0 / 2 + tx * 2 : n0 + tx * 4) + b;
-        if (c >= p.C) continue;
-        const float v = SWIGLU ? int8_swiglu(z[(2 * b) & 3], z[(2 * b + 1) & 3]) : z[b];
-        static_cast<uint16_t*>(p.y)[(size_t)(row0 + r) * p.C + c] = int8_round<YT>(v);
+        for (int i = 0; i < 2; ++i) z[i] = j + i < p.N ? (float)acc[b][2 * a + i] * xs * p.ws[(size_t)e * p.N + j + i] : 0.f;
+        uint16_t* y = static_cast<uint16_t*>(p.y) + (size_t)(row0 + r) * p.C;
+        if (SWIGLU) {
+          if (j < p.N) y[j >> 1] = int8_round<YT>(int8_swiglu(z[0], z[1]));
+        } else {
+          if (j < p.N) y[j] = int8_round<YT>(z[0]);
+          if (j + 1 < p.N) y[j + 1] = int8_round<YT>(z[1]);
+        }
       }
     }
   }

