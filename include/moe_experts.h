@@ -204,7 +204,7 @@ moe_status_t moe_int8_quantize(const void* x, int32_t x_dtype, int32_t mats, int
  *
  *   cfg           the dispatch's configuration: W, bs, topk, E, wait_timeout_us and
  *                 the workspace size are taken from it; h, types and modes are not
- *   k             elements of a row, [1, 131071]
+ *   k             elements of a row, [1, 131071]; multiples of 16 are some 7 times as fast as others
  *   x             [W][A][k] int8 (A from moe_get_workspace_size), 16-byte aligned
  *   x_scales      [W][A] fp32 as moe_dispatch (quant_mode 2) or moe_int8_quantize wrote
  *                 them, or NULL for 1 everywhere (static scales, folded into w_scales)

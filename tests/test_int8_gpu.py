@@ -294,6 +294,19 @@ def test_product(case, dtype):
     pr.check(pr.run(dtype, swiglu), dtype, swiglu)
 
 
+@pytest.mark.parametrize("case", [
+    (2, 4, 1, [0, 8], 33, 129, False), (2, 4, 1, [8, 0], 1, 1, False), (2, 4, 1, [3, 8], 65, 131, False), (2, 4, 1, [1, 8], 63, 127, False),
+    (2, 40, 1, [5, 80], 65, 2047, False), (2, 40, 1, [80, 33], 130, 1001, True), (2, 4, 1, [8, 8], 2, 257, True),
+    (2, 16, 1, [32, 1], 129, 2040, False), (2, 16, 1, [31, 32], 66, 4095, True), (2, 100, 1, [200, 7], 1023, 385, False),
+], ids=lambda c: f"n{c[4]}_k{c[5]}_{'swiglu' if c[6] else 'plain'}")
+def test_product_of_odd_lengths(case):
+    """Rows that begin at every byte of a word, matrices that end inside one, a full rank's last row."""
+    W, bs, topk, counts, n, k, swiglu = case
+    pr = Product(W, bs, topk, counts, n, k, seed=n + k)
+    for dtype in ("bf16", "f16"):
+        pr.check(pr.run(dtype, swiglu), dtype, swiglu)
+
+
 @pytest.mark.parametrize("k", [1024, 1000, 336])
 def test_product_sums_are_whole(k):
     """Sums that grow to millions and come back to a few units: exact up to k = 1024."""
