@@ -4,12 +4,13 @@
 //
 // One pass over the data, bound by HBM: a row stays in registers between its maximum
 // and its codes, in a warp's where it has up to 2048 elements, in a block's up to
-// 16384; as the codes of its elements are made, the next row's take their registers.
+// 32768; as the codes of its elements are made, the next row's take their registers.
 // Rows go in pieces of 8 elements (16-byte loads), 2 or 1, as they align. Longer rows are
-// read twice, the second time from cache.
+// read twice, the second time from cache; of narrow pieces, shorter ones too.
 //
-// Measured: 131072 rows of 2048 bf16 130 us, 6.2 TB/s; of 2046, in pieces of 2 elements, 129; of 2047, one by one,
-// 319 (waiting for its loads of 2 bytes a lane); 4096 rows 3.1 us.
+// Measured, bf16: 131072 rows of 2048 130 us, 6.2 TB/s; of 2046, in pieces of 2 elements, 129; of 2047, one by one,
+// 319 (waiting for its loads of 2 bytes a lane); 4096 rows of 512 3.1 us; 16384 rows of 16384 125 us, 6.4 TB/s, of 18432
+// 162, 5.6 TB/s, of 65536 (read twice) 781, 4.1 TB/s.
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
 #include "quant_common.cuh"
@@ -155,18 +156,18 @@ struct Int8Unit {
   }
 };
 
-// The largest magnitude among the threads of a warp, or (BLOCK) of the block.
-template <bool BLOCK>
-__device__ __forceinline__ float int8_amax(float m, float (&s_max)[kInt8Threads / 32]) {
+// The largest magnitude among the THREADS threads of a warp or of the block.
+template <int THREADS>
+__device__ __forceinline__ float int8_amax(float m, float (&s_max)[THREADS / 32]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (!BLOCK) return m;
+  if (THREADS == 32) return m;
   __syncthreads();  // the row before is done with s_max
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = s_max[threadIdx.x & (kInt8Threads / 32 - 1)];
+  m = s_max[threadIdx.x & (THREADS / 32 - 1)];
 #pragma unroll
-  for (int o = kInt8Threads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = THREADS / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
@@ -198,15 +199,17 @@ __device__ __forceinline__ uint2 int8_codes(const f32x2 (&v)[4], f32x2 scale2, f
   return pack8_low(c);
 }
 
-// Rows that a warp's (BLOCK: the block's) threads hold as NV units each; x, its strides, cols and codes
+// Rows that a warp's or (THREADS > 32) the block's threads hold as NV units each; x, its strides, cols and codes
 // aligned for pieces of PIECE elements (with 8: 16 bytes of x).
-template <int DT, int PIECE, int NV, bool BLOCK>
-__global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 8 ? 2 : 4) int8_quantize_kernel(Int8QuantParams p) {
+template <int DT, int PIECE, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS > 32 ? THREADS : kInt8Threads,
+                                  ((DT == MOE_F32 ? 2 * NV : NV) > 8 ? 2 : 4) / (THREADS > kInt8Threads ? 2 : 1))
+    int8_quantize_kernel(Int8QuantParams p) {
+  constexpr bool BLOCK = THREADS > 32;
   __shared__ int s_pre[kInt8CountedMats + 1];
-  __shared__ float s_max[kInt8Threads / 32];
+  __shared__ float s_max[THREADS / 32];
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kThreads = BLOCK ? kInt8Threads : 32;
   const int t = BLOCK ? threadIdx.x : threadIdx.x & 31;
   const uint8_t* x = static_cast<const uint8_t*>(p.x);
   constexpr size_t kEs = DT == MOE_F32 ? 4 : 2;
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 
   if (first >= rows.total) return;
   size_t place;
   size_t from = rows.find(first, place);
-  Int8Unit<DT, PIECE, kThreads> u[NV];
+  Int8Unit<DT, PIECE, THREADS> u[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) u[j].load(x + from * kEs, t, j, p.cols);
   for (long long i = first; i < rows.total; i += step) {
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 
       m = u[j].amax(m);
       u[j].forget();
     }
-    m = int8_amax<BLOCK>(m, s_max);
+    m = int8_amax<THREADS>(m, s_max);
     const float scale = __fdiv_rn(m, 127.0f);
     const float rcp = __frcp_rn(scale);
     const f32x2 rcp2 = f2_pack(rcp, rcp), scale2 = f2_pack(-scale, -scale);
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 
     if (t == 0) p.scales[place] = scale;
     if (!int8_rcp_ok(scale)) {  // zeros, infinities, the smallest numbers: by the division, an element at a time
 #pragma unroll 1
-      for (int c = t; c < p.cols; c += kThreads) out[c] = (int8_t)(m == 0.f ? 0 : token_q(int8_load<DT>(p.x, from + c), scale));
+      for (int c = t; c < p.cols; c += THREADS) out[c] = (int8_t)(m == 0.f ? 0 : token_q(int8_load<DT>(p.x, from + c), scale));
     }
     const bool fast = int8_rcp_ok(scale), more = i + step < rows.total;
     if (more) from = rows.find(i + step, place);
@@ -249,49 +252,72 @@ __global__ void __launch_bounds__(kInt8Threads, (DT == MOE_F32 ? 2 * NV : NV) > 
   }
 }
 
-// Rows that a block's registers do not hold: read twice, an element at a time, the second time from cache.
-template <int DT>
-__global__ void __launch_bounds__(kInt8Threads) int8_quantize_long_kernel(Int8QuantParams p) {
+// Rows that a block's registers do not hold: read twice, the second time from cache.
+template <int DT, int PIECE>
+__global__ void __launch_bounds__(kInt8Threads, 4) int8_quantize_long_kernel(Int8QuantParams p) {
   __shared__ int s_pre[kInt8CountedMats + 1];
   __shared__ float s_max[kInt8Threads / 32];
   pdl_wait();
   pdl_launch_dependents();
+  using Unit = Int8Unit<DT, PIECE, kInt8Threads>;
+  const int t = threadIdx.x;
   Int8Rows rows(p, s_pre);
   for (long long i = blockIdx.x; i < rows.total; i += gridDim.x) {
     size_t place;
     const size_t from = rows.find(i, place);
+    const uint8_t* x = static_cast<const uint8_t*>(p.x) + from * (DT == MOE_F32 ? 4 : 2);
     float m = 0.f;
 #pragma unroll 8
-    for (int c = threadIdx.x; c < p.cols; c += kInt8Threads) m = fmaxf(m, fabsf(int8_load<DT>(p.x, from + c)));
-    m = int8_amax<true>(m, s_max);
-    const float scale = __fdiv_rn(m, 127.0f);
-    const bool fast = token_rcp_ok(scale);
-    const float rcp = fast ? __frcp_rn(scale) : 0.f;
-    int8_t* out = p.codes + place * p.cols;
-#pragma unroll 8
-    for (int c = threadIdx.x; c < p.cols; c += kInt8Threads) {
-      const float v = int8_load<DT>(p.x, from + c);
-      out[c] = (int8_t)(fast ? token_code(v, scale, rcp) : m == 0.f ? 0u : (uint32_t)token_q(v, scale));
+    for (int j = 0; Unit::element(t, j, 0) < p.cols; ++j) {
+      Unit u;
+      u.load(x, t, j, p.cols);
+      m = u.amax(m);
     }
-    if (threadIdx.x == 0) p.scales[place] = scale;
+    m = int8_amax<kInt8Threads>(m, s_max);
+    const float scale = __fdiv_rn(m, 127.0f);
+    int8_t* out = p.codes + place * p.cols;
+    if (int8_rcp_ok(scale)) {
+      const float rcp = __frcp_rn(scale);
+      const f32x2 rcp2 = f2_pack(rcp, rcp), scale2 = f2_pack(-scale, -scale);
+#pragma unroll 8
+      for (int j = 0; Unit::element(t, j, 0) < p.cols; ++j) {
+        Unit u;
+        u.load(x, t, j, p.cols);
+        f32x2 v[4];
+        u.pairs(v);
+        u.store(out, t, j, p.cols, int8_codes(v, scale2, rcp2));
+      }
+    } else {
+#pragma unroll 1
+      for (int c = t; c < p.cols; c += kInt8Threads) out[c] = (int8_t)(m == 0.f ? 0 : token_q(int8_load<DT>(p.x, from + c), scale));
+    }
+    if (t == 0) p.scales[place] = scale;
   }
 }
 
 struct Int8QuantKernel {
   void (*kernel)(Int8QuantParams);
-  bool block;
+  int threads;  // to a row
 };
 
 // The narrowest group of threads that holds a row.
 template <int DT, int PIECE>
 Int8QuantKernel int8_quant_kernel(int cols) {
-  if (cols <= 256) return {int8_quantize_kernel<DT, PIECE, 1, false>, false};
-  if (cols <= 512) return {int8_quantize_kernel<DT, PIECE, 2, false>, false};
-  if (cols <= 1024) return {int8_quantize_kernel<DT, PIECE, 4, false>, false};
-  if (cols <= 2048) return {int8_quantize_kernel<DT, PIECE, 8, false>, false};
-  if (cols <= 8192) return {int8_quantize_kernel<DT, PIECE, 4, true>, true};
-  if (cols <= 16384) return {int8_quantize_kernel<DT, PIECE, 8, true>, true};
-  return {int8_quantize_long_kernel<DT>, true};
+  if (cols <= 256) return {int8_quantize_kernel<DT, PIECE, 1, 32>, 32};
+  if (cols <= 512) return {int8_quantize_kernel<DT, PIECE, 2, 32>, 32};
+  if (cols <= 1024) return {int8_quantize_kernel<DT, PIECE, 4, 32>, 32};
+  if (cols <= 2048) return {int8_quantize_kernel<DT, PIECE, 8, 32>, 32};
+  // A block holds longer rows as far as their pieces are wide. One by one the kernel that reads rows twice is faster (bf16,
+  // 16384 rows of 16383 223 us, held 310; 32768 of 4095 159 and 183; but 65536 of 2047 202, held by a warp 165), by twos
+  // it is as fast above 16384 (16384 of 18430 183, held 188), in 16-byte pieces slower (18432 216, held 162).
+  if constexpr (PIECE > 1) {
+    if (cols <= 8192) return {int8_quantize_kernel<DT, PIECE, 4, 256>, 256};
+    if (cols <= 16384) return {int8_quantize_kernel<DT, PIECE, 8, 256>, 256};
+  }
+  if constexpr (PIECE == 8) {
+    if (cols <= 32768) return {int8_quantize_kernel<DT, PIECE, 8, 512>, 512};
+  }
+  return {int8_quantize_long_kernel<DT, PIECE>, kInt8Threads};
 }
 template <int DT>
 Int8QuantKernel int8_quant_kernel(int cols, int piece) {
@@ -324,10 +350,11 @@ extern "C" moe_status_t moe_int8_quantize(const void* x, int32_t x_dtype, int32_
                             : x_dtype == MOE_F16 ? int8_quant_kernel<MOE_F16>(cols, piece)
                                                  : int8_quant_kernel<MOE_BF16>(cols, piece);
   int per_sm = 0;
-  if (resident_blocks((const void*)k.kernel, kInt8Threads, 0, &per_sm) != cudaSuccess || per_sm < 1) return MOE_ERR_CUDA;
-  const long long need = k.block ? mats * rows : (mats * rows + kInt8Threads / 32 - 1) / (kInt8Threads / 32);
+  const int threads = k.threads > 32 ? k.threads : kInt8Threads;
+  if (resident_blocks((const void*)k.kernel, threads, 0, &per_sm) != cudaSuccess || per_sm < 1) return MOE_ERR_CUDA;
+  const long long need = k.threads > 32 ? mats * rows : (mats * rows + kInt8Threads / 32 - 1) / (kInt8Threads / 32);
   const long long most = (long long)nsm * per_sm;
-  PdlLaunch L(dim3((unsigned)(need < most ? need : most)), dim3(kInt8Threads), 0, static_cast<cudaStream_t>(stream));
+  PdlLaunch L(dim3((unsigned)(need < most ? need : most)), dim3(threads), 0, static_cast<cudaStream_t>(stream));
   if (cudaLaunchKernelEx(&L.cfg, k.kernel, p) != cudaSuccess) return MOE_ERR_CUDA;
   note_launches(1);
   return MOE_OK;

@@ -44,7 +44,8 @@ def make_rows(rng, shape, dtype, std=1.0):
 QUANT_SHAPES = [(1, 1, 1), (3, 5, 7), (2, 3, 8), (1, 9, 250), (2, 33, 256), (2, 10, 264), (1, 40, 512), (3, 7, 1000), (2, 17, 1024),
                 (1, 19, 2048), (1, 5, 2056), (2, 3, 4090), (1, 4, 7168), (1, 3, 8192), (1, 3, 9000), (1, 2, 16384), (1, 2, 20001),
                 (700, 2, 16), (1, 5000, 24),
-                (2, 300, 511), (1, 90, 2046), (1, 90, 2047), (1, 20, 8190), (1, 9, 16383)]
+                (2, 300, 511), (1, 90, 2046), (1, 90, 2047), (1, 20, 8190), (1, 9, 16383), (3, 5, 18432), (1, 700, 18430),
+                (1, 700, 16385), (2, 9, 32768), (1, 5, 32766), (1, 3, 32769), (2, 90, 40000), (1, 30, 40002), (1, 9, 65535)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
