@@ -577,6 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
       if (!ok) break;
       for (; kb >= KB && at.u < units; kb -= KB) at.next();
     }
+    // the commit of the set's last slot comes from the first CTA: it is there before this one may leave
+    if (ok) int8_wait(wide_empty0 + set * 8, slot_phase, ab);
   } else {
     const uint32_t q = warp & 3;
     const uint32_t my_turn = smem_u32(turn) + q * kInt8TurnWarp, my_xs = smem_u32(turn) + 4 * kInt8TurnWarp + q * kInt8MostRows * 4;
@@ -585,6 +587,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
     for (Int8Cursor at(n_tiles); at.u < units; at.next(), ++done) {
       const Int8Unit un = int8_unit(p, pre, at, tile);
       const uint32_t buf = done & 1;
+      // An accumulator goes back only to a later unit, whose MMAs wait for all eight arrivals: one that nobody waits
+      // for could reach the first CTA when it has left.
+      const bool taken_again = at.u + 2 * (int)(gridDim.x >> 1) < units;
       const int n = un.n0 + (int)rank * kInt8Half + 32 * (int)q;  // the warp's first weight row
       const int groups = n < p.N ? (un.rows + 31) / 32 : 0;
       const float wscale = n + lane < p.N && groups ? p.ws[(size_t)un.e * p.N + n + lane] : 0.f;
@@ -607,14 +612,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
           // the last columns are in registers: the accumulator goes back before they are stored
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(empty0 + buf * 8);
+          if (lane == 0 && taken_again) mbar_arrive_cluster(empty0 + buf * 8);
         }
         int8_store<YT, SWIGLU>(p, my_turn, v, wscale, my_xs + g * 128, un.row0 + 32 * g, min(32, left), SWIGLU ? n / 2 : n);
       }
       if (groups == 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(empty0 + buf * 8);
+        if (lane == 0 && taken_again) mbar_arrive_cluster(empty0 + buf * 8);
       }
     }
   }
@@ -631,7 +636,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kInt8ProductThreads,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // nor does a CTA leave while the other one may still arrive on its barriers
+  // Nor does a CTA leave while the other one may still arrive on its barriers. The barrier releases nothing, so it orders no
+  // arrival: each one has been waited for, or (after an abort) a millisecond has passed.
+  cluster_sync();
   if (warp == kInt8PlanThreads / 32) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

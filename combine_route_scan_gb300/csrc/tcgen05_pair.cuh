@@ -75,7 +75,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // The cluster's barrier in two parts, for mbarriers initialised before (fence.mbarrier_init) and for leaving together: no
-// other writes are released, which would have every warp wait for its own.
+// other writes are released, which would have every warp wait for its own. Arrivals at the other CTA's mbarriers are not
+// ordered by it either: before they leave together, each has to have been waited for where it arrives.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
