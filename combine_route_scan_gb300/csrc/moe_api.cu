@@ -238,7 +238,8 @@ moe_status_t moe_get_workspace_size(const moe_config_t* cfg, size_t* ws_bytes, i
 // pass; every other combine on that workspace runs it, and the inverse kernel
 // itself returns at once when the routing kernel's record in the workspace
 // header shows the map already belongs to its buffers. moe_workspace_init
-// clears the mark.
+// clears the mark. The table remembers 256 workspaces; once it has let go of a
+// marked one, a workspace that it does not know counts as marked.
 namespace {
 struct MapOwner {
   const void* ws;
@@ -250,6 +251,7 @@ struct MapOwner {
 std::mutex g_owner_mu;
 MapOwner g_owner[256];
 int g_owner_next = 0;
+bool g_owner_forgot = false;  // a marked workspace is no longer in the table
 
 // Capture sequence of `s` (0 when the stream is not capturing).
 unsigned long long capture_id(cudaStream_t s) {
@@ -267,7 +269,8 @@ MapOwner* owner_slot(const void* ws) {
     if (o.ws == ws) return &o;
   MapOwner* o = &g_owner[g_owner_next];
   g_owner_next = (g_owner_next + 1) % 256;
-  *o = MapOwner{ws, nullptr, nullptr, 0ull, false};
+  g_owner_forgot |= o->graphed;
+  *o = MapOwner{ws, nullptr, nullptr, 0ull, g_owner_forgot};
   return o;
 }
 
