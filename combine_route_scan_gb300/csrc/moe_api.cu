@@ -7,6 +7,8 @@
 
 #include <atomic>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "../../include/moe_experts.h"
 #include "experts_host.h"
@@ -24,7 +26,8 @@ void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_
 cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* per_sm) {
   // The dynamic shared-memory limit is state of the kernel, not of one call:
   // it is only ever raised (to the largest size asked for so far), so a call
-  // with a smaller size never lowers it under a later, larger one.
+  // with a smaller size never lowers it under a later, larger one. Both tables
+  // grow with the kernels, devices and sizes that are asked for.
   struct Limit {
     const void* kernel;
     int dev;
@@ -36,35 +39,42 @@ cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* p
     size_t smem;
     int per_sm;
   };
-  static Limit limits[128];
-  static Occupancy occ[256];
-  static int n_limits = 0, n_occ = 0;
+  static std::vector<Limit> limits;
+  static std::vector<Occupancy> occ;
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  Limit* lim = nullptr;
-  for (int i = 0; i < n_limits; ++i)
-    if (limits[i].kernel == kernel && limits[i].dev == dev) lim = &limits[i];
-  if (!lim || lim->smem < smem) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (lim) lim->smem = smem;
-    else if (n_limits < 128) limits[n_limits++] = Limit{kernel, dev, smem};
-  }
-  for (int i = 0; i < n_occ; ++i) {
-    const Occupancy& t = occ[i];
+  for (const Occupancy& t : occ) {  // its limit is this size or more
     if (t.kernel == kernel && t.dev == dev && t.threads == threads && t.smem == smem) {
       *per_sm = t.per_sm;
       return cudaSuccess;
     }
   }
-  int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
-  if (e != cudaSuccess) return e;
-  if (n_occ < 256) occ[n_occ++] = Occupancy{kernel, dev, threads, smem, n};
-  *per_sm = n;
+  try {
+    if (smem > 0) {  // any limit allows none
+      Limit* lim = nullptr;
+      for (Limit& l : limits)
+        if (l.kernel == kernel && l.dev == dev) lim = &l;
+      if (!lim) {
+        limits.push_back(Limit{kernel, dev, 0});
+        lim = &limits.back();
+      }
+      if (lim->smem < smem) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        lim->smem = smem;
+      }
+    }
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    occ.push_back(Occupancy{kernel, dev, threads, smem, n});
+    *per_sm = n;
+  } catch (const std::bad_alloc&) {
+    return cudaErrorMemoryAllocation;
+  }
   return cudaSuccess;
 }
 
