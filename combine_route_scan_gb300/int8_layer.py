@@ -36,7 +36,7 @@ class Int8Layer(RoutedLayer):
         self.gate_up = M.alloc_int8(gate_up)
         M.int8_quantize(gate_up, *self.gate_up)
         self.down = M.alloc_int8(w_down)
-        M.int8_quantize(w_down, *self.down)
+        M.int8_quantize(w_down.contiguous(), *self.down)
         self.h1 = torch.empty((W, self.y.shape[1], I), dtype=dtype, device=w_gate.device)
         self.h1_rows = M.alloc_int8(self.h1)
 
