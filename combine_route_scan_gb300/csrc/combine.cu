@@ -75,9 +75,7 @@ struct ReduceTable {
   int n;
 };
 
-template <class P>
-__device__ __forceinline__ void build_reduce_table(const P& p, size_t tau, ReduceTable& tab) {
-  constexpr bool kGrad = std::is_same<P, DispatchGradParams>::value;
+__device__ __forceinline__ void build_reduce_table(const CombineParams& p, size_t tau, ReduceTable& tab) {
   const Shape& sh = p.sh;
   const int lane = threadIdx.x & 31;
   const uint8_t* src = nullptr;
@@ -102,17 +100,10 @@ __device__ __forceinline__ void build_reduce_table(const P& p, size_t tau, Reduc
       } else {
         set_error(p.status, MOE_ERR_BAD_ASSIST);
       }
-    } else if (!kGrad && c == kPickCopy) {
+    } else if (c == kPickCopy) {
       src = static_cast<const uint8_t*>(p.x) + tau * (size_t)sh.row_in;
     }
-    if constexpr (kGrad) {
-      w = __float_as_uint(1.f);
-      if (p.pick_weights)
-        p.pick_weights[tau * sh.K + lane] =
-            src ? p.row_weights[(src - static_cast<const uint8_t*>(p.expert_out)) / sh.row_in] : 0.f;
-    } else {
-      if (src) w = reinterpret_cast<const uint32_t*>(p.scales)[tau * sh.K + lane];
-    }
+    if (src) w = reinterpret_cast<const uint32_t*>(p.scales)[tau * sh.K + lane];
   }
   const uint32_t m = __ballot_sync(0xffffffffu, src != nullptr);
   if (src) {
