@@ -177,10 +177,12 @@ __device__ __forceinline__ float int8_load(const void* x, size_t i) {
   else return load_elem(x, i, DT);
 }
 
-// The codes of 8 elements, round(v / scale), from r = 1 / scale rounded to nearest: with y = v * r, which is within an
-// ulp of the quotient, y + r * (v - y * scale) is the quotient rounded to nearest (Markstein 1990, by fused
-// multiply-adds), as the division gives it; adding 1.5 * 2^23 leaves the integer in the low byte. For scales whose
-// residuals do not underflow (int8_rcp_ok); a quotient of smaller elements is 0 in any case. (dispatch's token_codes8
+// The codes of 8 elements, round(v / scale), from r = 1 / scale rounded to nearest: y = v * r is up to 1.5 ulps off the
+// quotient, and y + r * (v - y * scale), by fused multiply-adds, off it by a rounding and less than 2^-20 of an ulp before
+// that (after Markstein 1990, whose y is within one ulp); adding 1.5 * 2^23 leaves the integer in the low byte. That no
+// code differs from the division's was compared next to every half step for each of the 2^23 mantissas that a row's
+// largest magnitude may have (tests/test_int8_half_steps_gpu.py); powers of two change nothing, for scales whose residuals
+// do not underflow (int8_rcp_ok); a quotient of smaller elements is 0 in any case. (dispatch's token_codes8
 // takes the division where a product is near a half, which of bf16 rows is every other eight: half the largest
 // magnitude, 63.5, is a frequent number.)
 __device__ __forceinline__ bool int8_rcp_ok(float scale) { return scale >= 7.8886091e-31f && scale <= 3.40282347e38f; }  // 2^-100
