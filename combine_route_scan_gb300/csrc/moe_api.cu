@@ -247,8 +247,12 @@ moe_status_t moe_get_workspace_size(const moe_config_t* cfg, size_t* ws_bytes, i
 // sequence as the dispatch (the graph replays the two in order) skips the
 // pass; every other combine on that workspace runs it, and the inverse kernel
 // itself returns at once when the routing kernel's record in the workspace
-// header shows the map already belongs to its buffers. moe_workspace_init
-// clears the mark. The table remembers 256 workspaces; once it has let go of a
+// header shows the map already belongs to its buffers. A combine or a gradient
+// that rebuilds the map for other buffers replaces it as well: it drops the
+// record, and captured it marks the workspace too. The price of a mark is a
+// launch for each combine outside the dispatch's capture, also right behind
+// its own dispatch: dispatch and combine of 512 tokens of hidden 2048 take 16.6
+// us for 15.2, of 4096 of 7168 169 for 167. moe_workspace_init clears it. The table remembers 256 workspaces; once it has let go of a
 // marked one, a workspace that it does not know counts as marked.
 namespace {
 struct MapOwner {
@@ -256,7 +260,7 @@ struct MapOwner {
   const void* assist;
   const void* ep;
   unsigned long long capture;  // capture sequence of the dispatch, 0 = not captured
-  bool graphed;                // some dispatch on this workspace was captured
+  bool graphed;                // marked: a captured call may replace its map at any time
 };
 std::mutex g_owner_mu;
 MapOwner g_owner[256];
@@ -757,8 +761,10 @@ moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out,
   p.grad_rows = grad_expert_out;
   p.grad_scales = grad_scales;
   p.grad_x = grad_x;
-  // Looking for the rows costs less than the map's launch at every size (with and without: 16 tokens of hidden 256 5.3 and
-  // 7.1 us, 512 of 2048 10.6 and 12.1, 4096 of 7168 158 and 161).
+  // Looking for the rows costs less than rebuilding the map where an expert has tens of rows from a rank (with and
+  // without: 16 tokens of hidden 256 5.3 and 7.1 us, 512 of 2048 10.6 and 12.1, 4096 of 7168 158 and 161), and less than
+  // 3 us where it has a thousand, in dispatch's order. Rows in another order are looked for through all of them: 4096
+  // tokens of hidden 2048, top-2 of 4 experts on 2 ranks, take 32 us with a map of theirs, 35 without, 65 permuted.
   return run_grad(cfg, p, true, ws, static_cast<cudaStream_t>(stream), launch_combine_grad);
 }
 
@@ -782,9 +788,11 @@ moe_status_t moe_dispatch_backward(const moe_config_t* cfg, const void* grad_exp
   p.row_weights = grad_expand_scales;
   p.pick_weights = grad_scales;
   // A block a token that looks for its rows, or the map and the combine's reduce, whose warps need no barrier: the first
-  // for small batches and long rows (512 tokens of hidden 2048 6.4 and 8.4 us, 4096 of 7168 86 and 89), the second for
-  // many tokens of short ones (2048 of 2048 16.5 and 17.9, 4096 of 2048 29.8 and 31.5; nothing between 4 and 14 KB was
-  // measured). Rows that do not align to 16 bytes, which the reduce would take an element at a time (2048 tokens of
+  // for small batches and long rows (top-8 of 128 experts on 8 ranks, bf16: 512 tokens of hidden 2048 6.1 and 7.9 us, 1024
+  // of 1024 8.7 and 8.3; 4096 of 4096 49 and 53, of 5120 63 and 71, of 7168 96 and 97), the second for many tokens of
+  // short ones (4096 of 1024 25.6 and 17.9, of 2048 31 and 29, of 3584 46 and 47). Where an expert has a thousand rows
+  // and more from a rank, the search costs up to a tenth at long rows (top-2 of 4 experts on 2 ranks: 4096 of 7168 59.5
+  // and 57.6, 8192 of 7168 120 and 108). Rows that do not align to 16 bytes, which the reduce would take an element at a time (2048 tokens of
   // hidden 2047 53 us, 48 in pieces of 2 bytes, 24 of 2044 in pieces of 8), go the first way, with a map too.
   const bool search = p.sh.row_in >= 8192 || p.sh.row_in % 16 || (long long)p.sh.W * p.sh.bs * p.sh.K <= 8192;
   return run_grad(cfg, p, search, ws, static_cast<cudaStream_t>(stream), launch_dispatch_grad);

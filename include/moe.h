@@ -225,9 +225,9 @@ moe_status_t moe_dispatch(const moe_config_t* cfg, const void* x, const int32_t*
  * ep_recv_count it fills and records their addresses in the workspace; the
  * library also remembers (host side, per workspace) which two addresses the
  * last such call enqueued. When this call passes the same two and nothing can
- * have replaced the map since (no dispatch on this workspace was captured
- * into a CUDA graph, or this combine is captured in the same capture as that
- * dispatch), the map is used as it is; otherwise an inverse-map kernel first
+ * have replaced the map since (no dispatch on this workspace, nor a call that
+ * rebuilt its map, was captured into a CUDA graph, or this combine is captured
+ * in the same capture as that dispatch), the map is used as it is; otherwise an inverse-map kernel first
  * rebuilds it from assist_info, or returns at once when the workspace's
  * record shows the map already belongs to these buffers. The reduce checks
  * every pick's row against assist_info and ep_recv_count: contents changed in

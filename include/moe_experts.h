@@ -200,7 +200,11 @@ moe_status_t moe_int8_quantize(const void* x, int32_t x_dtype, int32_t mats, int
  *   z[r][j] = x_scales[r] * w_scales[e][j] * (sum over i of x[r][i] * w[e][j][i])
  * then the epilogue (MOE_EPI_*) in fp32, rounded once to y_dtype; silu as in
  * moe_expert_product. The integers' sum is exact where no partial sum is beyond 2^24
- * (any with k <= 1024); past that it is rounded as fp32 sums are.
+ * (any with k <= 1024). Past that, with k a multiple of 16, the tensor cores may cut what
+ * 16 products bring instead of rounding it: an error of up to 2^-23 of the running sum
+ * each time, k / 16 * 2^-23 in all (2^-10 for the longest rows, more than half a step of
+ * MOE_F16; a sum that grows to 2^29 over k = 131040 was 1.3e-4 of it off). With any
+ * other k the sum is an exact 32-bit integer, rounded once.
  *
  *   cfg           the dispatch's configuration: W, bs, topk, E, wait_timeout_us and
  *                 the workspace size are taken from it; h, types and modes are not
@@ -241,8 +245,8 @@ moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const int8_t* x, c
  *   grad_expert_out [W][A][h], grad_scales [W][bs][K] fp32, grad_x [W][bs][h]: any of them, but not all,
  *               may be NULL; none may overlap an input
  *   ws          a workspace of cfg, best the dispatch's, whose pick -> row map is then used; otherwise each pick's row is
- *               looked for among those that ep_recv_count gives to its expert and source rank, or (moe_dispatch_backward) the
- *               map rebuilt as moe_combine does. A pick that no row names, a count above the capacity and a bad id are
+ *               looked for among those that ep_recv_count gives to its expert and source rank (one by one where they are not
+ *               in dispatch's order), or (moe_dispatch_backward of many short rows) the map rebuilt as moe_combine does. A pick that no row names, a count above the capacity and a bad id are
  *               reported as there
  * Row arrays are 16-byte aligned. grad_scales is what moe_route_backward takes. */
 moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out, const void* expert_out,
