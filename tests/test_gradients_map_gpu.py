@@ -135,3 +135,43 @@ def test_the_backward_of_two_micro_batches():
         again = torch.empty_like(out)
         M.combine(r.cfg, y, r.out["assist_info"], r.out["ep_recv_count"], r.ids_d, r.weights_d, r.mask, r.x, again, None, ws)
         assert M.get_device_status(ws) == 0 and torch.equal(again, out)
+
+
+def test_a_step_in_one_graph_on_one_workspace():
+    """Dispatch, combine and both gradients captured together: by the dispatch's own map, whatever another batch's calls
+    leave in the workspace between the replays."""
+    a, b = Routed(*CASES[0], seed=30), Routed(*CASES[0], seed=31)
+    ya, ya64 = a.expert_rows()
+    yb, _ = b.expert_rows()
+    g, g64 = a.rows((a.W, a.bs, a.h))
+    want, want_b = a.combine_backward(g, ya, x=True), b.dispatch_backward(yb)[0]
+    gx = a.dispatch_backward(ya, g)[0]
+    ws = a.ws
+    rows, weights, x, sums = (torch.full_like(t, 7.0) for t in (*want.values(), gx))
+    result, eager = torch.empty_like(a.x), torch.empty_like(a.x)
+
+    def combine(out, space):
+        M.combine(a.cfg, ya, a.out["assist_info"], a.out["ep_recv_count"], a.ids_d, a.weights_d, a.mask, a.x, out, None, space)
+
+    combine(eager, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    before = M.launch_count()
+    with torch.cuda.graph(graph):
+        M.dispatch(a.cfg, a.x, a.ids_d, a.mask, a.weights_d, a.out["expand_x"], None, a.out["assist_info"], a.out["ep_recv_count"],
+                   a.out["expand_scales"], None, ws)
+        combine(result, ws)
+        M.combine_backward(a.cfg, g, ya, *a.route(), a.weights_d, a.mask, a.x, rows, weights, x, ws)
+        M.dispatch_backward(a.cfg, ya, *a.route(), a.mask, sums, g, ws=ws)
+    assert M.launch_count() - before == 5  # routing and scatter, then one each
+    for _ in range(2):
+        for t in (rows, weights, x, sums, result):
+            t.fill_(7.0)
+        again = b.dispatch_backward(yb, ws=ws)[0]  # rebuilds the map for its own rows
+        graph.replay()
+        torch.cuda.synchronize()
+        assert M.get_device_status(ws) == 0 and torch.equal(again, want_b)
+        assert torch.equal(rows, want["rows"]) and torch.equal(weights, want["weights"]) and torch.equal(x, want["x"])
+        assert torch.equal(sums, gx) and torch.equal(result, eager)
+    a.check_combine(dict(rows=rows, weights=weights, x=x), g64, ya64)
+    a.check_dispatch((sums, None), ya64, g64)
