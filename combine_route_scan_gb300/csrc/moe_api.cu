@@ -761,10 +761,11 @@ moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out,
   p.grad_rows = grad_expert_out;
   p.grad_scales = grad_scales;
   p.grad_x = grad_x;
-  // Looking for the rows costs less than rebuilding the map where an expert has tens of rows from a rank (with and
-  // without: 16 tokens of hidden 256 5.3 and 7.1 us, 512 of 2048 10.6 and 12.1, 4096 of 7168 158 and 161), and less than
-  // 3 us where it has a thousand, in dispatch's order. Rows in another order are looked for through all of them: 4096
-  // tokens of hidden 2048, top-2 of 4 experts on 2 ranks, take 32 us with a map of theirs, 35 without, 65 permuted.
+  // Always by looking for the rows: for few tokens or long rows that costs less than rebuilding the map (16 tokens of hidden
+  // 256 5.3 and 7.1 us, 512 of 2048 10.6 and 12.1, 4096 of 7168 158 and 161). For many tokens of short rows it costs far
+  // more: top-8 of 128 experts on 8 ranks, 16384 tokens of hidden 64 134 us, 256 136, 1024 150, 2048 195, where a map of
+  // theirs leaves 23, 29, 94 and 185, and rebuilding one takes some 4. Rows that are not in dispatch's order are looked for
+  // one by one: 4096 tokens of hidden 2048, top-2 of 4 experts on 2 ranks, 65 us, in order 35, with a map 32.
   return run_grad(cfg, p, true, ws, static_cast<cudaStream_t>(stream), launch_combine_grad);
 }
 

@@ -244,10 +244,11 @@ moe_status_t moe_expert_product_int8(const moe_config_t* cfg, const int8_t* x, c
  *   assist_info, ep_recv_count, expert_ids, expert_scales, active_mask: as given to moe_combine
  *   grad_expert_out [W][A][h], grad_scales [W][bs][K] fp32, grad_x [W][bs][h]: any of them, but not all,
  *               may be NULL; none may overlap an input
- *   ws          a workspace of cfg, best the dispatch's, whose pick -> row map is then used; otherwise each pick's row is
- *               looked for among those that ep_recv_count gives to its expert and source rank (one by one where they are not
- *               in dispatch's order), or (moe_dispatch_backward of many short rows) the map rebuilt as moe_combine does. A pick that no row names, a count above the capacity and a bad id are
- *               reported as there
+ *   ws          a workspace of cfg, best the dispatch's, whose pick -> row map is then used (for many tokens of short rows
+ *               several times as fast); otherwise each pick's row is looked for among those that ep_recv_count gives to its
+ *               expert and source rank (one by one where they are not in dispatch's order), or (moe_dispatch_backward of
+ *               many short rows) the map rebuilt as moe_combine does. A pick that no row names, a count above the capacity
+ *               and a bad id are reported as there
  * Row arrays are 16-byte aligned. grad_scales is what moe_route_backward takes. */
 moe_status_t moe_combine_backward(const moe_config_t* cfg, const void* grad_out, const void* expert_out,
                                   const int32_t* assist_info, const int32_t* ep_recv_count, const int32_t* expert_ids,
